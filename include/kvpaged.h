@@ -1,7 +1,8 @@
 /*
  * kvpaged.h -- C ABI of the GB300 paged KV-cache hot path (libkvpaged.so).
  *
- * Thirteen calls, each one kernel launch on the caller's stream:
+ * Eighteen calls, each one kernel launch on the caller's stream (the attention
+ * over the 4-bit cache adds a second one that joins the parts of its split):
  *   kv_slot_mapping_paged    token -> cache slot through a block table
  *   kv_slot_mapping_paged_cp the same, for one rank of context parallelism
  *   kv_slot_mapping_range    token -> cache slot through contiguous ranges
@@ -15,6 +16,11 @@
  *   kv_cache_gather_range    the gather, with blocks found from ranges
  *   kv_copy_blocks           copy-on-write copy of whole blocks
  *   kv_copy_blocks_bulk      the same copies, moved by bulk (TMA) copies
+ *   kv_qk_norm_rope_write    per-head norm and rotation of q and k, K/V write
+ *   kv_attention_prompt      causal attention of packed sequences
+ *   kv_cache_write_q4        quantise new K/V rows into the 4-bit paged caches
+ *   kv_cache_gather_q4       gather spans of the 4-bit caches as bf16 rows
+ *   kv_attention_q4          one query token per request over the 4-bit caches
  *
  * Sources (page title, section):
  *   [BT]  "Blocktabelle" (vLLM v0.25.1 walkthrough)
@@ -463,6 +469,168 @@ int kv_copy_blocks_bulk(void* k_cache, void* v_cache, int32_t num_layers, int64_
                         int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
                         const int32_t* src_blocks, const int32_t* dst_blocks,
                         int32_t num_pairs, int32_t* d_err, kv_stream_t stream);
+
+/*
+ * kv_qk_norm_rope_write -- what a layer does between its projection and its
+ * attention: RMS norm of every query and key head, rotation by the token's
+ * position, and the write of the new K and V rows to their slots.
+ *
+ *   query          bf16 [num_tokens, num_q_heads, head_dim]; key, value bf16
+ *                  [num_tokens, num_kv_heads, head_dim].  The heads of a token
+ *                  are dense; tokens are *_stride elements apart (the three may
+ *                  be slices of one projection's output).
+ *   q_weight, k_weight  bf16 [head_dim], the norms' weights.
+ *   positions      int64 [num_tokens]; cos_sin fp32 [max_position, rotary_dim]:
+ *                  rotary_dim/2 cosines, then as many sines, of a position's angles.
+ *   q_out, k_out   bf16 [num_tokens, num_q_heads / num_kv_heads, head_dim], dense.
+ *                  q_out may be query, and k_out key, where those rows are dense;
+ *                  any other overlap with an input is refused.  k_out may be NULL
+ *                  when there are caches.
+ *   k_cache, v_cache, layer, num_layers, num_blocks, block_size, slot_mapping
+ *                  as kv_cache_write, but only `layer` is written.  Both caches
+ *                  NULL: no write, and value and slot_mapping are not read.
+ *
+ * For a head x: y = x * weight / sqrt(mean(x^2) + eps); then for i <
+ * rotary_dim/2 with (a, b) = (y[i], y[i + rotary_dim/2]), or (y[2i], y[2i+1])
+ * when `interleaved`: a' = a cos_i - b sin_i, b' = b cos_i + a sin_i.  Channels
+ * at or past rotary_dim keep y.  All of it in 32 bits, rounded once.  V rows
+ * are copied bit for bit.
+ * A position outside [0, max_position) sets KV_ERR_BAD_POSITION: the token's
+ * q_out and k_out rows are zero and nothing is cached.  Slots follow
+ * kv_cache_write (PAD skipped; KV_ERR_NULL_WRITE; KV_ERR_BAD_SLOT); the outputs
+ * are written in each of these cases.
+ * Errors: KV_EINVAL for null or misaligned pointers (16 bytes; positions and
+ * slots 8), sizes out of range, a stride below the row, rotary_dim outside
+ * (0, head_dim], an overlap as above; KV_EUNSUPPORTED for head_dim above 256,
+ * head_dim or rotary_dim not a multiple of 8, a stride not a multiple of 8.
+ */
+int kv_qk_norm_rope_write(const void* query, int64_t query_stride, const void* key,
+                          int64_t key_stride, const void* value, int64_t value_stride,
+                          const void* q_weight, const void* k_weight, const int64_t* positions,
+                          const float* cos_sin, int64_t max_position, int32_t rotary_dim,
+                          int32_t interleaved, float eps, int32_t num_tokens,
+                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                          void* q_out, void* k_out, void* k_cache, void* v_cache, int32_t layer,
+                          int32_t num_layers, int64_t num_blocks, int32_t block_size,
+                          const int64_t* slot_mapping, int32_t* d_err, kv_stream_t stream);
+
+/*
+ * kv_attention_prompt -- causal attention of packed sequences with grouped
+ * heads, over packed K/V rows: a prompt's own, or those kv_cache_gather(_q4)
+ * read for a chunk behind earlier tokens.
+ *
+ *   query          bf16 [num_q_tokens, num_q_heads, head_dim]; key, value bf16
+ *                  [num_k_tokens, num_kv_heads, head_dim]; strides as in
+ *                  kv_qk_norm_rope_write.  Query head h reads KV head
+ *                  h / (num_q_heads / num_kv_heads).
+ *   q_start_loc, k_start_loc  int32 [num_reqs + 1]: request r owns query rows
+ *                  [q_start_loc[r], q_start_loc[r+1]) and key rows
+ *                  [k_start_loc[r], k_start_loc[r+1]).
+ *   out            bf16 [num_q_tokens, num_q_heads, head_dim], dense, apart from
+ *                  the inputs.
+ *
+ * With m query and n key rows, query i sees the keys j <= i + n - m:
+ *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j.
+ * A query that sees no key gets zeros.  Keys a query does not see contribute
+ * nothing to it, whatever they hold; a NaN or infinity in a value row that some
+ * query of the same 128-key tile does not see makes the outputs of those that
+ * do see it NaN in that channel.  Query rows of no request are left
+ * as they were.  A request whose rows are out of order or out of range sets
+ * KV_ERR_BAD_QSL and is skipped.  Products and sums are held in 32 bits; the
+ * weights are rounded to bf16 for their product with V.
+ * Errors: KV_EINVAL for null or misaligned pointers, negative sizes, a stride
+ * below the row, num_q_heads not a multiple of num_kv_heads, a scale that is
+ * not positive and finite, out overlapping an input; KV_EUNSUPPORTED for head_dim
+ * above 128 or not a multiple of 8, a stride not a multiple of 8, more than 128
+ * query heads per KV head, num_q_heads > 4096, num_reqs > KV_MAX_GATHER_REQS.
+ */
+int kv_attention_prompt(const void* query, int64_t query_stride, const void* key,
+                        int64_t key_stride, const void* value, int64_t value_stride,
+                        const int32_t* q_start_loc, const int32_t* k_start_loc,
+                        int32_t num_reqs, int32_t num_q_tokens, int32_t num_k_tokens,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                        void* out, int32_t* d_err, kv_stream_t stream);
+
+/*
+ * The 4-bit paged cache.  K and V are separate byte arrays [num_layers,
+ * num_blocks, num_kv_heads, record], a record being block_size *
+ * (head_dim/2 + head_dim/16) bytes: the block's tokens' codes (head_dim/2 bytes
+ * each), then their scales (one bf16 per 32 channels).  With G = head_dim/32,
+ * byte 2 G g + 2 j + b (g < 8, j < G, b < 2) of a token's codes holds channel
+ * 32 j + 4 g + 2 b in its low four bits and the next channel in its high ones;
+ * a code c stands for (c - 8) * scale of its group j of 32 channels.
+ * head_dim is 64 or 128 and block_size a multiple of 8 (else KV_EUNSUPPORTED;
+ * also above 4096 KV heads).  Whole blocks are copied by kv_copy_blocks with
+ * block_size = num_kv_heads, num_kv_heads = 1 and head_dim = record / 2.
+ *
+ * kv_cache_write_q4 -- kv_cache_write into `layer` of the 4-bit caches.
+ *
+ *   key, value    bf16 [num_tokens, num_kv_heads, head_dim], strides as in
+ *                 kv_qk_norm_rope_write.
+ *   slot_mapping  int64 [num_tokens], rules and error bits of kv_cache_write.
+ *
+ * Per group of 32 channels x: scale = bf16(max|x| / 7), code = round(x / scale)
+ * + 8, nearest with ties to even.  A scale below 2^-126 makes the group zeros; a
+ * group with a NaN or an infinity gets a NaN scale and reads as NaN.  Two tokens
+ * with the same slot race: the row is then undefined.
+ */
+int kv_cache_write_q4(const void* key, int64_t key_stride, const void* value,
+                      int64_t value_stride, void* k_cache, void* v_cache,
+                      const int64_t* slot_mapping, int32_t num_tokens, int32_t layer,
+                      int32_t num_layers, int64_t num_blocks, int32_t block_size,
+                      int32_t num_kv_heads, int32_t head_dim, int32_t* d_err,
+                      kv_stream_t stream);
+
+/*
+ * kv_cache_gather_q4 -- kv_cache_gather from the 4-bit caches: bf16 rows
+ * [out_rows, num_kv_heads, head_dim] of the values the codes stand for (rounded
+ * to bf16).  Packing, spans, zero rows, out_rows and error bits are those of
+ * kv_cache_gather.
+ */
+int kv_cache_gather_q4(const void* k_cache, const void* v_cache, int32_t layer,
+                       int32_t num_layers, int64_t num_blocks, int32_t block_size,
+                       int32_t num_kv_heads, int32_t head_dim, const int32_t* block_table,
+                       int32_t table_stride, const int32_t* gather_start,
+                       const int32_t* gather_end, int32_t num_reqs, void* k_out, void* v_out,
+                       int64_t out_rows, int32_t* d_err, kv_stream_t stream);
+
+/*
+ * kv_attention_q4 -- attention of one query token per request over the 4-bit
+ * caches (a decode step).
+ *
+ *   query          bf16 [num_reqs, num_q_heads, head_dim], tokens query_stride
+ *                  elements apart; query head h reads KV head
+ *                  h / (num_q_heads / num_kv_heads).
+ *   block_table    int32 [num_reqs, table_stride].
+ *   span_start, span_end  int32 [num_reqs]: request r attends its positions
+ *                  [start, end) (a sliding window starts late).
+ *   out            bf16 [num_reqs, num_q_heads, head_dim], dense, apart from query.
+ *   workspace      device memory, 16-byte aligned, of at least
+ *                  kv_attention_q4_workspace() bytes on the same device; it
+ *                  holds no state between calls, and two calls that may run at
+ *                  the same time need one each.
+ *
+ *   out = sum_p softmax_p(scale * q . k_p) v_p
+ * over the positions whose table entry is a block of the pool.  Null entries are
+ * left out; entries outside [0, num_blocks) are left out with KV_ERR_BAD_BLOCK,
+ * positions past the table row with KV_ERR_BAD_POSITION.  A request with no
+ * position left, or with start < 0 or end < start (KV_ERR_BAD_POSITION), gets
+ * zeros.
+ * Errors: as kv_attention_prompt and the 4-bit cache; KV_EINVAL for a workspace
+ * that is missing, misaligned or too small.
+ */
+int kv_attention_q4(const void* query, int64_t query_stride, const void* k_cache,
+                    const void* v_cache, int32_t layer, int32_t num_layers, int64_t num_blocks,
+                    int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                    int32_t head_dim, const int32_t* block_table, int32_t table_stride,
+                    const int32_t* span_start, const int32_t* span_end, int32_t num_reqs,
+                    float scale, void* out, void* workspace, int64_t workspace_bytes,
+                    int32_t* d_err, kv_stream_t stream);
+
+/* Workspace bytes of a kv_attention_q4 call on the current device (0 for none), or
+ * KV_EINVAL for sizes out of range. */
+int64_t kv_attention_q4_workspace(int32_t num_reqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim);
 
 /*
  * kv_diag_bounded_wait -- self-test of the bounded wait the bulk-copy gather

@@ -34,6 +34,7 @@ MAX_TOKENS = 2147418112  # largest max_num_tokens of one slot-mapping call (2^31
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 SIGNATURES = {
     "kv_slot_mapping_paged": ([_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I64, _P, _P, _P],
                               ctypes.c_int),
@@ -58,6 +59,18 @@ SIGNATURES = {
     "kv_copy_blocks": ([_P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _P], ctypes.c_int),
     "kv_copy_blocks_bulk": ([_P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _P],
                             ctypes.c_int),
+    "kv_qk_norm_rope_write": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I32, _I32, _F32,
+                               _I32, _I32, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _I64, _I32, _P,
+                               _P, _P], ctypes.c_int),
+    "kv_attention_prompt": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32,
+                             _I32, _F32, _P, _P, _P], ctypes.c_int),
+    "kv_cache_write_q4": ([_P, _I64, _P, _I64, _P, _P, _P, _I32, _I32, _I32, _I64, _I32, _I32, _I32,
+                           _P, _P], ctypes.c_int),
+    "kv_cache_gather_q4": ([_P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _P, _I32, _P, _P, _I32, _P,
+                            _P, _I64, _P, _P], ctypes.c_int),
+    "kv_attention_q4_workspace": ([_I32, _I32, _I32, _I32], ctypes.c_int64),
+    "kv_attention_q4": ([_P, _I64, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _P, _I32, _P,
+                         _P, _I32, _F32, _P, _P, _I64, _P, _P], ctypes.c_int),
     "kv_diag_bounded_wait": ([_I32, _P, _P], ctypes.c_int),
     "kv_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "kv_abi_version": ([], ctypes.c_int),

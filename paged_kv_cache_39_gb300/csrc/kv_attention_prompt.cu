@@ -1,78 +1,458 @@
 // kv_attention_prompt.cu -- causal attention of packed sequences with grouped
-// heads.
+// heads, on the matrix unit.
 //
 // Mathematics.  Request r holds query rows i < m and key rows j < n; row i sees
-// the keys j <= i + n - m (the last query sees every key):
-//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - max_j)
-// with a running maximum and sum over one pass of the keys.
+// the keys j < seen_i = i + n - m + 1:
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(c q_i . k_j - ref_i),
+// c = scale * log2(e).  One pass over the keys with a running reference ref_i:
+// it is the row's maximum when it was last raised, and is raised (with the
+// accumulator rescaled) only when a new maximum passes it by more than 8, so
+// that p stays below 2^8 and the rescale almost never runs.  Logits, weights,
+// sums and outputs are held in 32 bits; p is rounded to bf16 for its product
+// with V (the matrix unit takes both operands in one type), at most 2^-8 of a
+// weight; the sum takes p before that rounding.
 //
-// Plain form: one warp per (query row, head), D / 32 channels per lane.
+// GPU shape.  A CTA owns 2 tiles of 128 query rows and one KV head.  A tile's rows
+// are tq = 128 / group tokens x the group's heads, so every head of the group
+// shares the K and V tiles and rows of one tile end at almost the same key
+// whatever the group is.  Roles by warp:
+//   0-3, 4-7  softmax of tile 0 / 1: one row per thread, so no shuffles; also the
+//             rescale and the epilogue of its tile
+//   8         TMA: Q once, then K and V tiles of 128 keys into a ring
+//   9         issues the matrix instructions: S = Q K^T (both operands in shared
+//             memory), O += P V (P from tensor memory, over the S it came from)
+//   10, 11    check V tiles at the causal edge (below)
+// While one tile's softmax runs, the matrix unit works for the other.  Tensor
+// memory: S0 S1 (128 columns each, P in place), O0 O1: all 512 columns, hence one
+// CTA per SM.
+//
+// Hidden keys.  A hidden logit is replaced, so a NaN there is gone, but 0 * NaN in
+// P V is NaN.  So in the tiles where some key is hidden from some row (one or two
+// per CTA), V values that are not finite are set to 0 in shared memory, and the
+// first key that held one is kept per channel: rows that see that key
+// get NaN in the epilogue.  Rows behind the sequence are set to 0 outright.
 #include <cuda_bf16.h>
 
-#include "kv_common.cuh"
+#include "kv_tc.cuh"
 
 namespace kvp {
 namespace {
 
+constexpr int kTile = 128;                 // query rows of a tile, keys of a K/V tile
+constexpr int kThreads = 384;
+constexpr int kScrubThreads = 64;
+constexpr int kEdges = 3;                  // K/V tiles a CTA's rows see in part: 256 tokens span at most 3
+constexpr float kLazy = 8.0f;              // log2 of the most a weight may pass the reference
+// Registers: 384 threads x 168 at launch = 256 x 208 + 128 x 88.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+
 struct PromptArgs {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
-  int64_t q_stride, k_stride, v_stride;
   const int32_t* q_start;
   const int32_t* k_start;
   int32_t num_reqs, nq, nk, q_heads, kv_heads, head_dim;
-  float scale;
+  int32_t group, tq;       // query heads per KV head, tokens per tile
+  int32_t items;           // upper bound of (request, tile pair), the grid's extent per head
+  float scale_log2;
   __nv_bfloat16* out;
   int32_t* err;
 };
 
-__global__ void __launch_bounds__(128) prompt_kernel(PromptArgs a) {
+template <int DP>
+struct Smem {
+  static constexpr int kTileBytes = kTile * DP * 2;
+  static constexpr int kSlots = DP == 128 ? 5 : 8;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = 2 * kTileBytes;
+  static constexpr int kBars = kRing + kSlots * kTileBytes;
+  // an edge tile's slot is not used again (it would have to be kSlots loads later)
+  static_assert(kSlots >= 2 * kEdges - 1, "");
+  // full[slots], empty[slots], edge[3], v_ok[3], q_full, s_full[2], p_full[2], o_full[2], scrubbed,
+  // drain
+  static constexpr int kNumBars = 2 * kSlots + 2 * kEdges + 9;
+  static constexpr int kBad = kBars + kNumBars * 8;         // int[DP]: first key not finite
+  static constexpr int kMisc = kBad + DP * 4;
+  static constexpr int kBytes = kMisc + 64 + 1024;          // + alignment of the base
+};
+
+struct Work {
+  int32_t q0, k0, m, n;  // the request's first rows and lengths
+  int32_t t0;            // first token of the pair of tiles
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+              const __grid_constant__ CUtensorMap v_map, PromptArgs a) {
+  using L = Smem<DP>;
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* full = bars;
+  uint64_t* empty = full + L::kSlots;
+  uint64_t* edge = empty + L::kSlots;
+  uint64_t* v_ok = edge + kEdges;
+  uint64_t* q_full = v_ok + kEdges;
+  uint64_t* s_full = q_full + 1;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* scrubbed = o_full + 2;
+  uint64_t* drain = scrubbed + 1;
+  int* bad = reinterpret_cast<int*>(smem + L::kBad);
+  int* misc = reinterpret_cast<int*>(smem + L::kMisc);
+  uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(misc);
+  volatile int* abort = misc + 1;
+  int* any_bad = misc + 2;
+  Work* s_work = reinterpret_cast<Work*>(misc + 4);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kEdges; ++i) {
+      mbar_init(&edge[i], 1);
+      mbar_init(&v_ok[i], kScrubThreads);
+    }
+    mbar_init(q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kTile);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(scrubbed, kScrubThreads);
+    mbar_init(drain, 1);
+    mbar_fence_init();
+    *abort = 0;
+    *any_bad = 0;
+    s_work->m = 0;
+  }
+  if (tid < DP) bad[tid] = INT32_MAX;
+  if (warp == 9) tmem_alloc(tmem_ptr, 512);
   pdl_allow_next();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+
+  // Which pair of tiles is this?  Every thread counts the pairs of its share of
+  // the requests, a block-wide scan places them, the thread that owns
+  // pair `want` describes it.
+  const int head = blockIdx.x / a.items, want = blockIdx.x - head * a.items;
   uint32_t err = 0;
-  for (int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.num_reqs;
-       r += (int64_t)gridDim.x * blockDim.x) {
-    const int q0 = a.q_start[r], q1 = a.q_start[r + 1], k0 = a.k_start[r], k1 = a.k_start[r + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk) err |= KV_ERR_BAD_QSL;
-  }
-  report(a.err, err);
-  const int64_t t = w / a.q_heads;
-  const int h = (int)(w - t * a.q_heads);
-  if (t >= a.nq) return;
-  const int r = find_span(a.q_start, a.num_reqs, (int32_t)t);
-  if (r < 0) return;
-  const int q0 = a.q_start[r], q1 = a.q_start[r + 1], k0 = a.k_start[r], k1 = a.k_start[r + 1];
-  if (q0 < 0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk || t >= q1) return;
-  const int64_t seen = (t - q0) + (int64_t)(k1 - k0) - (q1 - q0) + 1;
-  const int D = a.head_dim, hk = h / (a.q_heads / a.kv_heads);
-  float q[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.f;
-  for (int i = 0; i < 4; ++i) {
-    const int c = lane + 32 * i;
-    q[i] = c < D ? __bfloat162float(a.q[t * a.q_stride + (int64_t)h * D + c]) : 0.f;
-  }
-  for (int64_t j = 0; j < seen; ++j) {
-    const __nv_bfloat16* kr = a.k + (k0 + j) * a.k_stride + (int64_t)hk * D;
-    const __nv_bfloat16* vr = a.v + (k0 + j) * a.v_stride + (int64_t)hk * D;
-    float s = 0.f, v[4];
-    for (int i = 0; i < 4; ++i) {
-      const int c = lane + 32 * i;
-      if (c < D) s += q[i] * __bfloat162float(kr[c]);
-      v[i] = c < D ? __bfloat162float(vr[c]) : 0.f;
+  {
+    __shared__ int warp_sum[kThreads / 32];
+    const int pair = 2 * a.tq;
+    const int per = (a.num_reqs + kThreads - 1) / kThreads;
+    const int r_lo = min(a.num_reqs, tid * per), r_hi = min(a.num_reqs, r_lo + per);
+    int count = 0;
+    for (int r = r_lo; r < r_hi; ++r) {
+      const int q0 = a.q_start[r], q1 = a.q_start[r + 1], k0 = a.k_start[r], k1 = a.k_start[r + 1];
+      if (q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk) err |= KV_ERR_BAD_QSL;
+      else count += (int)(((int64_t)(q1 - q0) + pair - 1) / pair);
     }
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-    s *= a.scale;
-    const float mn = fmaxf(m, s), f = m == mn ? 1.f : expf(m - mn), p = expf(s - mn);
-    m = mn;
-    l = l * f + p;
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * f + p * v[i];
+    const int incl = warp_inclusive_scan<int>(count);
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int at = incl - count;
+    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+    if (want >= at && want < at + count) {
+      for (int r = r_lo; r < r_hi; ++r) {
+        const int q0 = a.q_start[r], q1 = a.q_start[r + 1], k0 = a.k_start[r], k1 = a.k_start[r + 1];
+        if (q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk) continue;
+        const int c = (int)(((int64_t)(q1 - q0) + pair - 1) / pair);
+        if (want < at + c) {  // the last tokens first: they have the most keys
+          *s_work = Work{q0, k0, q1 - q0, k1 - k0, (c - 1 - (want - at)) * pair};
+          break;
+        }
+        at += c;
+      }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) report(a.err, err);
   }
-  for (int i = 0; i < 4; ++i) {
-    const int c = lane + 32 * i;
-    if (c < D) a.out[(t * a.q_heads + h) * D + c] = __float2bfloat16_rn(seen > 0 ? o[i] / l : 0.f);
+  const Work w = *s_work;
+  const int ahead = w.n - w.m;                                    // keys before the first query's own
+  const int last = min(w.t0 + 2 * a.tq, w.m) - 1;                 // last token here
+  const int keys = max(0, min(w.n, ahead + last + 1));            // keys the last token sees
+  const int tiles = (keys + kTile - 1) / kTile;
+  const int whole = max(0, ahead + w.t0 + 1) / kTile;             // tiles every row sees whole
+  const bool two = w.t0 + a.tq < w.m;
+  const bool work = w.m > 0 && tiles > 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+
+  if (w.m > 0 && tiles == 0) {  // no query here sees a key
+    const int64_t row = (int64_t)a.group * a.head_dim;
+    const int vecs = (int)(row / 8);
+    for (int64_t i = tid; i < (int64_t)(last + 1 - w.t0) * vecs; i += kThreads) {
+      const int64_t t = w.q0 + w.t0 + i / vecs;
+      reinterpret_cast<uint4*>(a.out + t * a.q_heads * a.head_dim + head * row)[i % vecs] =
+          make_uint4(0, 0, 0, 0);
+    }
   }
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8 && lane == 0 && work) {
+      // -------------------------------------------------------------- TMA
+      tma_prefetch_map(&q_map);
+      tma_prefetch_map(&k_map);
+      tma_prefetch_map(&v_map);
+      const uint32_t q_bytes = (uint32_t)(a.group * a.tq) * 128u * (DP / 64);
+      mbar_arrive_expect_tx(q_full, two ? 2 * q_bytes : q_bytes);
+      for (int t = 0; t < (two ? 2 : 1); ++t)
+        for (int c = 0; c < DP / 64; ++c)
+          tma_load_3d(smem + L::kQ + t * L::kTileBytes + c * (kTile * 128), &q_map, 64 * c,
+                      head * a.group, w.q0 + w.t0 + t * a.tq, q_full);
+      int u = 0;  // K and V tiles alternate in the ring
+      for (; u < 2 * tiles; ++u) {
+        const int slot = u % L::kSlots;
+        if (u >= L::kSlots &&
+            !mbar_wait_role(&empty[slot], ((u / L::kSlots) - 1) & 1, abort))
+          break;
+        const bool is_v = u & 1;
+        uint64_t* bar = is_v && (u >> 1) >= whole ? &edge[(u >> 1) - whole] : &full[slot];
+        mbar_arrive_expect_tx(bar, L::kTileBytes);
+        for (int c = 0; c < DP / 64; ++c)
+          tma_load_3d(smem + L::kRing + slot * L::kTileBytes + c * (kTile * 128),
+                      is_v ? &v_map : &k_map, 64 * c, head, w.k0 + (u >> 1) * kTile, bar);
+      }
+      if (*abort != 0) {  // bounded wait for the copies still in flight
+        mbar_wait_bounded(q_full, 0);
+        for (int x = max(0, u - L::kSlots); x < u; ++x) {
+          if ((x & 1) && (x >> 1) >= whole) mbar_wait_bounded(&edge[(x >> 1) - whole], 0);
+          else mbar_wait_bounded(&full[x % L::kSlots], (x / L::kSlots) & 1);
+        }
+      }
+    } else if (warp == 9 && lane == 0 && work) {
+      // -------------------------------------------------------------- matrix instructions
+      constexpr uint32_t s_desc = mma_desc(128, kTile, false), o_desc = mma_desc(128, DP, true);
+      const uint32_t q_at = smem_addr(smem + L::kQ), ring = smem_addr(smem + L::kRing);
+      auto scores = [&](int t, int slot) {
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t off = (k / 4) * (kTile * 128) + (k % 4) * 32;
+          mma_ss(tmem + t * kTile, smem_desc(q_at + t * L::kTileBytes + off, 16),
+                 smem_desc(ring + slot * L::kTileBytes + off, 16), s_desc, k > 0);
+        }
+        mma_commit(&s_full[t]);
+      };
+      auto values = [&](int t, int slot, bool add) {
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts(tmem + 2 * kTile + t * DP, tmem + t * kTile + k * 8,
+                 smem_desc(ring + slot * L::kTileBytes + k * 2048, kTile * 128), o_desc, add || k > 0);
+      };
+      const int nt = two ? 2 : 1;
+      bool ok = mbar_wait_role(q_full, 0, abort) && mbar_wait_role(&full[0], 0, abort);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < nt; ++t) scores(t, 0);
+        mma_commit(&empty[0]);
+      }
+      for (int j = 0; ok && j < tiles; ++j) {
+        const int uv = 2 * j + 1, uk = 2 * j + 2;
+        const int sv = uv % L::kSlots, sk = uk % L::kSlots;
+        const bool more = j + 1 < tiles;
+        // at the causal edge V is waited for through the warps that check it
+        ok = j < whole ? mbar_wait_role(&full[sv], (uv / L::kSlots) & 1, abort)
+                       : mbar_wait_role(&v_ok[j - whole], 0, abort);
+        if (ok && more) ok = mbar_wait_role(&full[sk], (uk / L::kSlots) & 1, abort);
+        for (int t = 0; ok && t < nt; ++t) {
+          ok = mbar_wait_role(&p_full[t], j & 1, abort);
+          if (!ok) break;
+          tc_fence_after();
+          values(t, sv, j > 0);
+          if (more) scores(t, sk);  // in issue order behind the P V that reads what it overwrites
+          else mma_commit(&o_full[t]);
+        }
+        if (!ok) break;
+        mma_commit(&empty[sv]);
+        if (more) mma_commit(&empty[sk]);
+      }
+      if (!ok) {  // bounded wait for the matrix instructions in flight
+        mma_commit(drain);
+        mbar_wait_bounded(drain, 0);
+      }
+    } else if (warp >= 10 && work) {
+      // -------------------------------------------------------------- V at the causal edge
+      const int st = tid - 10 * 32;
+      for (int j = whole; j < tiles; ++j) {
+        const int slot = (2 * j + 1) % L::kSlots;
+        if (!mbar_wait_role(&edge[j - whole], 0, abort)) break;
+        unsigned char* tile = smem + L::kRing + slot * L::kTileBytes;
+        for (int r = st; r < kTile; r += kScrubThreads) {
+          const int key = j * kTile + r;
+          for (int i = 0; i < DP / 8; ++i) {
+            const int c = (i / 8) * 8 + ((i + r) & 7);  // 16-byte chunk, banks spread by row
+            uint4* p = reinterpret_cast<uint4*>(tile + (c / 8) * (kTile * 128) + r * 128 +
+                                                ((c & 7) ^ (r & 7)) * 16);
+            if (key >= w.n) {
+              *p = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 x = *p;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&x);
+            bool hit = false;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if ((e[q] & 0x7f80u) == 0x7f80u) {
+                atomicMin(&bad[c * 8 + 2 * q], key);
+                e[q] &= 0xffff0000u;
+                hit = true;
+              }
+              if ((e[q] & 0x7f800000u) == 0x7f800000u) {
+                atomicMin(&bad[c * 8 + 2 * q + 1], key);
+                e[q] &= 0xffffu;
+                hit = true;
+              }
+            }
+            if (hit) {
+              *p = x;
+              *any_bad = 1;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&v_ok[j - whole]);
+      }
+      mbar_arrive(scrubbed);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int t = warp >> 2;  // the tile
+    if (work && (t == 0 || two)) {
+      // -------------------------------------------------------------- softmax
+      const int row = tid & 127;
+      const int tok = row / a.group, g = row - tok * a.group;
+      const int i = w.t0 + t * a.tq + tok;  // token in the request
+      const bool mine = tok < a.tq && i < w.m;
+      const int seen = min(w.n, ahead + i + 1);
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes, in bits 16..
+      const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 2 * kTile + t * DP;
+      const float c = a.scale_log2;
+      float ref = 0.f, sum = 0.f;
+      bool ok = true;
+      for (int j = 0; j < tiles; ++j) {
+        ok = mbar_wait_role(&s_full[t], j & 1, abort);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[kTile];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, s + 32 * b);
+        tmem_wait_ld();
+        if (j >= whole) {
+          const int left = seen - j * kTile;  // keys of this tile the row sees
+#pragma unroll
+          for (int x = 0; x < kTile; ++x)
+            if (x >= left) s[x] = 0xff800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < kTile; x += 4)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[x + y]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        if (j == 0) {
+          ref = top > -INFINITY ? top : 0.f;
+        } else {
+          const bool raise = top > ref + kLazy;
+          if (__any_sync(kFull, raise)) {
+            // P V of the earlier tiles is done: S of this tile was issued behind it
+            const float f = raise ? ex2(ref - top) : 1.f;
+            if (raise) ref = top;
+            sum *= f;
+#pragma unroll 1
+            for (int b = 0; b < DP / 32; ++b) {
+              uint32_t o[32];
+              tmem_ld32(o_at + 32 * b, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st32(o_at + 32 * b, o);
+            }
+          }
+        }
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t p[kTile / 2];
+#pragma unroll
+        for (int x = 0; x < kTile; x += 2) {
+          const float e0 = ex2(fmaf(__uint_as_float(s[x]), c, -ref));
+          const float e1 = ex2(fmaf(__uint_as_float(s[x + 1]), c, -ref));
+          part[x & 2] += e0;
+          part[(x & 2) + 1] += e1;
+          p[x / 2] = pack_bf16(e0, e1);
+        }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        tmem_st32(s_at, p);
+        tmem_st32(s_at + 32, p + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[t]);
+      }
+      // -------------------------------------------------------------- epilogue
+      if (ok) ok = __all_sync(kFull, mbar_wait_role(&o_full[t], 0, abort));
+      if (ok) ok = __all_sync(kFull, mbar_wait_role(scrubbed, 0, abort));
+      if (ok) {
+        tc_fence_after();
+        const bool check = *any_bad != 0;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: zeros
+        __nv_bfloat16* out = a.out + ((int64_t)(w.q0 + i) * a.q_heads + head * a.group + g) * a.head_dim;
+#pragma unroll 1
+        for (int b = 0; b < DP / 32; ++b) {
+          uint32_t o[32];
+          tmem_ld32(o_at + 32 * b, o);
+          tmem_wait_ld();
+          if (check) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (seen > bad[32 * b + x]) o[x] = 0x7fc00000u;
+          }
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) {
+            uint4 y;
+            y.x = pack_bf16(__uint_as_float(o[x]) * inv, __uint_as_float(o[x + 1]) * inv);
+            y.y = pack_bf16(__uint_as_float(o[x + 2]) * inv, __uint_as_float(o[x + 3]) * inv);
+            y.z = pack_bf16(__uint_as_float(o[x + 4]) * inv, __uint_as_float(o[x + 5]) * inv);
+            y.w = pack_bf16(__uint_as_float(o[x + 6]) * inv, __uint_as_float(o[x + 7]) * inv);
+            if (mine && 32 * b + x < a.head_dim)
+              *reinterpret_cast<uint4*>(out + 32 * b + x) = y;
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) {
+    tmem_dealloc(tmem, 512);
+    if (lane == 0 && *abort != 0 && a.err != nullptr) atomicOr(a.err, KV_ERR_TIMEOUT);
+  }
+}
+
+template <int DP>
+int launch(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+           cudaStream_t stream) {
+  auto kernel = prompt_kernel<DP>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Smem<DP>::kBytes) != cudaSuccess)
+    return KV_ECUDA;
+  const int64_t ctas = (int64_t)a.items * a.kv_heads;
+  if (ctas > INT32_MAX) return KV_EUNSUPPORTED;
+  return launch_pdl(kernel, (unsigned)ctas, kThreads, Smem<DP>::kBytes, stream, q, k, v, a);
 }
 
 }  // namespace
@@ -109,11 +489,22 @@ extern "C" int kv_attention_prompt(const void* query, int64_t query_stride, cons
       (num_k_tokens > 0 && (overlap(out, out_bytes, key, (n1 * key_stride + k_row) * 2) ||
                             overlap(out, out_bytes, value, (n1 * value_stride + k_row) * 2))))
     return KV_EINVAL;
-  PromptArgs a{static_cast<const __nv_bfloat16*>(query), static_cast<const __nv_bfloat16*>(key),
-               static_cast<const __nv_bfloat16*>(value), query_stride, key_stride, value_stride,
-               q_start_loc, k_start_loc, num_reqs, num_q_tokens, num_k_tokens, num_q_heads,
-               num_kv_heads, head_dim, scale, static_cast<__nv_bfloat16*>(out), d_err};
-  const int64_t ctas = ((int64_t)num_q_tokens * num_q_heads + 3) / 4;
-  if (ctas > INT32_MAX) return KV_EUNSUPPORTED;
-  return launch_pdl(prompt_kernel, (unsigned)ctas, 128, 0, stream, a);
+  const int group = num_q_heads / num_kv_heads, tq = kTile / group;
+  CUtensorMap q_map, k_map, v_map;
+  // no key at all: nothing is loaded through the K and V maps
+  const bool keys = num_k_tokens > 0;
+  if (!rows_map(&q_map, query, query_stride, num_q_tokens, num_q_heads, head_dim, group, tq) ||
+      !rows_map(&k_map, keys ? key : query, keys ? key_stride : query_stride,
+                keys ? num_k_tokens : num_q_tokens, keys ? num_kv_heads : num_q_heads, head_dim, 1,
+                kTile) ||
+      !rows_map(&v_map, keys ? value : query, keys ? value_stride : query_stride,
+                keys ? num_k_tokens : num_q_tokens, keys ? num_kv_heads : num_q_heads, head_dim, 1,
+                kTile))
+    return KV_ECUDA;
+  PromptArgs a{q_start_loc, k_start_loc, num_reqs, num_q_tokens, num_k_tokens, num_q_heads,
+               num_kv_heads, head_dim, group, tq,
+               (int32_t)((int64_t)num_q_tokens / (2 * tq) + num_reqs),
+               scale * 1.44269504088896340736f, static_cast<__nv_bfloat16*>(out), d_err};
+  return head_dim <= 64 ? launch<64>(a, q_map, k_map, v_map, stream)
+                        : launch<128>(a, q_map, k_map, v_map, stream);
 }

@@ -1,16 +1,48 @@
 // kv_attention_q4.cu -- attention of one query token per request over the 4-bit
 // paged cache.
 //
-// Mathematics.  Request r attends the positions [start, end) that its block
-// table maps to a block of the pool; with k, v the values the 4-bit rows stand
-// for (kv_q4.cuh)
-//   o = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale q . k_p - max_p).
+// Mathematics.  Request r attends the positions [start, end) that its block table
+// maps to a block of the pool.  With codes u, group scales a (of K) and b (of V)
+//   s_p = scale sum_j a_pj (sum_{c in j} q_c (u_pc - 8)),   w_p = 2^(s_p - ref)
+//   o_c = sum_p (w_p b_pj) (u_pc - 8) / sum_p w_p           (c in group j)
+// so the group scales never touch the codes: K's multiply the 32-bit partial sum of
+// their group, V's the weight.  u - 8 is exact in fp16, q is made exact by a power of
+// two per head (2^-24 of its largest channel is lost at most), w b is rounded to fp16
+// (2^-11 of a weight: fewer bits than that would double the output's own rounding
+// error).  ref is a running reference: the largest w b of a query was 1 when it was last
+// raised, and it is raised when one passes 2^8, so w b stays inside fp16 whatever the
+// scales are (between 2^-100 and 2^100); sums are held in 32 bits.
 //
-// Plain form: one warp per (request, query head), D / 32 channels per lane.
+// GPU shape.  The bytes of the cache bound this: 16 query rows at most read each of
+// them, far under a matrix unit tile of 128 rows, so the products go through the warp's
+// own m16n8k16 instruction with tokens (of K) or channels (of V) as its 16 rows and the
+// group's query heads as its 8 columns.  Every warp is a worker of its own:
+// all positions of all (request, KV head) are cut into units of 32 tokens, and worker i
+// takes the units [i C, (i+1) C) whatever requests they belong to, so every worker reads
+// the same number of bytes however long the contexts are.  Its units come through a ring
+// of kStages in shared memory, filled with cp.async by table lookups made one unit ahead,
+// and nothing but the warp itself waits for them.  A worker
+// whose range ends inside a (request, head) leaves its sums in the workspace; a second
+// kernel joins those.
+//
+// Layout of a unit in shared memory.  Row rho of the K product's 16 is token pi(rho) =
+// (rho >> 1) + 4 (rho & 1): its transpose then gives lane t the tokens t, t + 4, t + 8,
+// t + 12 it holds of V.  K rows are stored in the order of rho and V's 16-byte pieces
+// are xor-ed with the token, which makes every shared-memory read free of bank conflicts.
+#include <cuda_fp16.h>
+
 #include "kv_q4.cuh"
 
 namespace kvp {
 namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 3;
+constexpr int kUnit = 32;                 // tokens of a unit
+constexpr float kRefStart = -1e30f;       // below every logit, and finite
+constexpr float kLimit = 256.0f;          // a weight times its scale above this raises the reference
+constexpr float kUnitMin = 7.888609e-31f, kUnitMax = 1.2676506e30f;  // 2^-100, 2^100
 
 struct AttnArgs {
   const __nv_bfloat16* q;
@@ -18,62 +50,563 @@ struct AttnArgs {
   const uint8_t* k_cache;
   const uint8_t* v_cache;
   Q4Layout at;
+  BlockDiv div;
   const int32_t* table;
   int32_t stride;
   const int32_t* start;
   const int32_t* end;
-  int32_t num_reqs, q_heads;
-  float scale;
+  int32_t num_reqs, q_heads, group;
+  int32_t passes;   // groups of 8 NT query heads per KV head
+  int32_t workers;
+  float scale_log2;
   __nv_bfloat16* out;
+  int64_t* offsets;  // [num_reqs + 1] units before each request (written by CTA 0)
+  float* parts;      // [workers][2][8 NT][D + 2]: sums, reference, weight sum
   int32_t* err;
 };
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four pairs of codes (nibble n of the low and of the high half of x) as fp16 pairs u - 8.
+// 0x6400 | u is 1024 + u, and 0x6400 | u << 4 is 1024 + 16 u: one fma makes either exact.
+__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&f)[4]) {
+  const __half2 one = __float2half2_rn(1.f), sub = __float2half2_rn(-1032.f);
+  const __half2 sixteenth = __float2half2_rn(0.0625f), sub16 = __float2half2_rn(-72.f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t y = h ? x >> 8 : x;
+    const uint32_t lo = (y & 0x000f000fu) | 0x64006400u, hi = (y & 0x00f000f0u) | 0x64006400u;
+    const __half2 a = __hfma2(*reinterpret_cast<const __half2*>(&lo), one, sub);
+    const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), sixteenth, sub16);
+    f[2 * h] = *reinterpret_cast<const uint32_t*>(&a);
+    f[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+// src_bytes 0 writes zeros and reads nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
+               "r"(src_bytes)
+               : "memory");
+}
+
 template <int G>
-__global__ void __launch_bounds__(32) attention_q4_kernel(AttnArgs a) {
+struct Stage {
+  static constexpr int kCodes = kUnit * 16 * G;  // bytes of K (or V) codes
+  static constexpr int kScales = kUnit * 2 * G;
+  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+};
+
+// Units of a request's span, and 0 for an invalid one.  Positions past the table row are
+// cut off here, so the work is bounded by the table whatever the span says.
+__device__ __forceinline__ int span_units(const AttnArgs& a, int r, uint32_t& err) {
+  const int64_t row = (int64_t)a.stride * a.at.block_size;
+  const int64_t s0 = a.start[r], s1 = a.end[r];
+  if (s0 < 0 || s1 < s0 || (s1 > row && s1 > s0)) err |= KV_ERR_BAD_POSITION;
+  const int64_t n = s0 < 0 ? 0 : min(s1, row) - s0;
+  return n <= 0 ? 0 : (int)((n + kUnit - 1) / kUnit);
+}
+
+// Where a worker is: unit `unit` of `units` of segment `seg` of request r.
+struct Cursor {
+  int r, seg, unit, units;
+  __device__ __forceinline__ void next(const AttnArgs& a, int segs) {
+    if (++unit < units) return;
+    unit = 0;
+    if (++seg < segs) return;
+    seg = 0;
+    uint32_t ignore = 0;
+    do {
+      ++r;
+      units = r < a.num_reqs ? span_units(a, r, ignore) : 1;
+    } while (units == 0);
+  }
+};
+
+template <int G, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel(AttnArgs a) {
+  constexpr int D = 32 * G, NQ = 8 * NT;
+  using S = Stage<G>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_before[kThreads];  // units before each thread's share of the requests
+  __shared__ int64_t s_warp[kWarps];
+  __shared__ int64_t s_total;
+  __shared__ uint32_t s_valid[kWarps][kStages];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int H = a.at.kv_heads, segs = H * a.passes;
   pdl_allow_next();
   pdl_wait();
-  constexpr int D = 32 * G;
-  const int lane = threadIdx.x;
-  const int r = blockIdx.x / a.q_heads, h = blockIdx.x % a.q_heads;
-  const int hk = h / (a.q_heads / a.at.kv_heads);
-  const int T = a.at.block_size;
-  const int64_t s0 = a.start[r], s1 = a.end[r];
+
+  // ---- every CTA: where the requests' units begin
+  const int per = (a.num_reqs + kThreads - 1) / kThreads;
   uint32_t err = 0;
-  const bool ok = s0 >= 0 && s1 >= s0;
-  if (!ok) err |= KV_ERR_BAD_POSITION;
-  float q[G], o[G], m = -INFINITY, l = 0.f;
-  const int g = lane >> 2;
-  for (int j = 0; j < G; ++j) {
-    q[j] = __bfloat162float(a.q[r * a.q_stride + (int64_t)h * D + 32 * j + lane]);
-    o[j] = 0.f;
+  {
+    const int r_lo = min(a.num_reqs, tid * per), r_hi = min(a.num_reqs, r_lo + per);
+    uint32_t span_err = 0;
+    int64_t mine = 0;
+    for (int r = r_lo; r < r_hi; ++r) mine += (int64_t)span_units(a, r, span_err) * segs;
+    if (blockIdx.x == 0) err |= span_err;
+    const int64_t incl = warp_inclusive_scan<int64_t>(mine);
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    s_before[tid] = before;
+    if (tid == kThreads - 1) s_total = before + mine;
+    if (blockIdx.x == 0) {
+      uint32_t ignore = 0;
+      int64_t at = before;
+      for (int r = r_lo; r < r_hi; ++r) {
+        a.offsets[r] = at;
+        at += (int64_t)span_units(a, r, ignore) * segs;
+      }
+      if (tid == kThreads - 1) a.offsets[a.num_reqs] = at;
+    }
+    __syncthreads();
   }
-  for (int64_t p = s0; ok && p < s1; ++p) {
-    const int64_t lb = p / T;
-    if (lb >= a.stride) { err |= KV_ERR_BAD_POSITION; break; }
-    const int64_t b = a.table[(int64_t)r * a.stride + lb];
-    if (b == kNull) continue;
-    if (b < 0 || b >= a.at.num_blocks) { err |= KV_ERR_BAD_BLOCK; continue; }
-    const int64_t rec = a.at.record(b, hk);
-    const int off = (int)(p - lb * T);
-    auto val = [&](const uint8_t* c, int j) {
-      const uint32_t byte = c[rec + a.at.codes(off) + 2 * G * g + 2 * j + ((lane >> 1) & 1)];
-      const uint16_t sb = reinterpret_cast<const uint16_t*>(c + rec + a.at.scales(off))[j];
-      return (float)((int)((lane & 1) ? byte >> 4 : byte & 15u) - 8) *
-             __uint_as_float((uint32_t)sb << 16);
-    };
-    float s = 0.f;
-    for (int j = 0; j < G; ++j) s += q[j] * val(a.k_cache, j);
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-    s *= a.scale;
-    const float mn = fmaxf(m, s), f = m == mn ? 1.f : expf(m - mn), w = expf(s - mn);
-    m = mn;
-    l = l * f + w;
-    for (int j = 0; j < G; ++j) o[j] = o[j] * f + w * val(a.v_cache, j);
+  const int worker = blockIdx.x * kWarps + warp;
+  // requests without a position: zeros
+  for (int r = worker; r < a.num_reqs; r += a.workers) {
+    uint32_t ignore = 0;
+    if (span_units(a, r, ignore) > 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)r * a.q_heads * D);
+    for (int i = lane; i < a.q_heads * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
   }
-  for (int j = 0; j < G; ++j)
-    a.out[((int64_t)r * a.q_heads + h) * D + 32 * j + lane] =
-        __float2bfloat16_rn(l > 0.f || l != l ? o[j] / l : 0.f);
+  const int64_t total = s_total;
+  const int64_t share = (total + a.workers - 1) / a.workers;
+  const int64_t first = worker * share;
+  if (first >= total) {
+    report(a.err, err);
+    return;
+  }
+  const int64_t count = min(share, total - first);
+
+  // ---- this worker's first unit
+  Cursor load;
+  {
+    int lo = 0, hi = kThreads;  // last thread whose share begins at or before `first`
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_before[mid] <= first) lo = mid; else hi = mid;
+    }
+    int r = lo * per;
+    int64_t at = s_before[lo];
+    uint32_t ignore = 0;
+    int u = span_units(a, r, ignore);
+    while (at + (int64_t)u * segs <= first) {
+      at += (int64_t)u * segs;
+      u = span_units(a, ++r, ignore);
+    }
+    const int64_t rest = first - at;
+    load.r = r;
+    load.units = u;
+    load.seg = (int)(rest / u);
+    load.unit = (int)(rest - (int64_t)load.seg * u);
+  }
+  Cursor cur = load;
+
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_addr(smem) + warp * kStages * S::kBytes;
+  const unsigned char* ring_p = smem + warp * kStages * S::kBytes;
+  const int64_t rec_bytes = a.at.record_bytes();
+  const int T = a.at.block_size;
+
+  // ---- loads: the block of this lane's token of the next unit is looked up one unit ahead
+  int32_t nb = kNull;  // its block, or null
+  int32_t n_off = 0;
+  auto look_up = [&]() {
+    nb = kNull;
+    if (load.r >= a.num_reqs) return;
+    const int64_t p = (int64_t)a.start[load.r] + (int64_t)load.unit * kUnit + lane;
+    if (p >= a.end[load.r]) return;
+    int64_t lb, off;
+    a.div.divmod(p, lb, off);
+    n_off = (int32_t)off;
+    if (lb < a.stride) nb = a.table[(int64_t)load.r * a.stride + lb];
+  };
+  auto issue = [&](int stage) {
+    bool valid = nb != kNull;
+    if (valid && (nb < 0 || nb >= a.at.num_blocks)) {
+      err |= KV_ERR_BAD_BLOCK;
+      valid = false;
+    }
+    const int head = load.seg / a.passes;
+    const int64_t rec = valid ? a.at.record(nb, head) : 0;
+    const int64_t row = rec + (int64_t)n_off * (16 * G);
+    const uint32_t base = ring + stage * S::kBytes;
+    const uint32_t mask = __ballot_sync(kFull, valid);
+    if (lane == 0) s_valid[warp][stage] = mask;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int tok = i * (32 / G) + lane / G, c = lane % G;
+      const int64_t src = __shfl_sync(kFull, row, tok) + 16 * c;
+      const uint32_t bytes = (mask >> tok) & 1u ? 16u : 0u;
+      const int64_t at = bytes ? src : 0;
+      const uint32_t k_row = (tok & 24) + 2 * (tok & 3) + ((tok >> 2) & 1);
+      const uint32_t v_c = G == 4 ? c ^ (2 * ((tok >> 1) & 1)) : c;
+      copy16(base + k_row * (16 * G) + 16 * c, a.k_cache + at, bytes);
+      copy16(base + S::kCodes + tok * (16 * G) + 16 * v_c, a.v_cache + at, bytes);
+    }
+    const int64_t sc = valid ? rec + (int64_t)T * (16 * G) + (int64_t)n_off * (2 * G) : 0;
+    copy_small<2 * G>(base + 2 * S::kCodes + lane * (2 * G), a.k_cache + sc, valid ? 2 * G : 0);
+    copy_small<2 * G>(base + 2 * S::kCodes + S::kScales + lane * (2 * G), a.v_cache + sc,
+                      valid ? 2 * G : 0);
+    load.next(a, segs);
+    look_up();
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+
+  look_up();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (s < count) issue(s);
+    commit();
+  }
+
+  uint32_t qf[NT][G][2][2];  // query fragments
+  float qc[NT][2];           // what a logit of this lane's two columns is multiplied with
+  float o[NT][2 * G][4];     // sums: rows = channels, columns = query heads
+  float ref[NT][2], sum[NT][2];
+  bool fresh = true;
+  int seg_first = 0;  // the unit of the segment this worker started with
+
+  int stage = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();
+    if (i + kStages - 1 < count) issue(stage == 0 ? kStages - 1 : stage - 1);  // the unit before's
+    commit();
+
+    if (fresh) {  // a new (request, head, pass)
+      fresh = false;
+      seg_first = cur.unit;
+      const int head = cur.seg / a.passes, pass = cur.seg - head * a.passes;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int qi = pass * NQ + 8 * n + g;
+        float x[G][8], top = 0.f;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (qi < a.group)
+            v = *reinterpret_cast<const uint4*>(a.q + cur.r * a.q_stride +
+                                                (int64_t)(head * a.group + qi) * D + 32 * j + 8 * t);
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[j][2 * k] = __uint_as_float(e[k] << 16);
+            x[j][2 * k + 1] = __uint_as_float(e[k] & 0xffff0000u);
+            top = fmaxf(top, fmaxf(fabsf(x[j][2 * k]), fabsf(x[j][2 * k + 1])));
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        // 2^-e with e the exponent of the largest channel (1 for rows of zeros or infinities)
+        const int e = (int)(__float_as_uint(top) >> 23) - 127;
+        const bool usual = e > -100 && e < 120;
+        const float down = usual ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.f;
+        const float up = usual ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f;
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              qf[n][j][s][k] = pack_f16(x[j][2 * s + k] * down, x[j][4 + 2 * s + k] * down);
+        // column 2 t + k is the query head of lanes 4 (2 t + k) ..
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          qc[n][k] = __shfl_sync(kFull, up, 4 * (2 * t + k)) * a.scale_log2;
+          ref[n][k] = kRefStart;
+          sum[n][k] = 0.f;
+        }
+#pragma unroll
+        for (int m = 0; m < 2 * G; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[n][m][k] = 0.f;
+      }
+    }
+
+    const unsigned char* base = ring_p + stage * S::kBytes;
+    const uint32_t mask = s_valid[warp][stage];
+    const int tok = (g >> 1) + 4 * (g & 1);  // this lane's token in each 8 rows
+
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // 16 tokens each
+      // ---- logits
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+      uint32_t x[2][G];  // per row: the group's codes of g' = 2 t (low half) and 2 t + 1 (high)
+      float ks[2][G], vs[2][G];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const unsigned char* row = base + (16 * u + 8 * h + g) * (16 * G);
+        if constexpr (G == 4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * t);
+          x[h][0] = __byte_perm(w.x, w.z, 0x5410);
+          x[h][1] = __byte_perm(w.x, w.z, 0x7632);
+          x[h][2] = __byte_perm(w.y, w.w, 0x5410);
+          x[h][3] = __byte_perm(w.y, w.w, 0x7632);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * t);
+          x[h][0] = __byte_perm(w.x, w.y, 0x5410);
+          x[h][1] = __byte_perm(w.x, w.y, 0x7632);
+        }
+        const unsigned char* sc = base + 2 * S::kCodes + (16 * u + 8 * h + tok) * (2 * G);
+#pragma unroll
+        for (int j = 0; j < G; j += 2) {
+          const uint32_t kk = *reinterpret_cast<const uint32_t*>(sc + 2 * j);
+          const uint32_t vv = *reinterpret_cast<const uint32_t*>(sc + S::kScales + 2 * j);
+          ks[h][j] = __uint_as_float(kk << 16);
+          ks[h][j + 1] = __uint_as_float(kk & 0xffff0000u);
+          vs[h][j] = __uint_as_float(vv << 16);
+          vs[h][j + 1] = __uint_as_float(vv & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        uint32_t lo[4], hi[4];
+        codes_f16(x[0][j], lo);
+        codes_f16(x[1][j], hi);
+        const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(acc, a0, qf[n][j][0][0], qf[n][j][0][1]);
+          mma16816(acc, a1, qf[n][j][1][0], qf[n][j][1][1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[n][k] = fmaf(acc[k], ks[k >> 1][j], s[n][k]);
+        }
+      }
+      // ---- weights
+      float unit[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float m = fmaxf(vs[h][0], vs[h][1]);
+        if constexpr (G == 4) m = fmaxf(m, fmaxf(vs[h][2], vs[h][3]));
+        unit[h] = fminf(fmaxf(m, kUnitMin), kUnitMax);
+      }
+      float w[NT][4];
+      float most = 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[n][k] *= qc[n][k & 1];
+          if (mask != kFull && !((mask >> (16 * u + 8 * (k >> 1) + tok)) & 1u)) s[n][k] = -INFINITY;
+          w[n][k] = ex2(s[n][k] - ref[n][k & 1]);
+          most = fmaxf(most, w[n][k] * unit[k >> 1]);
+        }
+      if (__any_sync(kFull, most > kLimit)) {
+        // raise the references to the largest logit + log2(scale) of these tokens
+        const float l0 = log2f(unit[0]), l1 = log2f(unit[1]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float z = fmaxf(s[n][k] + l0, s[n][k + 2] + l1);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) z = fmaxf(z, __shfl_xor_sync(kFull, z, d));
+            const float up = fmaxf(ref[n][k], z), f = ex2(ref[n][k] - up);
+            ref[n][k] = up;
+            sum[n][k] *= f;
+#pragma unroll
+            for (int m = 0; m < 2 * G; ++m) {
+              o[n][m][k] *= f;
+              o[n][m][k + 2] *= f;
+            }
+            w[n][k] = ex2(s[n][k] - up);
+            w[n][k + 2] = ex2(s[n][k + 2] - up);
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        sum[n][0] += w[n][0] + w[n][2];
+        sum[n][1] += w[n][1] + w[n][3];
+      }
+      // ---- values
+      uint32_t vw[4][G / 2];  // tokens t, t + 4, t + 8, t + 12
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const unsigned char* row = base + S::kCodes + (16 * u + t + 4 * q) * (16 * G);
+        if constexpr (G == 4) {
+          const uint2 v =
+              *reinterpret_cast<const uint2*>(row + ((g >> 1) ^ (t & 2)) * 16 + (g & 1) * 8);
+          vw[q][0] = v.x;
+          vw[q][1] = v.y;
+        } else {
+          vw[q][0] = *reinterpret_cast<const uint32_t*>(row + 4 * g);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+        uint32_t lo[4], hi[4];
+        codes_f16(__byte_perm(vw[0][j / 2], vw[1][j / 2], sel), lo);
+        codes_f16(__byte_perm(vw[2][j / 2], vw[3][j / 2], sel), hi);
+        const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]}, a1[4] = {lo[2], lo[3], hi[2], hi[3]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint32_t b0 = transpose8x8(pack_f16(w[n][0] * vs[0][j], w[n][1] * vs[0][j]));
+          const uint32_t b1 = transpose8x8(pack_f16(w[n][2] * vs[1][j], w[n][3] * vs[1][j]));
+          mma16816(o[n][2 * j], a0, b0, b1);
+          mma16816(o[n][2 * j + 1], a1, b0, b1);
+        }
+      }
+    }
+
+    // ---- the segment or this worker's share of it is done
+    const bool last = cur.unit + 1 == cur.units;
+    if (last || i + 1 == count) {
+      fresh = true;
+      const int head = cur.seg / a.passes, pass = cur.seg - head * a.passes;
+      const bool whole = last && seg_first == 0;
+      float* part = a.parts + ((int64_t)worker * 2 + (seg_first == 0 ? 1 : 0)) * NQ * (D + 2);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float l = sum[n][k];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
+          const int qi = 8 * n + 2 * t + k;  // in this pass
+          if (pass * NQ + qi >= a.group) continue;
+          if (whole) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            __nv_bfloat16* out =
+                a.out + ((int64_t)cur.r * a.q_heads + head * a.group + pass * NQ + qi) * D;
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              const __nv_bfloat162 p0 = __floats2bfloat162_rn(o[n][2 * j][k] * inv, o[n][2 * j][k + 2] * inv);
+              const __nv_bfloat162 p1 =
+                  __floats2bfloat162_rn(o[n][2 * j + 1][k] * inv, o[n][2 * j + 1][k + 2] * inv);
+              *reinterpret_cast<uint2*>(out + 32 * j + 4 * g) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
+            }
+          } else {
+            float* p = part + qi * (D + 2);
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              float2* d = reinterpret_cast<float2*>(p + 32 * j + 4 * g);
+              d[0] = make_float2(o[n][2 * j][k], o[n][2 * j][k + 2]);
+              d[1] = make_float2(o[n][2 * j + 1][k], o[n][2 * j + 1][k + 2]);
+            }
+            if (g == 0) *reinterpret_cast<float2*>(p + D) = make_float2(ref[n][k], l);
+          }
+        }
+    }
+    cur.next(a, segs);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
   report(a.err, err);
+}
+
+// Join: out = sum_i 2^(ref_i - top) o_i / sum_i 2^(ref_i - top) l_i over the parts the
+// workers left of one (request, query head).  Its warps take the parts in turn, each
+// lane D / 32 channels; which worker holds which part follows from the offsets alone.
+template <int G, int NT>
+__global__ void __launch_bounds__(256) join_q4_kernel(AttnArgs a) {
+  constexpr int D = 32 * G, NQ = 8 * NT;
+  __shared__ float s_o[8][D], s_l[8], s_top[8];
+  pdl_allow_next();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int r = blockIdx.x / a.q_heads, qh = blockIdx.x - r * a.q_heads;
+  const int segs = a.at.kv_heads * a.passes;
+  const int64_t at = a.offsets[r], total = a.offsets[a.num_reqs];
+  const int64_t units = (a.offsets[r + 1] - at) / segs;
+  const int64_t share = (total + a.workers - 1) / a.workers;
+  if (units == 0) return;  // zeros, already written
+  const int head = qh / a.group, qi = qh - head * a.group;
+  const int64_t lo = at + (int64_t)(head * a.passes + qi / NQ) * units;
+  const int64_t i0 = lo / share, i1 = (lo + units - 1) / share;
+  if (i0 == i1) return;    // one worker saw it whole
+  const float* parts = a.parts + (int64_t)(qi % NQ) * (D + 2);
+  constexpr int64_t kPart = NQ * (D + 2);
+  auto part = [&](int64_t i) { return parts + (2 * i + (i == i0 ? 1 : 0)) * kPart; };
+
+  float top = kRefStart;
+  for (int64_t i = i0 + threadIdx.x; i <= i1; i += blockDim.x) top = fmaxf(top, part(i)[D]);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+  if (warps > 1) {
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < warps; ++w) top = fmaxf(top, s_top[w]);
+  }
+  float acc[G] = {}, l = 0.f;
+#pragma unroll 4
+  for (int64_t i = i0 + warp; i <= i1; i += warps) {
+    const float* p = part(i);
+    const float f = ex2(p[D] - top);
+    l += f * p[D + 1];
+#pragma unroll
+    for (int j = 0; j < G; ++j) acc[j] += f * p[32 * j + lane];
+  }
+  if (warps > 1) {
+#pragma unroll
+    for (int j = 0; j < G; ++j) s_o[warp][32 * j + lane] = acc[j];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < warps; ++w) {
+      l += s_l[w];
+#pragma unroll
+      for (int j = 0; j < G; ++j) acc[j] += s_o[w][32 * j + lane];
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int j = 0; j < G; ++j)
+    a.out[((int64_t)r * a.q_heads + qh) * D + 32 * j + lane] = __float2bfloat16_rn(acc[j] * inv);
+}
+
+// Query heads a warp takes at once: 8, or 16 where a KV head has more than 8 (the cache is
+// read once for both halves).
+int columns(int group) { return group > 8 ? 16 : 8; }
+int worker_count(int group) { return sm_count() * (group > 8 ? 3 : 4) * kWarps; }
+int64_t offsets_bytes(int32_t num_reqs) { return ((int64_t)(num_reqs + 1) * 8 + 127) / 128 * 128; }
+
+template <int G, int NT>
+int launch(const AttnArgs& a, cudaStream_t stream) {
+  auto kernel = attention_q4_kernel<G, NT>;
+  constexpr int smem = kWarps * kStages * Stage<G>::kBytes;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return KV_ECUDA;
+  const int rc = launch_pdl(kernel, a.workers / kWarps, kThreads, smem, stream, a);
+  if (rc != KV_OK) return rc;
+  // a row has about workers / (requests x KV heads) parts: more warps where that is long
+  const int64_t rows = (int64_t)a.num_reqs * a.q_heads;
+  const int warps = rows >= 2048 ? 1 : rows >= 512 ? 4 : 8;
+  return launch_pdl(join_q4_kernel<G, NT>, (unsigned)rows, 32 * warps, 0, stream, a);
 }
 
 }  // namespace
@@ -86,7 +619,11 @@ extern "C" int64_t kv_attention_q4_workspace(int32_t num_reqs, int32_t num_q_hea
   if (num_reqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       num_q_heads % num_kv_heads != 0)
     return KV_EINVAL;
-  return 0;
+  if (num_reqs > KV_MAX_GATHER_REQS || num_q_heads > 4096 || (head_dim != 64 && head_dim != 128))
+    return KV_EUNSUPPORTED;
+  const int group = num_q_heads / num_kv_heads;
+  return offsets_bytes(num_reqs) +
+         (int64_t)worker_count(group) * 2 * columns(group) * (head_dim + 2) * 4;
 }
 
 extern "C" int kv_attention_q4(const void* query, int64_t query_stride, const void* k_cache,
@@ -118,11 +655,16 @@ extern "C" int kv_attention_q4(const void* query, int64_t query_stride, const vo
   const int64_t need = kv_attention_q4_workspace(num_reqs, num_q_heads, num_kv_heads, head_dim);
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
     return KV_EINVAL;
+  const int group = num_q_heads / num_kv_heads;
   AttnArgs a{static_cast<const __nv_bfloat16*>(query), query_stride,
              static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
              Q4Layout{(int64_t)layer * num_blocks, num_blocks, block_size, num_kv_heads, head_dim},
-             block_table, table_stride, span_start, span_end, num_reqs, num_q_heads, scale,
-             static_cast<__nv_bfloat16*>(out), d_err};
-  return launch_pdl(head_dim == 128 ? attention_q4_kernel<4> : attention_q4_kernel<2>,
-                    (unsigned)((int64_t)num_reqs * num_q_heads), 32, 0, stream, a);
+             BlockDiv::make(block_size), block_table, table_stride, span_start, span_end, num_reqs,
+             num_q_heads, group, (group + columns(group) - 1) / columns(group),
+             worker_count(group), scale * 1.44269504088896340736f,
+             static_cast<__nv_bfloat16*>(out), static_cast<int64_t*>(workspace),
+             reinterpret_cast<float*>(static_cast<char*>(workspace) + offsets_bytes(num_reqs)),
+             d_err};
+  if (head_dim == 128) return group > 8 ? launch<4, 2>(a, stream) : launch<4, 1>(a, stream);
+  return group > 8 ? launch<2, 2>(a, stream) : launch<2, 1>(a, stream);
 }

@@ -168,5 +168,6 @@ def test_records_past_four_gigabytes():
     want = torch.from_numpy((codes.reshape(T, H, 4, 32) - 8) * scale[..., None]).reshape(T, H, D)
     assert torch.equal(k.cpu(), want.float().to(BF16)) and torch.equal(v.cpu(), (-want).float().to(BF16))
     o = kv.kv_attention_q4(x[:1], kc, vc, i32([[B - 1]]), i32([0]), i32([T]), T)
-    wo, bound = ref.attend(x[:1], want.to(dev()), -want.to(dev()), [T], D ** -0.5, 2.0 ** -8)
+    wo, bound = ref.attend(x[:1], want.to(dev()), -want.to(dev()), [T], D ** -0.5, 2.0 ** -8,
+                           unit=ref.units(vc, T, D, 0, slots.cpu()))
     ref.check(o, wo, bound)

@@ -87,17 +87,21 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four pairs of codes (nibble n of the low and of the high half of x) as fp16 pairs u - 8.
-// 0x6400 | u is 1024 + u, and 0x6400 | u << 4 is 1024 + 16 u: one fma makes either exact.
+// Four pairs of codes (nibble n of the low and of the high half of x) as fp16 pairs
+// (u - 8) 2^-9.  A masked nibble is an fp16 of its own: u 2^-24 below the normal range, or
+// u 2^-20 one nibble up, and one exact fma makes either what is wanted: one logic and one
+// fma instruction a pair, where or-ing an exponent in took two logic instructions
+// (0x64006400 and the mask do not fit one instruction: 292 of them per unit, now 164).
+constexpr float kCodeScale = 512.f;  // what products of codes are multiplied with
 __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&f)[4]) {
-  const __half2 one = __float2half2_rn(1.f), sub = __float2half2_rn(-1032.f);
-  const __half2 sixteenth = __float2half2_rn(0.0625f), sub16 = __float2half2_rn(-72.f);
+  const __half2 m0 = __float2half2_rn(32768.f), m1 = __float2half2_rn(2048.f);
+  const __half2 sub = __float2half2_rn(-8.f / kCodeScale);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t y = h ? x >> 8 : x;
-    const uint32_t lo = (y & 0x000f000fu) | 0x64006400u, hi = (y & 0x00f000f0u) | 0x64006400u;
-    const __half2 a = __hfma2(*reinterpret_cast<const __half2*>(&lo), one, sub);
-    const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), sixteenth, sub16);
+    const uint32_t lo = y & 0x000f000fu, hi = y & 0x00f000f0u;
+    const __half2 a = __hfma2(*reinterpret_cast<const __half2*>(&lo), m0, sub);
+    const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), m1, sub);
     f[2 * h] = *reinterpret_cast<const uint32_t*>(&a);
     f[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&b);
   }
@@ -114,6 +118,17 @@ __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, uint32
                : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)[N]) {
+  if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
 template <int G>
 struct Stage {
   static constexpr int kCodes = kUnit * 16 * G;  // bytes of K (or V) codes
@@ -121,29 +136,47 @@ struct Stage {
   static constexpr int kBytes = 2 * kCodes + 2 * kScales;
 };
 
-// Units of a request's span, and 0 for an invalid one.  Positions past the table row are
-// cut off here, so the work is bounded by the table whatever the span says.
-__device__ __forceinline__ int span_units(const AttnArgs& a, int r, uint32_t& err) {
+// A request's span, cut at the end of its table row (so the work is bounded by the table
+// whatever the span says), in units of 32 positions that start at multiples of 32.  Blocks
+// are multiples of 8 tokens, so 8 aligned positions always lie in one block.
+struct Span {
+  int32_t lo, hi;    // positions [lo, hi)
+  int32_t first;     // unit of position lo
+  int32_t units;     // 0: nothing to attend
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int r, uint32_t& err) {
   const int64_t row = (int64_t)a.stride * a.at.block_size;
-  const int64_t s0 = a.start[r], s1 = a.end[r];
+  const int32_t s0 = a.start[r], s1 = a.end[r];
   if (s0 < 0 || s1 < s0 || (s1 > row && s1 > s0)) err |= KV_ERR_BAD_POSITION;
-  const int64_t n = s0 < 0 ? 0 : min(s1, row) - s0;
-  return n <= 0 ? 0 : (int)((n + kUnit - 1) / kUnit);
+  Span s;
+  s.lo = s0;
+  s.hi = (int32_t)min((int64_t)s1, row);
+  const bool any = s0 >= 0 && s.hi > s0;
+  s.first = any ? s0 / kUnit : 0;
+  s.units = any ? (s.hi - 1) / kUnit - s.first + 1 : 0;
+  return s;
+}
+__device__ __forceinline__ int span_units(const AttnArgs& a, int r, uint32_t& err) {
+  return span_of(a, r, err).units;
 }
 
-// Where a worker is: unit `unit` of `units` of segment `seg` of request r.
+// Where a worker is: unit `unit` of its request's span, of head `head`, pass `pass`.
 struct Cursor {
-  int r, seg, unit, units;
-  __device__ __forceinline__ void next(const AttnArgs& a, int segs) {
-    if (++unit < units) return;
+  int r, head, pass, unit;
+  Span span;
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    if (++unit < span.units) return;
     unit = 0;
-    if (++seg < segs) return;
-    seg = 0;
+    if (++pass < a.passes) return;
+    pass = 0;
+    if (++head < a.at.kv_heads) return;
+    head = 0;
     uint32_t ignore = 0;
     do {
       ++r;
-      units = r < a.num_reqs ? span_units(a, r, ignore) : 1;
-    } while (units == 0);
+      if (r >= a.num_reqs) return;  // behind the last unit: not used again
+      span = span_of(a, r, ignore);
+    } while (span.units == 0);
   }
 };
 
@@ -216,37 +249,50 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
     int r = lo * per;
     int64_t at = s_before[lo];
     uint32_t ignore = 0;
-    int u = span_units(a, r, ignore);
-    while (at + (int64_t)u * segs <= first) {
-      at += (int64_t)u * segs;
-      u = span_units(a, ++r, ignore);
+    load.span = span_of(a, r, ignore);
+    while (at + (int64_t)load.span.units * segs <= first) {
+      at += (int64_t)load.span.units * segs;
+      load.span = span_of(a, ++r, ignore);
     }
     const int64_t rest = first - at;
+    const int seg = (int)(rest / load.span.units);
     load.r = r;
-    load.units = u;
-    load.seg = (int)(rest / u);
-    load.unit = (int)(rest - (int64_t)load.seg * u);
+    load.unit = (int)(rest - (int64_t)seg * load.span.units);
+    load.head = seg / a.passes;
+    load.pass = seg - load.head * a.passes;
   }
   Cursor cur = load;
 
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * kStages * S::kBytes;
   const unsigned char* ring_p = smem + warp * kStages * S::kBytes;
-  const int64_t rec_bytes = a.at.record_bytes();
+  // this lane's piece of every 512 bytes of codes: token tok, 16-byte chunk c, and where K and V
+  // pieces go (see the layout above)
+  const int piece_tok = lane / G, piece_c = lane % G;
+  const uint32_t k_dst = (2 * (piece_tok & 3) + ((piece_tok >> 2) & 1) + (piece_tok & 8)) * (16 * G) +
+                         16 * piece_c;
+  const uint32_t v_dst =
+      piece_tok * (16 * G) + 16 * (G == 4 ? piece_c ^ (2 * ((piece_tok >> 1) & 1)) : piece_c);
   const int T = a.at.block_size;
 
-  // ---- loads: the block of this lane's token of the next unit is looked up one unit ahead
-  int32_t nb = kNull;  // its block, or null
-  int32_t n_off = 0;
+  // ---- loads.  Lane l stands for run l & 3: 8 positions of the unit, in one block.  The
+  // block is looked up one unit ahead.
+  int32_t nb = kNull;   // the run's block, or null
+  int32_t n_off = 0;    // its first token in the block
+  uint32_t n_mask = 0;  // positions of the unit inside the span
   auto look_up = [&]() {
     nb = kNull;
+    n_mask = 0;
     if (load.r >= a.num_reqs) return;
-    const int64_t p = (int64_t)a.start[load.r] + (int64_t)load.unit * kUnit + lane;
-    if (p >= a.end[load.r]) return;
+    const int32_t p = (load.span.first + load.unit) * kUnit;
+    const int32_t skip = load.span.lo - p, stop = load.span.hi - p;  // both in this unit's terms
+    n_mask = (skip > 0 ? kFull << skip : kFull) & (stop < kUnit ? (1u << stop) - 1u : kFull);
+    const int32_t run = p + 8 * (lane & 3);
+    if (run >= load.span.hi || run + 7 < load.span.lo) return;
     int64_t lb, off;
-    a.div.divmod(p, lb, off);
+    a.div.divmod(run, lb, off);
     n_off = (int32_t)off;
-    if (lb < a.stride) nb = a.table[(int64_t)load.r * a.stride + lb];
+    nb = a.table[(int64_t)load.r * a.stride + lb];
   };
   auto issue = [&](int stage) {
     bool valid = nb != kNull;
@@ -254,28 +300,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
       err |= KV_ERR_BAD_BLOCK;
       valid = false;
     }
-    const int head = load.seg / a.passes;
-    const int64_t rec = valid ? a.at.record(nb, head) : 0;
-    const int64_t row = rec + (int64_t)n_off * (16 * G);
+    const int64_t rec = a.at.record(valid ? nb : 0, load.head);
+    const int64_t codes = rec + (int64_t)(valid ? n_off : 0) * (16 * G);
+    const int64_t scales = rec + (int64_t)T * (16 * G) + (int64_t)(valid ? n_off : 0) * (2 * G);
+    // 4 validity bits of the runs, each spread over its 8 positions
+    const uint32_t runs = __ballot_sync(kFull, valid) & 15u;
+    const uint32_t spread = ((runs * 0x00204081u) & 0x01010101u) * 0xffu;
     const uint32_t base = ring + stage * S::kBytes;
-    const uint32_t mask = __ballot_sync(kFull, valid);
-    if (lane == 0) s_valid[warp][stage] = mask;
+    if (lane == 0) s_valid[warp][stage] = n_mask & spread;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const int tok = i * (32 / G) + lane / G, c = lane % G;
-      const int64_t src = __shfl_sync(kFull, row, tok) + 16 * c;
-      const uint32_t bytes = (mask >> tok) & 1u ? 16u : 0u;
-      const int64_t at = bytes ? src : 0;
-      const uint32_t k_row = (tok & 24) + 2 * (tok & 3) + ((tok >> 2) & 1);
-      const uint32_t v_c = G == 4 ? c ^ (2 * ((tok >> 1) & 1)) : c;
-      copy16(base + k_row * (16 * G) + 16 * c, a.k_cache + at, bytes);
-      copy16(base + S::kCodes + tok * (16 * G) + 16 * v_c, a.v_cache + at, bytes);
+    for (int i = 0; i < G; ++i) {  // 32 / G tokens each: lane's piece is 16 lane bytes into them
+      const int run = G == 4 ? i : 2 * i + (lane >> 4);
+      const int64_t src = __shfl_sync(kFull, codes, run) + (G == 4 ? 16 * lane : 16 * (lane & 15));
+      const uint32_t bytes = (runs >> run) & 1u ? 16u : 0u;
+      copy16(base + k_dst + i * 512, a.k_cache + src, bytes);
+      copy16(base + S::kCodes + v_dst + i * 512, a.v_cache + src, bytes);
     }
-    const int64_t sc = valid ? rec + (int64_t)T * (16 * G) + (int64_t)n_off * (2 * G) : 0;
-    copy_small<2 * G>(base + 2 * S::kCodes + lane * (2 * G), a.k_cache + sc, valid ? 2 * G : 0);
-    copy_small<2 * G>(base + 2 * S::kCodes + S::kScales + lane * (2 * G), a.v_cache + sc,
-                      valid ? 2 * G : 0);
-    load.next(a, segs);
+    const int64_t sc = __shfl_sync(kFull, scales, lane >> 3) + (lane & 7) * (2 * G);
+    const uint32_t bytes = (runs >> (lane >> 3)) & 1u ? 2 * G : 0;
+    copy_small<2 * G>(base + 2 * S::kCodes + lane * (2 * G), a.k_cache + sc, bytes);
+    copy_small<2 * G>(base + 2 * S::kCodes + S::kScales + lane * (2 * G), a.v_cache + sc, bytes);
+    load.next(a);
     look_up();
   };
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
@@ -304,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
     if (fresh) {  // a new (request, head, pass)
       fresh = false;
       seg_first = cur.unit;
-      const int head = cur.seg / a.passes, pass = cur.seg - head * a.passes;
+      const int head = cur.head, pass = cur.pass;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int qi = pass * NQ + 8 * n + g;
@@ -340,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
         // column 2 t + k is the query head of lanes 4 (2 t + k) ..
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          qc[n][k] = __shfl_sync(kFull, up, 4 * (2 * t + k)) * a.scale_log2;
+          qc[n][k] = __shfl_sync(kFull, up, 4 * (2 * t + k)) * (a.scale_log2 * kCodeScale);
           ref[n][k] = kRefStart;
           sum[n][k] = 0.f;
         }
@@ -380,10 +425,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
           x[h][1] = __byte_perm(w.x, w.y, 0x7632);
         }
         const unsigned char* sc = base + 2 * S::kCodes + (16 * u + 8 * h + tok) * (2 * G);
+        uint32_t kw[G / 2], vv2[G / 2];
+        load_words<G / 2>(sc, kw);
+        load_words<G / 2>(sc + S::kScales, vv2);
 #pragma unroll
         for (int j = 0; j < G; j += 2) {
-          const uint32_t kk = *reinterpret_cast<const uint32_t*>(sc + 2 * j);
-          const uint32_t vv = *reinterpret_cast<const uint32_t*>(sc + S::kScales + 2 * j);
+          const uint32_t kk = kw[j / 2], vv = vv2[j / 2];
           ks[h][j] = __uint_as_float(kk << 16);
           ks[h][j + 1] = __uint_as_float(kk & 0xffff0000u);
           vs[h][j] = __uint_as_float(vv << 16);
@@ -406,6 +453,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
         }
       }
       // ---- weights
+      if (mask != kFull) {  // hidden positions: no weight, and a scale that may be anything
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (!((mask >> (16 * u + 8 * h + tok)) & 1u)) {
+#pragma unroll
+            for (int j = 0; j < G; ++j) vs[h][j] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][2 * h] = s[n][2 * h + 1] = -INFINITY;
+          }
+      }
       float unit[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -420,7 +477,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           s[n][k] *= qc[n][k & 1];
-          if (mask != kFull && !((mask >> (16 * u + 8 * (k >> 1) + tok)) & 1u)) s[n][k] = -INFINITY;
           w[n][k] = ex2(s[n][k] - ref[n][k & 1]);
           most = fmaxf(most, w[n][k] * unit[k >> 1]);
         }
@@ -483,10 +539,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
     }
 
     // ---- the segment or this worker's share of it is done
-    const bool last = cur.unit + 1 == cur.units;
+    const bool last = cur.unit + 1 == cur.span.units;
     if (last || i + 1 == count) {
       fresh = true;
-      const int head = cur.seg / a.passes, pass = cur.seg - head * a.passes;
+      const int head = cur.head, pass = cur.pass;
       const bool whole = last && seg_first == 0;
       float* part = a.parts + ((int64_t)worker * 2 + (seg_first == 0 ? 1 : 0)) * NQ * (D + 2);
 #pragma unroll
@@ -499,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
           const int qi = 8 * n + 2 * t + k;  // in this pass
           if (pass * NQ + qi >= a.group) continue;
           if (whole) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float inv = l == 0.f ? 0.f : kCodeScale / l;
             __nv_bfloat16* out =
                 a.out + ((int64_t)cur.r * a.q_heads + head * a.group + pass * NQ + qi) * D;
 #pragma unroll
@@ -522,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
           }
         }
     }
-    cur.next(a, segs);
+    cur.next(a);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   report(a.err, err);
@@ -582,7 +638,7 @@ __global__ void __launch_bounds__(256) join_q4_kernel(AttnArgs a) {
       for (int j = 0; j < G; ++j) acc[j] += s_o[w][32 * j + lane];
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : kCodeScale / l;
 #pragma unroll
   for (int j = 0; j < G; ++j)
     a.out[((int64_t)r * a.q_heads + qh) * D + 32 * j + lane] = __float2bfloat16_rn(acc[j] * inv);

@@ -38,7 +38,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 3;
+constexpr int kCtas = 3;                  // per SM: 12 warps of 168 registers
+constexpr int kStages = 4;
 constexpr int kUnit = 32;                 // tokens of a unit
 constexpr float kRefStart = -1e30f;       // below every logit, and finite
 constexpr float kLimit = 256.0f;          // a weight times its scale above this raises the reference
@@ -50,6 +51,7 @@ struct AttnArgs {
   const uint8_t* k_cache;
   const uint8_t* v_cache;
   Q4Layout at;
+  int32_t num_blocks32;  // num_blocks, or the largest block id + 1 there can be
   BlockDiv div;
   const int32_t* table;
   int32_t stride;
@@ -87,23 +89,37 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four pairs of codes (nibble n of the low and of the high half of x) as fp16 pairs
-// (u - 8) 2^-9.  A masked nibble is an fp16 of its own: u 2^-24 below the normal range, or
-// u 2^-20 one nibble up, and one exact fma makes either what is wanted: one logic and one
-// fma instruction a pair, where or-ing an exponent in took two logic instructions
-// (0x64006400 and the mask do not fit one instruction: 292 of them per unit, now 164).
-constexpr float kCodeScale = 512.f;  // what products of codes are multiplied with
-__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&f)[4]) {
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1, float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+// Four pairs of codes (nibble n of the low and of the high half of x) as fp16 operands.  A
+// masked nibble is an fp16 of its own, below the normal range: u 2^-24, or u 2^-20 one nibble
+// up (odd n).
+constexpr float kCode = 16777216.f;  // 2^24
+__device__ __forceinline__ void codes_raw(uint32_t x, uint32_t (&f)[4]) {
+  const uint32_t y = x >> 8;
+  f[0] = x & 0x000f000fu;
+  f[1] = x & 0x00f000f0u;
+  f[2] = y & 0x000f000fu;
+  f[3] = y & 0x00f000f0u;
+}
+// K's go into the product as they are (one logic instruction a pair): odd channels meet a
+// query divided by 16, and the 8 that belongs off every code is what the accumulator starts
+// from, -8 sum q.  V's become (u - 8) 2^-9 with one exact fma a pair: their sums run over
+// thousands of tokens, where an 8 taken off at the end would cost the bits of the result.
+constexpr float kCentred = 512.f;
+__device__ __forceinline__ void codes_centred(uint32_t x, uint32_t (&f)[4]) {
   const __half2 m0 = __float2half2_rn(32768.f), m1 = __float2half2_rn(2048.f);
-  const __half2 sub = __float2half2_rn(-8.f / kCodeScale);
+  const __half2 sub = __float2half2_rn(-8.f / kCentred);
+  codes_raw(x, f);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t y = h ? x >> 8 : x;
-    const uint32_t lo = y & 0x000f000fu, hi = y & 0x00f000f0u;
-    const __half2 a = __hfma2(*reinterpret_cast<const __half2*>(&lo), m0, sub);
-    const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), m1, sub);
-    f[2 * h] = *reinterpret_cast<const uint32_t*>(&a);
-    f[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&b);
+  for (int n = 0; n < 4; ++n) {
+    const __half2 a = __hfma2(*reinterpret_cast<const __half2*>(&f[n]), n & 1 ? m1 : m0, sub);
+    f[n] = *reinterpret_cast<const uint32_t*>(&a);
   }
 }
 // src_bytes 0 writes zeros and reads nothing.
@@ -118,14 +134,21 @@ __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, uint32
                : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)[N]) {
-  if constexpr (N == 2) {
+// The G bf16 scales of a token.
+template <int G>
+__device__ __forceinline__ void load_scales(const unsigned char* p, float (&f)[G]) {
+  uint32_t w[G / 2];
+  if constexpr (G == 4) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x;
     w[1] = v.y;
   } else {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+#pragma unroll
+  for (int j = 0; j < G; j += 2) {
+    f[j] = __uint_as_float(w[j / 2] << 16);
+    f[j + 1] = __uint_as_float(w[j / 2] & 0xffff0000u);
   }
 }
 
@@ -156,39 +179,54 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int r, uint32_t& err)
   s.units = any ? (s.hi - 1) / kUnit - s.first + 1 : 0;
   return s;
 }
-__device__ __forceinline__ int span_units(const AttnArgs& a, int r, uint32_t& err) {
-  return span_of(a, r, err).units;
-}
-
-// Where a worker is: unit `unit` of its request's span, of head `head`, pass `pass`.
+// The unit a worker loads next: positions [p, p + 32) of request r, for head `head`, pass
+// `pass`; `left` units of this (request, head, pass) are still to load, this one included.
 struct Cursor {
-  int r, head, pass, unit;
+  int r, head, pass, left;
+  int32_t p;
   Span span;
   __device__ __forceinline__ void next(const AttnArgs& a) {
-    if (++unit < span.units) return;
-    unit = 0;
-    if (++pass < a.passes) return;
-    pass = 0;
-    if (++head < a.at.kv_heads) return;
-    head = 0;
-    uint32_t ignore = 0;
-    do {
-      ++r;
-      if (r >= a.num_reqs) return;  // behind the last unit: not used again
-      span = span_of(a, r, ignore);
-    } while (span.units == 0);
+    p += kUnit;
+    if (--left == 0) next_segment(a);
+  }
+  __device__ __forceinline__ void next_segment(const AttnArgs& a) {
+    if (++pass == a.passes) {
+      pass = 0;
+      if (++head == a.at.kv_heads) {
+        head = 0;
+        uint32_t ignore = 0;
+        do {
+          if (++r >= a.num_reqs) {  // behind the last unit: not loaded
+            left = 1;
+            p = 0;
+            span.lo = span.hi = 0;
+            return;
+          }
+          span = span_of(a, r, ignore);
+        } while (span.units == 0);
+      }
+    }
+    left = span.units;
+    p = span.first * kUnit;
   }
 };
 
-template <int G, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel(AttnArgs a) {
-  constexpr int D = 32 * G, NQ = 8 * NT;
+// kPack (at most 4 query heads per KV head): the 8 columns of the products are the 4 heads for
+// tokens 0-15 of the unit and the 4 heads for tokens 16-31, so the work between the products is
+// done once per unit.  Query fragments hold zeros in the other half's columns; each half has
+// sums and references of its own, added when the segment ends.
+template <int G, int NT, bool kPack>
+__global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs a) {
+  constexpr int D = 32 * G, NQ = kPack ? 4 : 8 * NT;
+  constexpr int kHalves = kPack ? 2 : 1;  // token halves that share the columns
   using S = Stage<G>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_before[kThreads];  // units before each thread's share of the requests
   __shared__ int64_t s_warp[kWarps];
   __shared__ int64_t s_total;
-  __shared__ uint32_t s_valid[kWarps][kStages];
+  // per unit in the ring: positions that count; request; head << 16 | pass; 1: first of its
+  // segment, 2: last
+  __shared__ int4 s_unit[kWarps][kStages];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = a.at.kv_heads, segs = H * a.passes;
   pdl_allow_next();
@@ -201,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
     const int r_lo = min(a.num_reqs, tid * per), r_hi = min(a.num_reqs, r_lo + per);
     uint32_t span_err = 0;
     int64_t mine = 0;
-    for (int r = r_lo; r < r_hi; ++r) mine += (int64_t)span_units(a, r, span_err) * segs;
+    for (int r = r_lo; r < r_hi; ++r) mine += (int64_t)span_of(a, r, span_err).units * segs;
     if (blockIdx.x == 0) err |= span_err;
     const int64_t incl = warp_inclusive_scan<int64_t>(mine);
     if (lane == 31) s_warp[warp] = incl;
@@ -215,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
       int64_t at = before;
       for (int r = r_lo; r < r_hi; ++r) {
         a.offsets[r] = at;
-        at += (int64_t)span_units(a, r, ignore) * segs;
+        at += (int64_t)span_of(a, r, ignore).units * segs;
       }
       if (tid == kThreads - 1) a.offsets[a.num_reqs] = at;
     }
@@ -225,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
   // requests without a position: zeros
   for (int r = worker; r < a.num_reqs; r += a.workers) {
     uint32_t ignore = 0;
-    if (span_units(a, r, ignore) > 0) continue;
+    if (span_of(a, r, ignore).units > 0) continue;
     uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)r * a.q_heads * D);
     for (int i = lane; i < a.q_heads * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
   }
@@ -236,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
     report(a.err, err);
     return;
   }
-  const int64_t count = min(share, total - first);
+  int64_t count = min(share, total - first);
 
   // ---- this worker's first unit
   Cursor load;
@@ -256,12 +294,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
     }
     const int64_t rest = first - at;
     const int seg = (int)(rest / load.span.units);
+    const int unit = (int)(rest - (int64_t)seg * load.span.units);
     load.r = r;
-    load.unit = (int)(rest - (int64_t)seg * load.span.units);
+    load.left = load.span.units - unit;
+    load.p = (load.span.first + unit) * kUnit;
     load.head = seg / a.passes;
     load.pass = seg - load.head * a.passes;
   }
-  Cursor cur = load;
 
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * kStages * S::kBytes;
@@ -269,96 +308,114 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
   // this lane's piece of every 512 bytes of codes: token tok, 16-byte chunk c, and where K and V
   // pieces go (see the layout above)
   const int piece_tok = lane / G, piece_c = lane % G;
-  const uint32_t k_dst = (2 * (piece_tok & 3) + ((piece_tok >> 2) & 1) + (piece_tok & 8)) * (16 * G) +
-                         16 * piece_c;
-  const uint32_t v_dst =
-      piece_tok * (16 * G) + 16 * (G == 4 ? piece_c ^ (2 * ((piece_tok >> 1) & 1)) : piece_c);
+  const uint32_t k_dst = ring + 16 * piece_c +
+                         (2 * (piece_tok & 3) + ((piece_tok >> 2) & 1) + (piece_tok & 8)) * (16 * G);
+  const uint32_t v_dst = ring + S::kCodes + piece_tok * (16 * G) +
+                         16 * (G == 4 ? piece_c ^ (2 * ((piece_tok >> 1) & 1)) : piece_c);
+  const uint32_t s_dst = ring + 2 * S::kCodes + lane * (2 * G);
   const int T = a.at.block_size;
+  const uint32_t rec16 = (uint32_t)(T / 8) * (9 * G);  // T (16 G + 2 G) / 16
 
   // ---- loads.  Lane l stands for run l & 3: 8 positions of the unit, in one block.  The
   // block is looked up one unit ahead.
-  int32_t nb = kNull;   // the run's block, or null
-  int32_t n_off = 0;    // its first token in the block
-  uint32_t n_mask = 0;  // positions of the unit inside the span
+  int32_t nb;     // the run's block, or null
+  int32_t n_off;  // its first token in the block
   auto look_up = [&]() {
+    const int32_t run = load.p + 8 * (lane & 3);
     nb = kNull;
-    n_mask = 0;
-    if (load.r >= a.num_reqs) return;
-    const int32_t p = (load.span.first + load.unit) * kUnit;
-    const int32_t skip = load.span.lo - p, stop = load.span.hi - p;  // both in this unit's terms
-    n_mask = (skip > 0 ? kFull << skip : kFull) & (stop < kUnit ? (1u << stop) - 1u : kFull);
-    const int32_t run = p + 8 * (lane & 3);
-    if (run >= load.span.hi || run + 7 < load.span.lo) return;
     int64_t lb, off;
     a.div.divmod(run, lb, off);
     n_off = (int32_t)off;
-    nb = a.table[(int64_t)load.r * a.stride + lb];
+    if (run < load.span.hi && run + 7 >= load.span.lo) nb = a.table[(int64_t)load.r * a.stride + lb];
   };
   auto issue = [&](int stage) {
-    bool valid = nb != kNull;
-    if (valid && (nb < 0 || nb >= a.at.num_blocks)) {
-      err |= KV_ERR_BAD_BLOCK;
-      valid = false;
-    }
-    const int64_t rec = a.at.record(valid ? nb : 0, load.head);
-    const int64_t codes = rec + (int64_t)(valid ? n_off : 0) * (16 * G);
-    const int64_t scales = rec + (int64_t)T * (16 * G) + (int64_t)(valid ? n_off : 0) * (2 * G);
-    // 4 validity bits of the runs, each spread over its 8 positions
+    // offsets in 16-byte pieces of the layer (32 bits: checked on the host); a run's codes are
+    // 8 G pieces, its scales G
+    const bool valid = nb > kNull && nb < a.num_blocks32;
     const uint32_t runs = __ballot_sync(kFull, valid) & 15u;
-    const uint32_t spread = ((runs * 0x00204081u) & 0x01010101u) * 0xffu;
-    const uint32_t base = ring + stage * S::kBytes;
-    if (lane == 0) s_valid[warp][stage] = n_mask & spread;
+    const uint32_t rec = valid ? ((uint32_t)nb * (uint32_t)H + (uint32_t)load.head) * rec16 : 0u;
+    const uint32_t off = valid ? (uint32_t)n_off : 0u;
+    const uint32_t codes = rec + off * G, scales = rec + (uint32_t)T * G + (off >> 3) * G;
+    uint32_t mask = kFull;
+    if (runs != 15u || load.p < load.span.lo || load.p + kUnit - 1 >= load.span.hi) {
+      if (!valid && nb != kNull) err |= KV_ERR_BAD_BLOCK;
+      // 4 validity bits of the runs, each spread over its 8 positions
+      mask = ((runs * 0x00204081u) & 0x01010101u) * 0xffu;
+      const int32_t skip = load.span.lo - load.p, stop = load.span.hi - load.p;
+      if (skip > 0) mask &= kFull << skip;
+      if (stop < kUnit) mask &= stop > 0 ? (1u << stop) - 1u : 0u;
+    }
+    if (lane == 0)
+      s_unit[warp][stage] = make_int4((int)mask, load.r, load.head << 16 | load.pass,
+                                      (load.p == load.span.first * kUnit ? 1 : 0) |
+                                          (load.left == 1 ? 2 : 0));
+    const uint32_t at = stage * S::kBytes;
 #pragma unroll
     for (int i = 0; i < G; ++i) {  // 32 / G tokens each: lane's piece is 16 lane bytes into them
       const int run = G == 4 ? i : 2 * i + (lane >> 4);
-      const int64_t src = __shfl_sync(kFull, codes, run) + (G == 4 ? 16 * lane : 16 * (lane & 15));
+      const uint64_t src =
+          (uint64_t)(__shfl_sync(kFull, codes, run) + (G == 4 ? lane : lane & 15)) * 16;
       const uint32_t bytes = (runs >> run) & 1u ? 16u : 0u;
-      copy16(base + k_dst + i * 512, a.k_cache + src, bytes);
-      copy16(base + S::kCodes + v_dst + i * 512, a.v_cache + src, bytes);
+      copy16(k_dst + at + i * 512, a.k_cache + src, bytes);
+      copy16(v_dst + at + i * 512, a.v_cache + src, bytes);
     }
-    const int64_t sc = __shfl_sync(kFull, scales, lane >> 3) + (lane & 7) * (2 * G);
+    const uint64_t sc =
+        (uint64_t)__shfl_sync(kFull, scales, lane >> 3) * 16 + (lane & 7) * (2 * G);
     const uint32_t bytes = (runs >> (lane >> 3)) & 1u ? 2 * G : 0;
-    copy_small<2 * G>(base + 2 * S::kCodes + lane * (2 * G), a.k_cache + sc, bytes);
-    copy_small<2 * G>(base + 2 * S::kCodes + S::kScales + lane * (2 * G), a.v_cache + sc, bytes);
+    copy_small<2 * G>(s_dst + at, a.k_cache + sc, bytes);
+    copy_small<2 * G>(s_dst + at + S::kScales, a.v_cache + sc, bytes);
     load.next(a);
     look_up();
   };
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
   look_up();
-#pragma unroll
+  int64_t to_load = count;
+#pragma unroll 1
   for (int s = 0; s < kStages - 1; ++s) {
-    if (s < count) issue(s);
+    if (to_load > 0) {
+      issue(s);
+      --to_load;
+    }
     commit();
   }
 
-  uint32_t qf[NT][G][2][2];  // query fragments
+  uint32_t qf[kHalves][NT][G][2][2];  // query fragments
   float qc[NT][2];           // what a logit of this lane's two columns is multiplied with
+  float qs[NT][G][2];        // -8 2^-24 sum q of a group, for those columns
   float o[NT][2 * G][4];     // sums: rows = channels, columns = query heads
   float ref[NT][2], sum[NT][2];
-  bool fresh = true;
-  int seg_first = 0;  // the unit of the segment this worker started with
+  bool fresh = true, from_start = false;
+  const int tok = (g >> 1) + 4 * (g & 1);               // this lane's token of each 8
+  const uint32_t half_mask = g < 4 ? kFull : 0u;        // kPack: columns of tokens 0-15
+  const int half_tok = kPack ? 16 * (t >> 1) + tok : tok;
 
   int stage = 0;
-  for (int64_t i = 0; i < count; ++i) {
+#pragma unroll 1
+  for (; count > 0; --count) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();
-    if (i + kStages - 1 < count) issue(stage == 0 ? kStages - 1 : stage - 1);  // the unit before's
+    if (to_load > 0) {
+      issue(stage == 0 ? kStages - 1 : stage - 1);  // where the unit before this one was
+      --to_load;
+    }
     commit();
 
+    const int4 now = s_unit[warp][stage];
+    const uint32_t mask = (uint32_t)now.x;
     if (fresh) {  // a new (request, head, pass)
       fresh = false;
-      seg_first = cur.unit;
-      const int head = cur.head, pass = cur.pass;
+      from_start = now.w & 1;
+      const int head = now.z >> 16, pass = now.z & 0xffff;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int qi = pass * NQ + 8 * n + g;
+        const int qi = pass * NQ + 8 * n + (kPack ? g & 3 : g);
         float x[G][8], top = 0.f;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (qi < a.group)
-            v = *reinterpret_cast<const uint4*>(a.q + cur.r * a.q_stride +
+            v = *reinterpret_cast<const uint4*>(a.q + now.y * a.q_stride +
                                                 (int64_t)(head * a.group + qi) * D + 32 * j + 8 * t);
           const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -370,22 +427,39 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
         }
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-        // 2^-e with e the exponent of the largest channel (1 for rows of zeros or infinities)
+        // 2^(13-e) with e the exponent of the largest channel (1 for rows of zeros, infinities)
         const int e = (int)(__float_as_uint(top) >> 23) - 127;
         const bool usual = e > -100 && e < 120;
-        const float down = usual ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.f;
-        const float up = usual ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f;
+        const float down = usual ? __uint_as_float((uint32_t)(140 - e) << 23) : 1.f;
+        const float up = usual ? __uint_as_float((uint32_t)(114 + e) << 23) : 1.f;
 #pragma unroll
-        for (int j = 0; j < G; ++j)
+        for (int j = 0; j < G; ++j) {
+          float total = 0.f;
 #pragma unroll
           for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              qf[n][j][s][k] = pack_f16(x[j][2 * s + k] * down, x[j][4 + 2 * s + k] * down);
+            for (int k = 0; k < 2; ++k) {
+              const float by = k ? down * 0.0625f : down;
+              const uint32_t f = pack_f16(x[j][2 * s + k] * by, x[j][4 + 2 * s + k] * by);
+              if (kPack) {
+                qf[0][n][j][s][k] = f & half_mask;
+                qf[kHalves - 1][n][j][s][k] = f & ~half_mask;
+              } else {
+                qf[0][n][j][s][k] = f;
+              }
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+              total += (k ? 16.f : 1.f) * (v.x + v.y);
+            }
+          total += __shfl_xor_sync(kFull, total, 1);
+          total += __shfl_xor_sync(kFull, total, 2);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            qs[n][j][k] = __shfl_sync(kFull, total, 4 * (2 * t + k)) * (-8.f / kCode);
+        }
         // column 2 t + k is the query head of lanes 4 (2 t + k) ..
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          qc[n][k] = __shfl_sync(kFull, up, 4 * (2 * t + k)) * (a.scale_log2 * kCodeScale);
+          qc[n][k] = __shfl_sync(kFull, up, 4 * (2 * t + k)) * (a.scale_log2 * kCode);
           ref[n][k] = kRefStart;
           sum[n][k] = 0.f;
         }
@@ -397,66 +471,63 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
     }
 
     const unsigned char* base = ring_p + stage * S::kBytes;
-    const uint32_t mask = s_valid[warp][stage];
-    const int tok = (g >> 1) + 4 * (g & 1);  // this lane's token in each 8 rows
-
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {  // 16 tokens each
-      // ---- logits
-      float s[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+    // K codes of 16 tokens (half u) times the query fragments, group by group
+    auto logits = [&](int u, int h, float (&acc)[G][NT][4], bool start) {
       uint32_t x[2][G];  // per row: the group's codes of g' = 2 t (low half) and 2 t + 1 (high)
-      float ks[2][G], vs[2][G];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const unsigned char* row = base + (16 * u + 8 * h + g) * (16 * G);
+      for (int r = 0; r < 2; ++r) {
+        const unsigned char* row = base + (16 * u + 8 * r + g) * (16 * G);
         if constexpr (G == 4) {
           const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * t);
-          x[h][0] = __byte_perm(w.x, w.z, 0x5410);
-          x[h][1] = __byte_perm(w.x, w.z, 0x7632);
-          x[h][2] = __byte_perm(w.y, w.w, 0x5410);
-          x[h][3] = __byte_perm(w.y, w.w, 0x7632);
+          x[r][0] = __byte_perm(w.x, w.z, 0x5410);
+          x[r][1] = __byte_perm(w.x, w.z, 0x7632);
+          x[r][2] = __byte_perm(w.y, w.w, 0x5410);
+          x[r][3] = __byte_perm(w.y, w.w, 0x7632);
         } else {
           const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * t);
-          x[h][0] = __byte_perm(w.x, w.y, 0x5410);
-          x[h][1] = __byte_perm(w.x, w.y, 0x7632);
-        }
-        const unsigned char* sc = base + 2 * S::kCodes + (16 * u + 8 * h + tok) * (2 * G);
-        uint32_t kw[G / 2], vv2[G / 2];
-        load_words<G / 2>(sc, kw);
-        load_words<G / 2>(sc + S::kScales, vv2);
-#pragma unroll
-        for (int j = 0; j < G; j += 2) {
-          const uint32_t kk = kw[j / 2], vv = vv2[j / 2];
-          ks[h][j] = __uint_as_float(kk << 16);
-          ks[h][j + 1] = __uint_as_float(kk & 0xffff0000u);
-          vs[h][j] = __uint_as_float(vv << 16);
-          vs[h][j + 1] = __uint_as_float(vv & 0xffff0000u);
+          x[r][0] = __byte_perm(w.x, w.y, 0x5410);
+          x[r][1] = __byte_perm(w.x, w.y, 0x7632);
         }
       }
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         uint32_t lo[4], hi[4];
-        codes_f16(x[0][j], lo);
-        codes_f16(x[1][j], hi);
+        codes_raw(x[0][j], lo);
+        codes_raw(x[1][j], hi);
         const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(acc, a0, qf[n][j][0][0], qf[n][j][0][1]);
-          mma16816(acc, a1, qf[n][j][1][0], qf[n][j][1][1]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[n][k] = fmaf(acc[k], ks[k >> 1][j], s[n][k]);
+          if (start)
+            mma16816_from(acc[j][n], a0, qf[h][n][j][0][0], qf[h][n][j][0][1], qs[n][j][0],
+                          qs[n][j][1]);
+          else
+            mma16816(acc[j][n], a0, qf[h][n][j][0][0], qf[h][n][j][0][1]);
+          mma16816(acc[j][n], a1, qf[h][n][j][1][0], qf[h][n][j][1][1]);
         }
       }
-      // ---- weights
-      if (mask != kFull) {  // hidden positions: no weight, and a scale that may be anything
+    };
+    // From the products to the weights times V's scales, as fragments of the second product;
+    // `first_tok`: this lane's first token of the unit (the second is 8 further).
+    auto weights = [&](int first_tok, const float (&acc)[G][NT][4], uint32_t (&b)[G][NT][2]) {
+      float ks[2][G], vs[2][G], s[NT][4], w[NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const unsigned char* sc = base + 2 * S::kCodes + (first_tok + 8 * h) * (2 * G);
+        load_scales<G>(sc, ks[h]);
+        load_scales<G>(sc + S::kScales, vs[h]);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[n][k] = acc[0][n][k] * ks[k >> 1][0];
+#pragma unroll
+          for (int j = 1; j < G; ++j) s[n][k] = fmaf(acc[j][n][k], ks[k >> 1][j], s[n][k]);
+        }
+      if (__any_sync(kFull, mask != kFull)) {  // hidden positions: no weight, any scale
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (!((mask >> (16 * u + 8 * h + tok)) & 1u)) {
+          if (!((mask >> (first_tok + 8 * h)) & 1u)) {
 #pragma unroll
             for (int j = 0; j < G; ++j) vs[h][j] = 0.f;
 #pragma unroll
@@ -470,14 +541,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
         if constexpr (G == 4) m = fmaxf(m, fmaxf(vs[h][2], vs[h][3]));
         unit[h] = fminf(fmaxf(m, kUnitMin), kUnitMax);
       }
-      float w[NT][4];
       float most = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          s[n][k] *= qc[n][k & 1];
-          w[n][k] = ex2(s[n][k] - ref[n][k & 1]);
+          w[n][k] = ex2(fmaf(s[n][k], qc[n][k & 1], -ref[n][k & 1]));
           most = fmaxf(most, w[n][k] * unit[k >> 1]);
         }
       if (__any_sync(kFull, most > kLimit)) {
@@ -487,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float z = fmaxf(s[n][k] + l0, s[n][k + 2] + l1);
+            float z = fmaxf(fmaf(s[n][k], qc[n][k], l0), fmaf(s[n][k + 2], qc[n][k], l1));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) z = fmaxf(z, __shfl_xor_sync(kFull, z, d));
             const float up = fmaxf(ref[n][k], z), f = ex2(ref[n][k] - up);
@@ -498,16 +567,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
               o[n][m][k] *= f;
               o[n][m][k + 2] *= f;
             }
-            w[n][k] = ex2(s[n][k] - up);
-            w[n][k + 2] = ex2(s[n][k + 2] - up);
+            w[n][k] = ex2(fmaf(s[n][k], qc[n][k], -up));
+            w[n][k + 2] = ex2(fmaf(s[n][k + 2], qc[n][k], -up));
           }
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         sum[n][0] += w[n][0] + w[n][2];
         sum[n][1] += w[n][1] + w[n][3];
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          b[j][n][0] = transpose8x8(pack_f16(w[n][0] * vs[0][j], w[n][1] * vs[0][j]));
+          b[j][n][1] = transpose8x8(pack_f16(w[n][2] * vs[1][j], w[n][3] * vs[1][j]));
+        }
       }
-      // ---- values
+    };
+    // V codes of 16 tokens (half u) times weight fragments; columns outside `keep` count as 0
+    auto values = [&](int u, const uint32_t (&b)[G][NT][2], uint32_t keep) {
       uint32_t vw[4][G / 2];  // tokens t, t + 4, t + 8, t + 12
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -525,26 +601,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
       for (int j = 0; j < G; ++j) {
         const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
         uint32_t lo[4], hi[4];
-        codes_f16(__byte_perm(vw[0][j / 2], vw[1][j / 2], sel), lo);
-        codes_f16(__byte_perm(vw[2][j / 2], vw[3][j / 2], sel), hi);
+        codes_centred(__byte_perm(vw[0][j / 2], vw[1][j / 2], sel), lo);
+        codes_centred(__byte_perm(vw[2][j / 2], vw[3][j / 2], sel), hi);
         const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]}, a1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint32_t b0 = transpose8x8(pack_f16(w[n][0] * vs[0][j], w[n][1] * vs[0][j]));
-          const uint32_t b1 = transpose8x8(pack_f16(w[n][2] * vs[1][j], w[n][3] * vs[1][j]));
+          const uint32_t b0 = kPack ? b[j][n][0] & keep : b[j][n][0];
+          const uint32_t b1 = kPack ? b[j][n][1] & keep : b[j][n][1];
           mma16816(o[n][2 * j], a0, b0, b1);
           mma16816(o[n][2 * j + 1], a1, b0, b1);
         }
       }
+    };
+
+    float acc[G][NT][4];
+    uint32_t b[G][NT][2];
+    if constexpr (kPack) {
+      logits(0, 0, acc, true);
+      logits(1, 1, acc, false);
+      weights(half_tok, acc, b);
+      values(0, b, half_mask);
+      values(1, b, ~half_mask);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        logits(u, 0, acc, true);
+        weights(16 * u + tok, acc, b);
+        values(u, b, kFull);
+      }
     }
 
     // ---- the segment or this worker's share of it is done
-    const bool last = cur.unit + 1 == cur.span.units;
-    if (last || i + 1 == count) {
+    const bool last = now.w & 2;
+    if (last || count == 1) {
       fresh = true;
-      const int head = cur.head, pass = cur.pass;
-      const bool whole = last && seg_first == 0;
-      float* part = a.parts + ((int64_t)worker * 2 + (seg_first == 0 ? 1 : 0)) * NQ * (D + 2);
+      const int head = now.z >> 16, pass = now.z & 0xffff;
+      const bool whole = last && from_start;
+      float* part = a.parts + ((int64_t)worker * 2 + (from_start ? 1 : 0)) * NQ * (D + 2);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -552,15 +645,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
           float l = sum[n][k];
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
+          if (kPack) {  // columns 4.. are the same heads, over the other half of the tokens
+            const float other = __shfl_xor_sync(kFull, ref[n][k], 2);
+            const float top = fmaxf(ref[n][k], other), f = ex2(ref[n][k] - top);
+            l *= f;
+            l += __shfl_xor_sync(kFull, l, 2);
+            ref[n][k] = top;
+#pragma unroll
+            for (int m = 0; m < 2 * G; ++m)
+#pragma unroll
+              for (int i = k; i < 4; i += 2) {
+                o[n][m][i] *= f;
+                o[n][m][i] += __shfl_xor_sync(kFull, o[n][m][i], 2);
+              }
+          }
           const int qi = 8 * n + 2 * t + k;  // in this pass
-          if (pass * NQ + qi >= a.group) continue;
+          if (qi >= NQ || pass * NQ + qi >= a.group) continue;
           if (whole) {
-            const float inv = l == 0.f ? 0.f : kCodeScale / l;
+            const float inv = l == 0.f ? 0.f : kCentred / l;
             __nv_bfloat16* out =
-                a.out + ((int64_t)cur.r * a.q_heads + head * a.group + pass * NQ + qi) * D;
+                a.out + ((int64_t)now.y * a.q_heads + head * a.group + pass * NQ + qi) * D;
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-              const __nv_bfloat162 p0 = __floats2bfloat162_rn(o[n][2 * j][k] * inv, o[n][2 * j][k + 2] * inv);
+              const __nv_bfloat162 p0 =
+                  __floats2bfloat162_rn(o[n][2 * j][k] * inv, o[n][2 * j][k + 2] * inv);
               const __nv_bfloat162 p1 =
                   __floats2bfloat162_rn(o[n][2 * j + 1][k] * inv, o[n][2 * j + 1][k + 2] * inv);
               *reinterpret_cast<uint2*>(out + 32 * j + 4 * g) =
@@ -578,7 +686,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
           }
         }
     }
-    cur.next(a);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   report(a.err, err);
@@ -587,9 +694,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) attention_q4_kernel
 // Join: out = sum_i 2^(ref_i - top) o_i / sum_i 2^(ref_i - top) l_i over the parts the
 // workers left of one (request, query head).  Its warps take the parts in turn, each
 // lane D / 32 channels; which worker holds which part follows from the offsets alone.
-template <int G, int NT>
+template <int G, int NQ>
 __global__ void __launch_bounds__(256) join_q4_kernel(AttnArgs a) {
-  constexpr int D = 32 * G, NQ = 8 * NT;
+  constexpr int D = 32 * G;
   __shared__ float s_o[8][D], s_l[8], s_top[8];
   pdl_allow_next();
   pdl_wait();
@@ -638,21 +745,20 @@ __global__ void __launch_bounds__(256) join_q4_kernel(AttnArgs a) {
       for (int j = 0; j < G; ++j) acc[j] += s_o[w][32 * j + lane];
     }
   }
-  const float inv = l == 0.f ? 0.f : kCodeScale / l;
+  const float inv = l == 0.f ? 0.f : kCentred / l;
 #pragma unroll
   for (int j = 0; j < G; ++j)
     a.out[((int64_t)r * a.q_heads + qh) * D + 32 * j + lane] = __float2bfloat16_rn(acc[j] * inv);
 }
 
-// Query heads a warp takes at once: 8, or 16 where a KV head has more than 8 (the cache is
-// read once for both halves).
-int columns(int group) { return group > 8 ? 16 : 8; }
-int worker_count(int group) { return sm_count() * (group > 8 ? 3 : 4) * kWarps; }
+// Query heads a warp takes at once: 4, 8, or 16 (the cache is read once for all of them).
+int columns(int group) { return group > 8 ? 16 : group > 4 ? 8 : 4; }
+int worker_count() { return sm_count() * kCtas * kWarps; }
 int64_t offsets_bytes(int32_t num_reqs) { return ((int64_t)(num_reqs + 1) * 8 + 127) / 128 * 128; }
 
-template <int G, int NT>
+template <int G, int NQ>
 int launch(const AttnArgs& a, cudaStream_t stream) {
-  auto kernel = attention_q4_kernel<G, NT>;
+  auto kernel = attention_q4_kernel<G, NQ == 16 ? 2 : 1, NQ == 4>;
   constexpr int smem = kWarps * kStages * Stage<G>::kBytes;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
@@ -662,7 +768,16 @@ int launch(const AttnArgs& a, cudaStream_t stream) {
   // a row has about workers / (requests x KV heads) parts: more warps where that is long
   const int64_t rows = (int64_t)a.num_reqs * a.q_heads;
   const int warps = rows >= 2048 ? 1 : rows >= 512 ? 4 : 8;
-  return launch_pdl(join_q4_kernel<G, NT>, (unsigned)rows, 32 * warps, 0, stream, a);
+  return launch_pdl(join_q4_kernel<G, NQ>, (unsigned)rows, 32 * warps, 0, stream, a);
+}
+
+template <int G>
+int launch(const AttnArgs& a, cudaStream_t stream) {
+  switch (columns(a.group)) {
+    case 4: return launch<G, 4>(a, stream);
+    case 8: return launch<G, 8>(a, stream);
+    default: return launch<G, 16>(a, stream);
+  }
 }
 
 }  // namespace
@@ -679,7 +794,7 @@ extern "C" int64_t kv_attention_q4_workspace(int32_t num_reqs, int32_t num_q_hea
     return KV_EUNSUPPORTED;
   const int group = num_q_heads / num_kv_heads;
   return offsets_bytes(num_reqs) +
-         (int64_t)worker_count(group) * 2 * columns(group) * (head_dim + 2) * 4;
+         (int64_t)worker_count() * 2 * columns(group) * (head_dim + 2) * 4;
 }
 
 extern "C" int kv_attention_q4(const void* query, int64_t query_stride, const void* k_cache,
@@ -712,15 +827,20 @@ extern "C" int kv_attention_q4(const void* query, int64_t query_stride, const vo
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
     return KV_EINVAL;
   const int group = num_q_heads / num_kv_heads;
+  const Q4Layout at{0, num_blocks, block_size, num_kv_heads, head_dim};
+  // the kernel addresses a layer in 16-byte pieces of 32 bits
+  const int64_t block_bytes = at.record_bytes() * num_kv_heads;
+  if (num_blocks > ((int64_t)1 << 36) / block_bytes) return KV_EUNSUPPORTED;
+  const int64_t layer_at = layer * num_blocks * block_bytes;
   AttnArgs a{static_cast<const __nv_bfloat16*>(query), query_stride,
-             static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
-             Q4Layout{(int64_t)layer * num_blocks, num_blocks, block_size, num_kv_heads, head_dim},
+             static_cast<const uint8_t*>(k_cache) + layer_at,
+             static_cast<const uint8_t*>(v_cache) + layer_at, at,
+             (int32_t)(num_blocks < INT32_MAX ? num_blocks : INT32_MAX),
              BlockDiv::make(block_size), block_table, table_stride, span_start, span_end, num_reqs,
              num_q_heads, group, (group + columns(group) - 1) / columns(group),
-             worker_count(group), scale * 1.44269504088896340736f,
+             worker_count(), scale * 1.44269504088896340736f,
              static_cast<__nv_bfloat16*>(out), static_cast<int64_t*>(workspace),
              reinterpret_cast<float*>(static_cast<char*>(workspace) + offsets_bytes(num_reqs)),
              d_err};
-  if (head_dim == 128) return group > 8 ? launch<4, 2>(a, stream) : launch<4, 1>(a, stream);
-  return group > 8 ? launch<2, 2>(a, stream) : launch<2, 1>(a, stream);
+  return head_dim == 128 ? launch<4>(a, stream) : launch<2>(a, stream);
 }

@@ -16,14 +16,16 @@
 // GPU shape.  The bytes of the cache bound this: 16 query rows at most read each of
 // them, far under a matrix unit tile of 128 rows, so the products go through the warp's
 // own m16n8k16 instruction with tokens (of K) or channels (of V) as its 16 rows and the
-// group's query heads as its 8 columns.  Every warp is a worker of its own:
-// all positions of all (request, KV head) are cut into units of 32 tokens, and worker i
-// takes the units [i C, (i+1) C) whatever requests they belong to, so every worker reads
-// the same number of bytes however long the contexts are.  Its units come through a ring
-// of kStages in shared memory, filled with cp.async by table lookups made one unit ahead,
-// and nothing but the warp itself waits for them.  A worker
-// whose range ends inside a (request, head) leaves its sums in the workspace; a second
-// kernel joins those.
+// group's query heads as its 8 columns.  The positions of all requests are cut into units of
+// 32, and the warps into gangs of one warp per KV head (at most 16): gang i takes the units
+// [i C, (i+1) C) whatever requests they belong to, so every warp reads the same number of
+// bytes however long the contexts are, and the heads of a block, which lie side by side in
+// memory, are read at about the same time (a warp per equal share of all (head, position)
+// instead: the loads alone took 237 us for 1.2 GB, DRAM pages being opened once per head).
+// A warp's units come through a ring of kStages in shared memory, filled with cp.async by
+// table lookups made a window of 8 units ahead, and nothing but the warp itself waits for them.  A warp
+// whose range ends inside a (request, head) leaves its sums in the workspace; a second kernel
+// joins those.
 //
 // Layout of a unit in shared memory.  Row rho of the K product's 16 is token pi(rho) =
 // (rho >> 1) + 4 (rho & 1): its transpose then gives lane t the tokens t, t + 4, t + 8,
@@ -41,6 +43,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kCtas = 3;                  // per SM: 12 warps of 168 registers
 constexpr int kStages = 4;
 constexpr int kUnit = 32;                 // tokens of a unit
+constexpr int kWindow = 8 * kUnit;        // tokens of a table lookup
 constexpr float kRefStart = -1e30f;       // below every logit, and finite
 constexpr float kLimit = 256.0f;          // a weight times its scale above this raises the reference
 constexpr float kUnitMin = 7.888609e-31f, kUnitMax = 1.2676506e30f;  // 2^-100, 2^100
@@ -58,8 +61,9 @@ struct AttnArgs {
   const int32_t* start;
   const int32_t* end;
   int32_t num_reqs, q_heads, group;
-  int32_t passes;   // groups of 8 NT query heads per KV head
-  int32_t workers;
+  int32_t passes;   // groups of NQ query heads per KV head
+  int32_t gang;     // warps that take the same positions of neighbouring (KV head, pass)
+  int32_t gangs;
   float scale_log2;
   __nv_bfloat16* out;
   int64_t* offsets;  // [num_reqs + 1] units before each request (written by CTA 0)
@@ -122,18 +126,9 @@ __device__ __forceinline__ void codes_centred(uint32_t x, uint32_t (&f)[4]) {
     f[n] = *reinterpret_cast<const uint32_t*>(&a);
   }
 }
-// src_bytes 0 writes zeros and reads nothing.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
-               "r"(src_bytes)
-               : "memory");
-}
-
 // The G bf16 scales of a token.
 template <int G>
 __device__ __forceinline__ void load_scales(const unsigned char* p, float (&f)[G]) {
@@ -179,35 +174,33 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int r, uint32_t& err)
   s.units = any ? (s.hi - 1) / kUnit - s.first + 1 : 0;
   return s;
 }
-// The unit a worker loads next: positions [p, p + 32) of request r, for head `head`, pass
-// `pass`; `left` units of this (request, head, pass) are still to load, this one included.
+// The unit a worker loads next: positions [p, p + 32) of request r for seg = head * passes +
+// pass; `left` units of this (request, seg) are still to load, this one included.
 struct Cursor {
-  int r, head, pass, left;
+  int r, seg, left;
   int32_t p;
   Span span;
-  __device__ __forceinline__ void next(const AttnArgs& a) {
+  // Steps to the next unit; true when that is the first of another segment.
+  __device__ __forceinline__ bool next(const AttnArgs& a, int segs) {
     p += kUnit;
-    if (--left == 0) next_segment(a);
-  }
-  __device__ __forceinline__ void next_segment(const AttnArgs& a) {
-    if (++pass == a.passes) {
-      pass = 0;
-      if (++head == a.at.kv_heads) {
-        head = 0;
-        uint32_t ignore = 0;
-        do {
-          if (++r >= a.num_reqs) {  // behind the last unit: not loaded
-            left = 1;
-            p = 0;
-            span.lo = span.hi = 0;
-            return;
-          }
-          span = span_of(a, r, ignore);
-        } while (span.units == 0);
-      }
+    if (--left > 0) return false;
+    seg += a.gang;
+    if (seg >= segs) {
+      seg %= a.gang;
+      uint32_t ignore = 0;
+      do {
+        if (++r >= a.num_reqs) {  // behind the last unit: not loaded
+          left = 1;
+          p = 0;
+          span.lo = span.hi = 0;
+          return true;
+        }
+        span = span_of(a, r, ignore);
+      } while (span.units == 0);
     }
     left = span.units;
     p = span.first * kUnit;
+    return true;
   }
 };
 
@@ -224,11 +217,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
   __shared__ int64_t s_before[kThreads];  // units before each thread's share of the requests
   __shared__ int64_t s_warp[kWarps];
   __shared__ int64_t s_total;
-  // per unit in the ring: positions that count; request; head << 16 | pass; 1: first of its
-  // segment, 2: last
+  // per unit in the ring: positions that count; request; seg; 1: first of its segment, 2: last
   __shared__ int4 s_unit[kWarps][kStages];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = a.at.kv_heads, segs = H * a.passes;
+  const int rounds = segs / a.gang;  // times a gang goes over a request's positions
   pdl_allow_next();
   pdl_wait();
 
@@ -239,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
     const int r_lo = min(a.num_reqs, tid * per), r_hi = min(a.num_reqs, r_lo + per);
     uint32_t span_err = 0;
     int64_t mine = 0;
-    for (int r = r_lo; r < r_hi; ++r) mine += (int64_t)span_of(a, r, span_err).units * segs;
+    for (int r = r_lo; r < r_hi; ++r) mine += (int64_t)span_of(a, r, span_err).units * rounds;
     if (blockIdx.x == 0) err |= span_err;
     const int64_t incl = warp_inclusive_scan<int64_t>(mine);
     if (lane == 31) s_warp[warp] = incl;
@@ -253,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
       int64_t at = before;
       for (int r = r_lo; r < r_hi; ++r) {
         a.offsets[r] = at;
-        at += (int64_t)span_of(a, r, ignore).units * segs;
+        at += (int64_t)span_of(a, r, ignore).units * rounds;
       }
       if (tid == kThreads - 1) a.offsets[a.num_reqs] = at;
     }
@@ -261,16 +254,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
   }
   const int worker = blockIdx.x * kWarps + warp;
   // requests without a position: zeros
-  for (int r = worker; r < a.num_reqs; r += a.workers) {
+  for (int r = worker; r < a.num_reqs; r += gridDim.x * kWarps) {
     uint32_t ignore = 0;
     if (span_of(a, r, ignore).units > 0) continue;
     uint4* o = reinterpret_cast<uint4*>(a.out + (int64_t)r * a.q_heads * D);
     for (int i = lane; i < a.q_heads * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
   }
   const int64_t total = s_total;
-  const int64_t share = (total + a.workers - 1) / a.workers;
-  const int64_t first = worker * share;
-  if (first >= total) {
+  const int64_t share = (total + a.gangs - 1) / a.gangs;
+  const int my_gang = worker / a.gang;
+  const int64_t first = my_gang * share;
+  if (my_gang >= a.gangs || first >= total) {
     report(a.err, err);
     return;
   }
@@ -288,18 +282,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
     int64_t at = s_before[lo];
     uint32_t ignore = 0;
     load.span = span_of(a, r, ignore);
-    while (at + (int64_t)load.span.units * segs <= first) {
-      at += (int64_t)load.span.units * segs;
+    while (at + (int64_t)load.span.units * rounds <= first) {
+      at += (int64_t)load.span.units * rounds;
       load.span = span_of(a, ++r, ignore);
     }
     const int64_t rest = first - at;
-    const int seg = (int)(rest / load.span.units);
-    const int unit = (int)(rest - (int64_t)seg * load.span.units);
+    const int round = (int)(rest / load.span.units);
+    const int unit = (int)(rest - (int64_t)round * load.span.units);
     load.r = r;
+    load.seg = round * a.gang + (worker - my_gang * a.gang);
     load.left = load.span.units - unit;
     load.p = (load.span.first + unit) * kUnit;
-    load.head = seg / a.passes;
-    load.pass = seg - load.head * a.passes;
   }
 
   const int g = lane >> 2, t = lane & 3;
@@ -312,64 +305,97 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
                          (2 * (piece_tok & 3) + ((piece_tok >> 2) & 1) + (piece_tok & 8)) * (16 * G);
   const uint32_t v_dst = ring + S::kCodes + piece_tok * (16 * G) +
                          16 * (G == 4 ? piece_c ^ (2 * ((piece_tok >> 1) & 1)) : piece_c);
-  const uint32_t s_dst = ring + 2 * S::kCodes + lane * (2 * G);
+  const uint32_t s_dst = ring + 2 * S::kCodes + lane * 16;
   const int T = a.at.block_size;
+  const int step_off = kUnit % T;
   const uint32_t rec16 = (uint32_t)(T / 8) * (9 * G);  // T (16 G + 2 G) / 16
+  const uint32_t block16 = rec16 * (uint32_t)H;
 
-  // ---- loads.  Lane l stands for run l & 3: 8 positions of the unit, in one block.  The
-  // block is looked up one unit ahead.
-  int32_t nb;     // the run's block, or null
-  int32_t n_off;  // its first token in the block
-  auto look_up = [&]() {
-    const int32_t run = load.p + 8 * (lane & 3);
-    nb = kNull;
-    int64_t lb, off;
-    a.div.divmod(run, lb, off);
-    n_off = (int32_t)off;
-    if (run < load.span.hi && run + 7 >= load.span.lo) nb = a.table[(int64_t)load.r * a.stride + lb];
+  // ---- loads.  Blocks are looked up for 8 units at once, lane l for positions 8 l .. 8 l + 7
+  // of the window, and one window ahead: a unit's copies never wait for its table entry.
+  // Offsets are in 16-byte pieces of the layer (32 bits: checked on the host); the codes of 8
+  // tokens are 8 G pieces, their scales G.
+  const uint8_t* const k_lane = a.k_cache + 16 * (G == 4 ? lane : lane & 15);
+  const int64_t k_to_v = a.v_cache - a.k_cache;
+  const uint8_t* const s_lane = (lane < 4 * G ? a.k_cache : a.v_cache) + 16 * (lane % G);
+  const int s_run = lane % (4 * G) / G;
+  int32_t window, blocks, blocks_next;
+  int32_t off;       // first token of run lane & 3 in its block
+  uint32_t head_at;  // the head's record in a block
+  auto look_up = [&](int32_t from) {
+    const int64_t run = (int64_t)from + 8 * lane;
+    if (run >= load.span.hi || run + 7 < load.span.lo) return kNull;
+    int64_t lb, ignore;
+    a.div.divmod(run, lb, ignore);
+    return a.table[(int64_t)load.r * a.stride + lb];
+  };
+  auto open_segment = [&]() {
+    window = load.p;
+    blocks = look_up(window);
+    blocks_next = look_up(window + kWindow);
+    int64_t lb, first_off;
+    a.div.divmod((int64_t)load.p + 8 * (lane & 3), lb, first_off);
+    off = (int32_t)first_off;
+    head_at = (uint32_t)(load.seg / a.passes) * rec16;
   };
   auto issue = [&](int stage) {
-    // offsets in 16-byte pieces of the layer (32 bits: checked on the host); a run's codes are
-    // 8 G pieces, its scales G
-    const bool valid = nb > kNull && nb < a.num_blocks32;
-    const uint32_t runs = __ballot_sync(kFull, valid) & 15u;
-    const uint32_t rec = valid ? ((uint32_t)nb * (uint32_t)H + (uint32_t)load.head) * rec16 : 0u;
-    const uint32_t off = valid ? (uint32_t)n_off : 0u;
-    const uint32_t codes = rec + off * G, scales = rec + (uint32_t)T * G + (off >> 3) * G;
+    if (load.p - window >= kWindow) {
+      window += kWindow;
+      blocks = blocks_next;
+      blocks_next = look_up(window + kWindow);
+    }
+    // lane l stands for run l & 3 of the unit
+    const int32_t nb = __shfl_sync(kFull, blocks, (load.p - window) / 8 + (lane & 3));
+    const uint32_t runs =
+        __ballot_sync(kFull, (uint32_t)nb - 1u < (uint32_t)a.num_blocks32 - 1u) & 15u;
+    const uint32_t rec = (uint32_t)nb * block16 + head_at;
+    const uint32_t codes = rec + (uint32_t)off * G;
+    const uint32_t scales = rec + (uint32_t)T * G + (uint32_t)(off >> 3) * G;
+    const uint32_t at = stage * S::kBytes;
     uint32_t mask = kFull;
-    if (runs != 15u || load.p < load.span.lo || load.p + kUnit - 1 >= load.span.hi) {
-      if (!valid && nb != kNull) err |= KV_ERR_BAD_BLOCK;
+    if (runs == 15u && load.p >= load.span.lo && load.p + kUnit - 1 < load.span.hi) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {  // 32 / G tokens each: lane's piece is 16 lane bytes into them
+        const uint32_t c = __shfl_sync(kFull, codes, G == 4 ? i : 2 * i + (lane >> 4));
+        const uint8_t* src = k_lane + (uint64_t)c * 16;
+        copy16(k_dst + at + i * 512, src);
+        copy16(v_dst + at + i * 512, src + k_to_v);
+      }
+      // scales: K's by the first 4 G lanes, V's by the next, 16 bytes each like the codes
+      const uint32_t c = __shfl_sync(kFull, scales, s_run);
+      if (G == 4 || lane < 8 * G) copy16(s_dst + at, s_lane + (uint64_t)c * 16);
+    } else {  // a span's edge, or a run without a block: nothing is read for that run
+      if (!((runs >> (lane & 3)) & 1u) && nb != kNull) err |= KV_ERR_BAD_BLOCK;
       // 4 validity bits of the runs, each spread over its 8 positions
       mask = ((runs * 0x00204081u) & 0x01010101u) * 0xffu;
       const int32_t skip = load.span.lo - load.p, stop = load.span.hi - load.p;
       if (skip > 0) mask &= kFull << skip;
       if (stop < kUnit) mask &= stop > 0 ? (1u << stop) - 1u : 0u;
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int run = G == 4 ? i : 2 * i + (lane >> 4);
+        const uint32_t c = __shfl_sync(kFull, codes, run);
+        const uint8_t* src = k_lane + (uint64_t)c * 16;
+        if ((runs >> run) & 1u) {
+          copy16(k_dst + at + i * 512, src);
+          copy16(v_dst + at + i * 512, src + k_to_v);
+        }
+      }
+      const uint32_t c = __shfl_sync(kFull, scales, s_run);
+      if ((G == 4 || lane < 8 * G) && ((runs >> s_run) & 1u))
+        copy16(s_dst + at, s_lane + (uint64_t)c * 16);
     }
     if (lane == 0)
-      s_unit[warp][stage] = make_int4((int)mask, load.r, load.head << 16 | load.pass,
+      s_unit[warp][stage] = make_int4((int)mask, load.r, load.seg,
                                       (load.p == load.span.first * kUnit ? 1 : 0) |
                                           (load.left == 1 ? 2 : 0));
-    const uint32_t at = stage * S::kBytes;
-#pragma unroll
-    for (int i = 0; i < G; ++i) {  // 32 / G tokens each: lane's piece is 16 lane bytes into them
-      const int run = G == 4 ? i : 2 * i + (lane >> 4);
-      const uint64_t src =
-          (uint64_t)(__shfl_sync(kFull, codes, run) + (G == 4 ? lane : lane & 15)) * 16;
-      const uint32_t bytes = (runs >> run) & 1u ? 16u : 0u;
-      copy16(k_dst + at + i * 512, a.k_cache + src, bytes);
-      copy16(v_dst + at + i * 512, a.v_cache + src, bytes);
-    }
-    const uint64_t sc =
-        (uint64_t)__shfl_sync(kFull, scales, lane >> 3) * 16 + (lane & 7) * (2 * G);
-    const uint32_t bytes = (runs >> (lane >> 3)) & 1u ? 2 * G : 0;
-    copy_small<2 * G>(s_dst + at, a.k_cache + sc, bytes);
-    copy_small<2 * G>(s_dst + at + S::kScales, a.v_cache + sc, bytes);
-    load.next(a);
-    look_up();
+    off += step_off;
+    if (off >= T) off -= T;
+    if (load.next(a, segs)) open_segment();
   };
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
-  look_up();
+  open_segment();
   int64_t to_load = count;
 #pragma unroll 1
   for (int s = 0; s < kStages - 1; ++s) {
@@ -406,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
     if (fresh) {  // a new (request, head, pass)
       fresh = false;
       from_start = now.w & 1;
-      const int head = now.z >> 16, pass = now.z & 0xffff;
+      const int head = now.z / a.passes, pass = now.z - head * a.passes;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int qi = pass * NQ + 8 * n + (kPack ? g & 3 : g);
@@ -524,7 +550,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
 #pragma unroll
           for (int j = 1; j < G; ++j) s[n][k] = fmaf(acc[j][n][k], ks[k >> 1][j], s[n][k]);
         }
-      if (__any_sync(kFull, mask != kFull)) {  // hidden positions: no weight, any scale
+      // hidden positions: no weight, and whatever bits the ring holds as scales (codes are finite
+      // whatever they are)
+      if (mask != kFull) {
+        asm volatile("" ::: "memory");  // a branch: as selects it cost 30 instructions in every unit
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (!((mask >> (first_tok + 8 * h)) & 1u)) {
@@ -635,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
     const bool last = now.w & 2;
     if (last || count == 1) {
       fresh = true;
-      const int head = now.z >> 16, pass = now.z & 0xffff;
+      const int head = now.z / a.passes, pass = now.z - head * a.passes;
       const bool whole = last && from_start;
       float* part = a.parts + ((int64_t)worker * 2 + (from_start ? 1 : 0)) * NQ * (D + 2);
 #pragma unroll
@@ -702,18 +731,21 @@ __global__ void __launch_bounds__(256) join_q4_kernel(AttnArgs a) {
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int r = blockIdx.x / a.q_heads, qh = blockIdx.x - r * a.q_heads;
-  const int segs = a.at.kv_heads * a.passes;
+  const int rounds = a.at.kv_heads * a.passes / a.gang;
   const int64_t at = a.offsets[r], total = a.offsets[a.num_reqs];
-  const int64_t units = (a.offsets[r + 1] - at) / segs;
-  const int64_t share = (total + a.workers - 1) / a.workers;
+  const int64_t units = (a.offsets[r + 1] - at) / rounds;
+  const int64_t share = (total + a.gangs - 1) / a.gangs;
   if (units == 0) return;  // zeros, already written
   const int head = qh / a.group, qi = qh - head * a.group;
-  const int64_t lo = at + (int64_t)(head * a.passes + qi / NQ) * units;
+  const int seg = head * a.passes + qi / NQ, round = seg / a.gang;
+  const int64_t lo = at + round * units;
   const int64_t i0 = lo / share, i1 = (lo + units - 1) / share;
   if (i0 == i1) return;    // one worker saw it whole
   const float* parts = a.parts + (int64_t)(qi % NQ) * (D + 2);
   constexpr int64_t kPart = NQ * (D + 2);
-  auto part = [&](int64_t i) { return parts + (2 * i + (i == i0 ? 1 : 0)) * kPart; };
+  auto part = [&](int64_t i) {
+    return parts + (2 * (i * a.gang + (seg - round * a.gang)) + (i == i0 ? 1 : 0)) * kPart;
+  };
 
   float top = kRefStart;
   for (int64_t i = i0 + threadIdx.x; i <= i1; i += blockDim.x) top = fmaxf(top, part(i)[D]);
@@ -754,6 +786,12 @@ __global__ void __launch_bounds__(256) join_q4_kernel(AttnArgs a) {
 // Query heads a warp takes at once: 4, 8, or 16 (the cache is read once for all of them).
 int columns(int group) { return group > 8 ? 16 : group > 4 ? 8 : 4; }
 int worker_count() { return sm_count() * kCtas * kWarps; }
+// The largest divisor of the (KV head, pass) pairs up to 16.
+int gang_size(int segs) {
+  int g = segs < 16 ? segs : 16;
+  while (segs % g != 0) --g;
+  return g;
+}
 int64_t offsets_bytes(int32_t num_reqs) { return ((int64_t)(num_reqs + 1) * 8 + 127) / 128 * 128; }
 
 template <int G, int NQ>
@@ -763,7 +801,7 @@ int launch(const AttnArgs& a, cudaStream_t stream) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return KV_ECUDA;
-  const int rc = launch_pdl(kernel, a.workers / kWarps, kThreads, smem, stream, a);
+  const int rc = launch_pdl(kernel, worker_count() / kWarps, kThreads, smem, stream, a);
   if (rc != KV_OK) return rc;
   // a row has about workers / (requests x KV heads) parts: more warps where that is long
   const int64_t rows = (int64_t)a.num_reqs * a.q_heads;
@@ -827,6 +865,8 @@ extern "C" int kv_attention_q4(const void* query, int64_t query_stride, const vo
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
     return KV_EINVAL;
   const int group = num_q_heads / num_kv_heads;
+  const int passes = (group + columns(group) - 1) / columns(group);
+  const int gang = gang_size(num_kv_heads * passes);
   const Q4Layout at{0, num_blocks, block_size, num_kv_heads, head_dim};
   // the kernel addresses a layer in 16-byte pieces of 32 bits
   const int64_t block_bytes = at.record_bytes() * num_kv_heads;
@@ -837,8 +877,7 @@ extern "C" int kv_attention_q4(const void* query, int64_t query_stride, const vo
              static_cast<const uint8_t*>(v_cache) + layer_at, at,
              (int32_t)(num_blocks < INT32_MAX ? num_blocks : INT32_MAX),
              BlockDiv::make(block_size), block_table, table_stride, span_start, span_end, num_reqs,
-             num_q_heads, group, (group + columns(group) - 1) / columns(group),
-             worker_count(), scale * 1.44269504088896340736f,
+             num_q_heads, group, passes, gang, worker_count() / gang, scale * 1.44269504088896340736f,
              static_cast<__nv_bfloat16*>(out), static_cast<int64_t*>(workspace),
              reinterpret_cast<float*>(static_cast<char*>(workspace) + offsets_bytes(num_reqs)),
              d_err};

@@ -66,9 +66,9 @@ struct Smem {
   static constexpr int kBars = kRing + kSlots * kTileBytes;
   // an edge tile's slot is not used again (it would have to be kSlots loads later)
   static_assert(kSlots >= 2 * kEdges - 1, "");
-  // full[slots], empty[slots], edge[3], v_ok[3], q_full, s_full[2], p_full[2], o_full[2], scrubbed,
-  // drain
-  static constexpr int kNumBars = 2 * kSlots + 2 * kEdges + 9;
+  // full[slots], empty[slots], edge[3], v_ok[3], q_full, s_full[2], p_full[2][2], o_full[2],
+  // scrubbed, drain
+  static constexpr int kNumBars = 2 * kSlots + 2 * kEdges + 11;
   static constexpr int kBad = kBars + kNumBars * 8;         // int[DP]: first key not finite
   static constexpr int kMisc = kBad + DP * 4;
   static constexpr int kBytes = kMisc + 64 + 1024;          // + alignment of the base
@@ -90,6 +90,31 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -106,7 +131,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   uint64_t* q_full = v_ok + kEdges;
   uint64_t* s_full = q_full + 1;
   uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
+  uint64_t* o_full = p_full + 4;
   uint64_t* scrubbed = o_full + 2;
   uint64_t* drain = scrubbed + 1;
   int* bad = reinterpret_cast<int*>(smem + L::kBad);
@@ -115,7 +140,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   volatile int* abort = misc + 1;
   int* any_bad = misc + 2;
   Work* s_work = reinterpret_cast<Work*>(misc + 4);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform for the compiler, too
 
   if (tid == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
@@ -129,7 +155,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     mbar_init(q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kTile);
+      mbar_init(&p_full[2 * i], kTile / 32);  // the first 64 keys' weights, one arrival a warp
+      mbar_init(&p_full[2 * i + 1], kTile / 32);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(scrubbed, kScrubThreads);
@@ -180,7 +207,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     __syncthreads();
     if (blockIdx.x == 0) report(a.err, err);
   }
-  const Work w = *s_work;
+  Work w = *s_work;  // the same in every lane: tell the compiler
+  w.q0 = __shfl_sync(kFull, w.q0, 0);
+  w.k0 = __shfl_sync(kFull, w.k0, 0);
+  w.m = __shfl_sync(kFull, w.m, 0);
+  w.n = __shfl_sync(kFull, w.n, 0);
+  w.t0 = __shfl_sync(kFull, w.t0, 0);
   const int ahead = w.n - w.m;                                    // keys before the first query's own
   const int last = min(w.t0 + 2 * a.tq, w.m) - 1;                 // last token here
   const int keys = max(0, min(w.n, ahead + last + 1));            // keys the last token sees
@@ -191,7 +223,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_ptr;
+  const uint32_t tmem = __shfl_sync(kFull, *tmem_ptr, 0);
 
   if (w.m > 0 && tiles == 0) {  // no query here sees a key
     const int64_t row = (int64_t)a.group * a.head_dim;
@@ -205,29 +237,36 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8 && lane == 0 && work) {
+    if (warp == 8 && work) {
       // -------------------------------------------------------------- TMA
-      tma_prefetch_map(&q_map);
-      tma_prefetch_map(&k_map);
-      tma_prefetch_map(&v_map);
-      const uint32_t q_bytes = (uint32_t)(a.group * a.tq) * 128u * (DP / 64);
-      mbar_arrive_expect_tx(q_full, two ? 2 * q_bytes : q_bytes);
-      for (int t = 0; t < (two ? 2 : 1); ++t)
-        for (int c = 0; c < DP / 64; ++c)
-          tma_load_3d(smem + L::kQ + t * L::kTileBytes + c * (kTile * 128), &q_map, 64 * c,
-                      head * a.group, w.q0 + w.t0 + t * a.tq, q_full);
-      int u = 0;  // K and V tiles alternate in the ring
+      const bool leader = elect_one();
+      if (leader) {
+        tma_prefetch_map(&q_map);
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
+        const uint32_t q_bytes = (uint32_t)(a.group * a.tq) * 128u * (DP / 64);
+        mbar_arrive_expect_tx(q_full, two ? 2 * q_bytes : q_bytes);
+        for (int t = 0; t < (two ? 2 : 1); ++t)
+          for (int c = 0; c < DP / 64; ++c)
+            tma_load_3d(smem + L::kQ + t * L::kTileBytes + c * (kTile * 128), &q_map, 64 * c,
+                        head * a.group, w.q0 + w.t0 + t * a.tq, q_full);
+      }
+      int u = 0, slot = 0, turn = 0;  // K and V tiles alternate in the ring
+#pragma unroll 1
       for (; u < 2 * tiles; ++u) {
-        const int slot = u % L::kSlots;
-        if (u >= L::kSlots &&
-            !mbar_wait_role(&empty[slot], ((u / L::kSlots) - 1) & 1, abort))
-          break;
+        if (turn > 0 && !mbar_wait_role(&empty[slot], (turn - 1) & 1, abort)) break;
         const bool is_v = u & 1;
         uint64_t* bar = is_v && (u >> 1) >= whole ? &edge[(u >> 1) - whole] : &full[slot];
-        mbar_arrive_expect_tx(bar, L::kTileBytes);
-        for (int c = 0; c < DP / 64; ++c)
-          tma_load_3d(smem + L::kRing + slot * L::kTileBytes + c * (kTile * 128),
-                      is_v ? &v_map : &k_map, 64 * c, head, w.k0 + (u >> 1) * kTile, bar);
+        if (leader) {
+          mbar_arrive_expect_tx(bar, L::kTileBytes);
+          for (int c = 0; c < DP / 64; ++c)
+            tma_load_3d(smem + L::kRing + slot * L::kTileBytes + c * (kTile * 128),
+                        is_v ? &v_map : &k_map, 64 * c, head, w.k0 + (u >> 1) * kTile, bar);
+        }
+        if (++slot == L::kSlots) {
+          slot = 0;
+          ++turn;
+        }
       }
       if (*abort != 0) {  // bounded wait for the copies still in flight
         mbar_wait_bounded(q_full, 0);
@@ -236,52 +275,82 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
           else mbar_wait_bounded(&full[x % L::kSlots], (x / L::kSlots) & 1);
         }
       }
-    } else if (warp == 9 && lane == 0 && work) {
+    } else if (warp == 9 && work) {
       // -------------------------------------------------------------- matrix instructions
       constexpr uint32_t s_desc = mma_desc(128, kTile, false), o_desc = mma_desc(128, DP, true);
-      const uint32_t q_at = smem_addr(smem + L::kQ), ring = smem_addr(smem + L::kRing);
+      constexpr uint32_t kSlotStep = L::kTileBytes >> 4;  // descriptors count 16 bytes
+      const uint64_t q_at = smem_desc(smem_addr(smem + L::kQ), 16);
+      const uint64_t k_at = smem_desc(smem_addr(smem + L::kRing), 16);
+      const uint64_t v_at = smem_desc(smem_addr(smem + L::kRing), kTile * 128);
+      const bool leader = elect_one();
       auto scores = [&](int t, int slot) {
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t off = (k / 4) * (kTile * 128) + (k % 4) * 32;
-          mma_ss(tmem + t * kTile, smem_desc(q_at + t * L::kTileBytes + off, 16),
-                 smem_desc(ring + slot * L::kTileBytes + off, 16), s_desc, k > 0);
+        const uint64_t qd = q_at + t * kSlotStep, kd = k_at + slot * kSlotStep;
+        const uint32_t d = tmem + t * kTile;
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t off = ((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+            mma_ss(d, qd + off, kd + off, s_desc, k > 0);
+          }
+          mma_commit(&s_full[t]);
         }
-        mma_commit(&s_full[t]);
       };
-      auto values = [&](int t, int slot, bool add) {
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + 2 * kTile + t * DP, tmem + t * kTile + k * 8,
-                 smem_desc(ring + slot * L::kTileBytes + k * 2048, kTile * 128), o_desc, add || k > 0);
+      auto values = [&](int t, int slot, bool add, int half) {
+        const uint64_t vd = v_at + slot * kSlotStep + half * ((kTile / 2 * 128) >> 4);
+        const uint32_t d = tmem + 2 * kTile + t * DP, p = tmem + t * kTile + half * (kTile / 4);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_ts(d, p + k * 8, vd + k * (2048 >> 4), o_desc, add || k > 0);
+        }
       };
       const int nt = two ? 2 : 1;
       bool ok = mbar_wait_role(q_full, 0, abort) && mbar_wait_role(&full[0], 0, abort);
       if (ok) {
         tc_fence_after();
-        for (int t = 0; t < nt; ++t) scores(t, 0);
-        mma_commit(&empty[0]);
+        scores(0, 0);
+        if (two) scores(1, 0);
+        if (leader) mma_commit(&empty[0]);
       }
+      int sv = 1, sk = 2, pv = 0, pk = 0;  // slots of V_j and K_{j+1}, parities of their phases
+#pragma unroll 1
       for (int j = 0; ok && j < tiles; ++j) {
-        const int uv = 2 * j + 1, uk = 2 * j + 2;
-        const int sv = uv % L::kSlots, sk = uk % L::kSlots;
         const bool more = j + 1 < tiles;
         // at the causal edge V is waited for through the warps that check it
-        ok = j < whole ? mbar_wait_role(&full[sv], (uv / L::kSlots) & 1, abort)
+        ok = j < whole ? mbar_wait_role(&full[sv], pv, abort)
                        : mbar_wait_role(&v_ok[j - whole], 0, abort);
-        if (ok && more) ok = mbar_wait_role(&full[sk], (uk / L::kSlots) & 1, abort);
+        if (ok && more) ok = mbar_wait_role(&full[sk], pk, abort);
+#pragma unroll 1
         for (int t = 0; ok && t < nt; ++t) {
-          ok = mbar_wait_role(&p_full[t], j & 1, abort);
+          ok = mbar_wait_role(&p_full[2 * t], j & 1, abort);
           if (!ok) break;
           tc_fence_after();
-          values(t, sv, j > 0);
+          values(t, sv, j > 0, 0);
+          ok = mbar_wait_role(&p_full[2 * t + 1], j & 1, abort);
+          if (!ok) break;
+          tc_fence_after();
+          values(t, sv, true, 1);
           if (more) scores(t, sk);  // in issue order behind the P V that reads what it overwrites
-          else mma_commit(&o_full[t]);
+          else if (leader) mma_commit(&o_full[t]);
         }
         if (!ok) break;
-        mma_commit(&empty[sv]);
-        if (more) mma_commit(&empty[sk]);
+        if (leader) {
+          mma_commit(&empty[sv]);
+          if (more) mma_commit(&empty[sk]);
+        }
+        sv += 2;
+        sk += 2;
+        if (sv >= L::kSlots) {
+          sv -= L::kSlots;
+          pv ^= 1;
+        }
+        if (sk >= L::kSlots) {
+          sk -= L::kSlots;
+          pk ^= 1;
+        }
       }
       if (!ok) {  // bounded wait for the matrix instructions in flight
-        mma_commit(drain);
+        if (leader) mma_commit(drain);
         mbar_wait_bounded(drain, 0);
       }
     } else if (warp >= 10 && work) {
@@ -341,7 +410,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes, in bits 16..
       const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 2 * kTile + t * DP;
       const float c = a.scale_log2;
-      float ref = 0.f, sum = 0.f;
+      float ref = 0.f;
+      uint64_t part[2] = {0, 0};  // sums of weights, two by two
       bool ok = true;
       for (int j = 0; j < tiles; ++j) {
         ok = mbar_wait_role(&s_full[t], j & 1, abort);
@@ -372,7 +442,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             // P V of the earlier tiles is done: S of this tile was issued behind it
             const float f = raise ? ex2(ref - top) : 1.f;
             if (raise) ref = top;
-            sum *= f;
+            part[0] = mul2(part[0], pair(f, f));
+            part[1] = mul2(part[1], pair(f, f));
 #pragma unroll 1
             for (int b = 0; b < DP / 32; ++b) {
               uint32_t o[32];
@@ -384,22 +455,37 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             }
           }
         }
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t p[kTile / 2];
+        // 2^(c s - ref) two at a time; half of the weights go to the matrix unit while the other
+        // half is computed
+        const uint64_t c2 = pair(c, c), r2 = pair(-ref, -ref);
 #pragma unroll
-        for (int x = 0; x < kTile; x += 2) {
-          const float e0 = ex2(fmaf(__uint_as_float(s[x]), c, -ref));
-          const float e1 = ex2(fmaf(__uint_as_float(s[x + 1]), c, -ref));
-          part[x & 2] += e0;
-          part[(x & 2) + 1] += e1;
-          p[x / 2] = pack_bf16(e0, e1);
+        for (int b = 0; b < 4; ++b) {
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float e0, e1;
+            unpair(fma2(pair(__uint_as_float(s[32 * b + 2 * x]), __uint_as_float(s[32 * b + 2 * x + 1])),
+                        c2, r2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            part[x & 1] = add2(part[x & 1], pair(e0, e1));
+            p[x] = pack_bf16(e0, e1);
+          }
+          tmem_st16(s_at + 16 * b, p);
+          if (b & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * t + (b >> 1)]);
+          }
         }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
-        tmem_st32(s_at, p);
-        tmem_st32(s_at + 32, p + 32);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[t]);
+      }
+      float sum;
+      {
+        float a0, a1, b0, b1;
+        unpair(part[0], a0, a1);
+        unpair(part[1], b0, b1);
+        sum = (a0 + a1) + (b0 + b1);
       }
       // -------------------------------------------------------------- epilogue
       if (ok) ok = __all_sync(kFull, mbar_wait_role(&o_full[t], 0, abort));

@@ -41,7 +41,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtas = 3;                  // per SM: 12 warps of 168 registers
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kUnit = 32;                 // tokens of a unit
 constexpr int kWindow = 8 * kUnit;        // tokens of a table lookup
 constexpr float kRefStart = -1e30f;       // below every logit, and finite

@@ -53,8 +53,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       KVP_S4(r, 24), KVP_S4(r, 28)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(addr),
+      KVP_S4(r, 0), KVP_S4(r, 4), KVP_S4(r, 8), KVP_S4(r, 12)
+      : "memory");
+}
 #undef KVP_R4
 #undef KVP_S4
+
+// True in one lane of a converged warp.  A role that issues for its CTA runs its loop and
+// waits in the whole warp, so that the compiler keeps descriptors in uniform registers, and
+// only the issue itself under this predicate (with the loop in one lane, every matrix
+// instruction carried about 20 others and the issue, not the matrix unit, was the bound).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
+}
 
 // ---------------------------------------------------------------------------
 // Matrix instructions: D[128 x N] (+)= A[128 x 16] B[16 x N], bf16 in, fp32 out.
@@ -101,12 +118,13 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 // Wait for a phase, bounded like mbar_wait_bounded, but with no timer on the usual path: the
-// timer starts after the first tries.  Gives up at once when another role of the CTA has
-// (*abort), and tells the others when it does.
+// timer starts after the first tries (a try suspends the thread for a while, so these pass in
+// milliseconds at most).  Gives up when another role of the CTA has (*abort), and tells the
+// others when it does.
 __device__ __forceinline__ bool mbar_wait_role(uint64_t* bar, uint32_t parity,
                                                volatile int* abort) {
 #pragma unroll 1
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 4096; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
 #pragma unroll 1

@@ -8,13 +8,17 @@
 // Everything is held in 32 bits from the bf16 input to the one rounding of the
 // output.
 //
-// GPU shape.  8 channels (4 pairs) per lane, so a head is D / 8 lanes and the
-// sum of squares is a shuffle reduction inside them; with half-split pairs a
-// lane holds 4 consecutive channels of each half (two 8-byte loads), with
-// interleaved pairs 8 consecutive ones (one 16-byte load), so no pair ever
-// crosses lanes.  A warp takes kSteps x (32 / lanes per head) heads of ONE
-// token: the position, the slot and the (cos, sin) row are read once for all
-// of them, and every head's load is issued before the first is used.
+// Both at once: a' = r (x_a (w_a c) - x_b (w_b s)) with r = 1 / sqrt(..), and the products
+// of weights and angles are one set for all heads of a token.
+//
+// GPU shape.  The bytes bound a large batch, the chain position -> (cos, sin) -> store a small
+// one.  8 channels (4 pairs) per lane, so a head is D / 8 lanes and the sum of squares is a
+// shuffle reduction inside them; with half-split pairs a lane holds 4 consecutive channels of
+// each half (two 8-byte loads), with interleaved pairs 8 consecutive ones (one 16-byte load),
+// so no pair ever crosses lanes.  A warp takes kSteps x (32 / lanes per head) heads of one kind
+// (query, key or value) of ONE token: position, slot and angles are read once for all of them
+// and every head's load is issued before the first is used.  fp32 in pairs (one instruction for
+// two).
 #include <cuda_bf16.h>
 
 #include "kv_common.cuh"
@@ -44,9 +48,10 @@ struct NormRopeArgs {
   int64_t layer_base;      // layer * num_blocks
   int64_t num_blocks;
   int32_t block_size;
+  BlockDiv div;
   const int64_t* slots;
   int32_t* err;
-  int32_t units;           // warps per token
+  int32_t units, q_units, kv_units;  // warps per token; of them for queries; for keys
 };
 
 // The 8 channels of a lane: pairs (x[i], x[4 + i]), i < 4.
@@ -54,13 +59,13 @@ struct Pairs {
   uint2 a, b;
 };
 
-__device__ __forceinline__ void unpack4(const uint2& u, float* f) {
-  f[0] = __uint_as_float(u.x << 16);
-  f[1] = __uint_as_float(u.x & 0xffff0000u);
-  f[2] = __uint_as_float(u.y << 16);
-  f[3] = __uint_as_float(u.y & 0xffff0000u);
+// Two bf16 values as a pair of fp32.
+__device__ __forceinline__ uint64_t unpack2(uint32_t u) {
+  return pair(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  unpair(v, lo, hi);
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
@@ -91,22 +96,30 @@ __device__ __forceinline__ void store_pairs(__nv_bfloat16* row, int ca, int cb, 
   }
 }
 
-// kLanes: lanes per head (8, 16, 32: head_dim / 8 rounded up to a power of two).
-template <int kLanes, bool kInterleaved, int kSteps>
+// kLanes: lanes per head (8, 16, 32: head_dim / 8 rounded up to a power of two).  kAll: every
+// channel is rotated.
+template <int kLanes, bool kInterleaved, bool kAll, int kSteps>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a) {
   pdl_allow_next();
   pdl_wait();
-  constexpr int kHeads = 32 / kLanes;  // heads of a warp step
+  constexpr int kHeads = 32 / kLanes;        // heads of a warp step
+  constexpr int kUnit = kSteps * kHeads;     // heads of a warp
   const int lane = threadIdx.x & 31;
   const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
   const int64_t t = unit / a.units;
   if (t >= a.num_tokens) return;
-  const int head0 = (int)(unit - t * a.units) * (kSteps * kHeads) + lane / kLanes;
+  // which heads: query units, then key units, then value units
+  int u = (int)(unit - t * a.units);
+  const bool is_q = u < a.q_units;
+  const bool is_k = !is_q && u < a.q_units + a.kv_units;
+  u -= is_q ? 0 : is_k ? a.q_units : a.q_units + a.kv_units;
+  const int heads = is_q ? a.q_heads : a.kv_heads;
+  const int head0 = u * kUnit + lane / kLanes;
   const int l = lane % kLanes;
   const int D = a.head_dim, R = a.rotary_dim;
   const bool active = l * 8 < D;
   // this lane's channels: pairs (ca + i, cb + i), rotated by pair index 4 l + i
-  const bool rot = l * 8 < R;
+  const bool rot = kAll || l * 8 < R;
   int ca, cb;
   if (kInterleaved) {
     ca = cb = 8 * l;
@@ -117,107 +130,124 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a) {
     ca = R + 4 * l - R / 2;
     cb = ca + (D - R) / 2;
   }
-  const int total = a.q_heads + 2 * a.kv_heads;
-
+  const __nv_bfloat16* in = is_q   ? a.q + t * a.q_stride
+                            : is_k ? a.k + t * a.k_stride
+                                   : a.v + t * a.v_stride;
   Pairs x[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int h = head0 + s * kHeads;
     x[s].a = x[s].b = make_uint2(0, 0);
-    if (!active || h >= total) continue;
-    if (h < a.q_heads) {
-      x[s] = load_pairs<kInterleaved>(a.q + t * a.q_stride + (int64_t)h * D, ca, cb);
-    } else if (h < a.q_heads + a.kv_heads) {
-      x[s] = load_pairs<kInterleaved>(a.k + t * a.k_stride + (int64_t)(h - a.q_heads) * D, ca, cb);
-    } else if (a.v_cache != nullptr) {
-      x[s] = load_pairs<kInterleaved>(
-          a.v + t * a.v_stride + (int64_t)(h - a.q_heads - a.kv_heads) * D, ca, cb);
-    }
+    if (active && h < heads) x[s] = load_pairs<kInterleaved>(in + h * D, ca, cb);
   }
   uint32_t err = 0;
   const int64_t pos = a.positions[t];
   const bool pos_ok = pos >= 0 && pos < a.max_position;
   if (!pos_ok) err |= KV_ERR_BAD_POSITION;
   int64_t cache_row = -1;
-  if (a.k_cache != nullptr) {
+  if (!is_q && a.k_cache != nullptr) {
     const int64_t s = a.slots[t];
     if (s >= 0) {
-      const int64_t b = s / a.block_size;
+      int64_t b, off;
+      a.div.divmod(s, b, off);
       if (b == kNull) err |= KV_ERR_NULL_WRITE;
       else if (b >= a.num_blocks) err |= KV_ERR_BAD_SLOT;
-      else if (pos_ok) cache_row = (a.layer_base + b) * a.block_size + (s - b * a.block_size);
+      else if (pos_ok) cache_row = (a.layer_base + b) * a.block_size + off;
     }
   }
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), z = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (rot && pos_ok) {
-    const float* row = a.cos_sin + pos * R;
-    c = *reinterpret_cast<const float4*>(row + 4 * l);
-    z = *reinterpret_cast<const float4*>(row + R / 2 + 4 * l);
+  if (!is_q && !is_k) {  // values: their bits, to the cache
+    __nv_bfloat16* out = a.v_cache + cache_row * a.kv_heads * D;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int h = head0 + s * kHeads;
+      if (active && h < heads && cache_row >= 0) store_pairs<kInterleaved>(out + h * D, ca, cb, x[s]);
+    }
+    return;  // errors are reported by the keys' units
   }
-  Pairs wq, wk;
-  wq.a = wq.b = wk.a = wk.b = make_uint2(0, 0);
+  // weights times angles: a' = r (x_a wc_a - x_b ws_b), b' = r (x_b wc_b + x_a ws_a)
+  uint64_t wc_a[2] = {}, wc_b[2] = {}, ws_a[2] = {}, ws_b[2] = {};
   if (active) {
-    wq = load_pairs<kInterleaved>(a.q_weight, ca, cb);
-    wk = load_pairs<kInterleaved>(a.k_weight, ca, cb);
+    const Pairs w = load_pairs<kInterleaved>(is_q ? a.q_weight : a.k_weight, ca, cb);
+    const uint64_t wa[2] = {unpack2(w.a.x), unpack2(w.a.y)};
+    const uint64_t wb[2] = {unpack2(w.b.x), unpack2(w.b.y)};
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), z = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (rot && pos_ok) {
+      const float* row = a.cos_sin + pos * R;
+      c = *reinterpret_cast<const float4*>(row + 4 * l);
+      z = *reinterpret_cast<const float4*>(row + R / 2 + 4 * l);
+    }
+    const uint64_t cc[2] = {pair(c.x, c.y), pair(c.z, c.w)}, zz[2] = {pair(z.x, z.y), pair(z.z, z.w)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      wc_a[i] = mul2(wa[i], cc[i]);
+      wc_b[i] = mul2(wb[i], cc[i]);
+      ws_a[i] = mul2(wa[i], zz[i]);
+      ws_b[i] = mul2(wb[i], zz[i]) ^ 0x8000000080000000ull;  // negated
+    }
   }
   const float inv_d = 1.0f / (float)D;
-  const float cc[4] = {c.x, c.y, c.z, c.w}, zz[4] = {z.x, z.y, z.z, z.w};
+  __nv_bfloat16* out =
+      is_q ? a.q_out + t * a.q_heads * D : a.k_out == nullptr ? nullptr : a.k_out + t * a.kv_heads * D;
+  __nv_bfloat16* cached = cache_row >= 0 ? a.k_cache + cache_row * a.kv_heads * D : nullptr;
 
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int h = head0 + s * kHeads;
-    const bool is_q = h < a.q_heads, is_k = !is_q && h < a.q_heads + a.kv_heads;
-    float p[4], q[4], w[4], u[4];
-    unpack4(x[s].a, p);
-    unpack4(x[s].b, q);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ss += p[i] * p[i] + q[i] * q[i];
+    const uint64_t xa[2] = {unpack2(x[s].a.x), unpack2(x[s].a.y)};
+    const uint64_t xb[2] = {unpack2(x[s].b.x), unpack2(x[s].b.y)};
+    uint64_t sq = mul2(xa[0], xa[0]);
+    sq = fma2(xa[1], xa[1], sq);
+    sq = fma2(xb[0], xb[0], sq);
+    sq = fma2(xb[1], xb[1], sq);
+    float s0, s1;
+    unpair(sq, s0, s1);
+    float ss = s0 + s1;
 #pragma unroll
     for (int m = 1; m < kLanes; m <<= 1) ss += __shfl_xor_sync(kFull, ss, m);
-    const float r = rsqrtf(ss * inv_d + a.eps);
-    unpack4(is_q ? wq.a : wk.a, w);
-    unpack4(is_q ? wq.b : wk.b, u);
-    float ya[4], yb[4];
+    const float r = pos_ok ? rsqrtf(ss * inv_d + a.eps) : 0.f;
+    const uint64_t r2 = pair(r, r);
+    uint64_t ya[2], yb[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float f = p[i] * r * w[i], g = q[i] * r * u[i];
-      ya[i] = rot ? f * cc[i] - g * zz[i] : f;
-      yb[i] = rot ? g * cc[i] + f * zz[i] : g;
+    for (int i = 0; i < 2; ++i) {
+      ya[i] = mul2(xa[i], wc_a[i]);
+      yb[i] = mul2(xb[i], wc_b[i]);
+      if (kAll || rot) {  // an infinity must not reach a channel it is not rotated with
+        ya[i] = fma2(xb[i], ws_b[i], ya[i]);
+        yb[i] = fma2(xa[i], ws_a[i], yb[i]);
+      }
+      ya[i] = mul2(ya[i], r2);
+      yb[i] = mul2(yb[i], r2);
     }
     Pairs o;
-    o.a = make_uint2(pack2(ya[0], ya[1]), pack2(ya[2], ya[3]));
-    o.b = make_uint2(pack2(yb[0], yb[1]), pack2(yb[2], yb[3]));
+    o.a = make_uint2(pack2(ya[0]), pack2(ya[1]));
+    o.b = make_uint2(pack2(yb[0]), pack2(yb[1]));
     if (!pos_ok) o.a = o.b = make_uint2(0, 0);
-    if (!active || h >= total) continue;
-    if (is_q) {
-      store_pairs<kInterleaved>(a.q_out + (t * a.q_heads + h) * D, ca, cb, o);
-    } else if (is_k) {
-      const int hk = h - a.q_heads;
-      if (a.k_out != nullptr)
-        store_pairs<kInterleaved>(a.k_out + (t * a.kv_heads + hk) * D, ca, cb, o);
-      if (cache_row >= 0)
-        store_pairs<kInterleaved>(a.k_cache + (cache_row * a.kv_heads + hk) * D, ca, cb, o);
-    } else if (cache_row >= 0) {
-      store_pairs<kInterleaved>(
-          a.v_cache + (cache_row * a.kv_heads + h - a.q_heads - a.kv_heads) * D, ca, cb, x[s]);
-    }
+    if (!active || h >= heads) continue;
+    if (out != nullptr) store_pairs<kInterleaved>(out + h * D, ca, cb, o);
+    if (cached != nullptr) store_pairs<kInterleaved>(cached + h * D, ca, cb, o);
   }
   report(a.err, err);
 }
 
-template <int kLanes, bool kInterleaved>
+template <int kLanes, bool kInterleaved, bool kAll>
 int launch(NormRopeArgs a, cudaStream_t stream) {
-  constexpr int kHeads = 32 / kLanes;
-  const int heads = a.q_heads + a.kv_heads + (a.v_cache != nullptr ? a.kv_heads : 0);
-  const int steps = (heads + kHeads - 1) / kHeads;
   constexpr int kSteps = 4;
-  a.units = (steps + kSteps - 1) / kSteps;
+  constexpr int kUnit = kSteps * (32 / kLanes);
+  a.q_units = (a.q_heads + kUnit - 1) / kUnit;
+  a.kv_units = (a.kv_heads + kUnit - 1) / kUnit;
+  a.units = a.q_units + a.kv_units * (a.v_cache != nullptr ? 2 : 1);
   const int64_t warps = (int64_t)a.num_tokens * a.units;
   const int64_t ctas = (warps * 32 + kThreads - 1) / kThreads;
   if (ctas > INT32_MAX) return KV_EUNSUPPORTED;
-  return launch_pdl(norm_rope_kernel<kLanes, kInterleaved, kSteps>, (unsigned)ctas, kThreads, 0,
-                    stream, a);
+  return launch_pdl(norm_rope_kernel<kLanes, kInterleaved, kAll, kSteps>, (unsigned)ctas, kThreads,
+                    0, stream, a);
+}
+
+template <int kLanes>
+int launch(const NormRopeArgs& a, bool interleaved, cudaStream_t stream) {
+  const bool all = a.rotary_dim == a.head_dim;
+  if (interleaved) return all ? launch<kLanes, true, true>(a, stream) : launch<kLanes, true, false>(a, stream);
+  return all ? launch<kLanes, false, true>(a, stream) : launch<kLanes, false, false>(a, stream);
 }
 
 }  // namespace
@@ -286,10 +316,9 @@ extern "C" int kv_qk_norm_rope_write(
                  num_kv_heads, head_dim, static_cast<__nv_bfloat16*>(q_out),
                  static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(k_cache),
                  static_cast<__nv_bfloat16*>(v_cache),
-                 cached ? (int64_t)layer * num_blocks : 0, num_blocks, block_size, slot_mapping,
-                 d_err, 0};
-  if (head_dim <= 64) return interleaved ? launch<8, true>(a, stream) : launch<8, false>(a, stream);
-  if (head_dim <= 128)
-    return interleaved ? launch<16, true>(a, stream) : launch<16, false>(a, stream);
-  return interleaved ? launch<32, true>(a, stream) : launch<32, false>(a, stream);
+                 cached ? (int64_t)layer * num_blocks : 0, num_blocks, block_size,
+                 BlockDiv::make(block_size), slot_mapping, d_err, 0, 0, 0};
+  if (head_dim <= 64) return launch<8>(a, interleaved != 0, stream);
+  if (head_dim <= 128) return launch<16>(a, interleaved != 0, stream);
+  return launch<32>(a, interleaved != 0, stream);
 }

@@ -3,18 +3,18 @@
 //
 // Mathematics (layout in kv_q4.cuh).  For a group of 32 channels x of one row
 //   s = bf16(max|x| / 7),  code = round(x / s) + 8  (nearest, ties to even),
-// read back as (code - 8) * s.  round(x / s) is found without a division: with
-// t = x * (1/s) rounded to an integer q, x / s is within 2^-23 of t, and as x
-// and s have 8 significant bits each, x / s is either a tie (k + 1/2) or more
-// than 2^-13 away from one.  So q is right unless 2 |x - q s| == s, which is
-// tested exactly (q s and the difference fit 32 bits), and a tie goes to even.
-// |x / s| <= 7 (1 + 2^-8), so no clamp is needed.
+// read back as (code - 8) * s.  round(x / s) is found without a division: x and s have 8
+// significant bits each, so x / s, at most 7 (1 + 2^-8), is either a tie k + 1/2 or more than
+// 2^-10 away from every one, and the integer q nearest to x times an approximate 1 / s (within
+// 2^-22) is right unless x / s is a tie.  Then, and only then, 2 |x - q s| == s, which is exact in
+// 32 bits; groups with a tie are done again value by value.  No clamp is needed.
 #include "kv_q4.cuh"
 
 namespace kvp {
 namespace {
 
-constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+constexpr float kRound = 12582920.0f;  // 1.5 * 2^23 + 8: adding it rounds to an integer and
+                                       // leaves the code, the integer + 8, in the low bits
 
 struct WriteArgs {
   const __nv_bfloat16* key;
@@ -25,62 +25,107 @@ struct WriteArgs {
   const int64_t* slots;
   int32_t num_tokens;
   Q4Layout at;
+  BlockDiv div;
   int32_t* err;
 };
 
 constexpr int kWriteThreads = 128;
 
-// One row of one head by 8 lanes: lane g holds channels 32 j + 4 g .. + 3.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Correctly rounded max / 7: a product and one step of its own remainder.  (The remainder of
+// a tiny value would leave the normal range: divided.)
+__device__ __forceinline__ float over_seven(float x) {
+  if (x < 1e-18f) return __fdiv_rn(x, 7.0f);
+  const float c = 1.0f / 7.0f, q = x * c;
+  return fmaf(fmaf(-7.0f, q, x), c, q);
+}
+// The codes of 4 values of scale s, ties to even: the slow way, for groups that hold a tie.
+__device__ __noinline__ uint32_t codes_with_ties(float v0, float v1, float v2, float v3, float s,
+                                                 float inv) {
+  const float v[4] = {v0, v1, v2, v3};
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float t = fmaf(v[i], inv, kRound);
+    int code = __float_as_int(t) & 15;
+    const float r = fmaf(kRound - t, s, v[i]);  // x - q s
+    if (fabsf(r) * 2.f == s && (code & 1)) code += r > 0.f ? 1 : -1;
+    c |= (uint32_t)code << (4 * i);
+  }
+  return c;
+}
+
+// One row of one head by 8 lanes: lane g holds channels 32 j + 4 g .. + 3.  `top`: the largest
+// magnitudes of the groups as bf16 bits, two groups to a word.
 template <int G>
-__device__ __forceinline__ void quantise_row(const uint2 (&x)[G], uint8_t* codes, uint8_t* scales,
-                                             int g, bool store) {
+__device__ __forceinline__ void quantise_row(const uint2 (&x)[G], const uint32_t (&top)[G / 2],
+                                             uint8_t* codes, uint8_t* scales, int g, bool store) {
   uint32_t half[G];   // 4 codes of each group
   uint32_t sbits[G];  // bf16 scales
 #pragma unroll
   for (int j = 0; j < G; ++j) {
-    // magnitudes as integers: NaN > infinity > every finite value
-    const uint32_t m2 = __vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu);
-    uint32_t m = max(m2 & 0xffffu, m2 >> 16);
-#pragma unroll
-    for (int k = 1; k < 8; k <<= 1) m = max(m, __shfl_xor_sync(kFull, m, k));
-    const float amax = __uint_as_float(m << 16);
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
+    const uint32_t m = j & 1 ? top[j / 2] & 0xffff0000u : top[j / 2] << 16;
+    const __nv_bfloat16 sb = __float2bfloat16_rn(over_seven(__uint_as_float(m)));
     float s = __bfloat162float(sb);
     sbits[j] = __bfloat16_as_ushort(sb);
-    float inv = 0.f;
-    if (m >= 0x7f80u) {          // an infinity or a NaN: the whole group reads as NaN
-      sbits[j] = 0x7fc0u;
-    } else if (s < 1.17549435e-38f) {  // scale below the normal range: a group of zeros
-      sbits[j] = 0u;
-    } else {
-      inv = __frcp_rn(s);
-    }
-    const float v[4] = {__uint_as_float(x[j].x << 16), __uint_as_float(x[j].x & 0xffff0000u),
-                        __uint_as_float(x[j].y << 16), __uint_as_float(x[j].y & 0xffff0000u)};
+    if (s < 1.17549435e-38f) s = 0.f, sbits[j] = 0u;   // below the normal range: a group of zeros
+    if (m >= 0x7f800000u) s = 0.f, sbits[j] = 0x7fc0u;  // infinity or NaN: the group reads as NaN
+    const float inv = s > 0.f ? rcp_approx(s) : 0.f;
+    const float tie = s > 0.f ? 0.5f * s : -1.f;
+    const uint64_t v[2] = {pair(__uint_as_float(x[j].x << 16), __uint_as_float(x[j].x & 0xffff0000u)),
+                           pair(__uint_as_float(x[j].y << 16), __uint_as_float(x[j].y & 0xffff0000u))};
+    const uint64_t inv2 = pair(inv, inv), s2 = pair(s, s), round2 = pair(kRound, kRound);
+    const uint64_t minus = pair(-1.f, -1.f);
     uint32_t c = 0;
+    bool tied = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int ti = 0;
-      if (inv != 0.f) {
-        const float t = fmaf(v[i], inv, kRound);
-        ti = __float_as_int(t);
-        const float r = fmaf(kRound - t, s, v[i]);  // x - q s, exact
-        if (fabsf(r) * 2.f == s && (ti & 1)) ti += r > 0.f ? 1 : -1;
-      }
-      c |= (uint32_t)((ti + 8) & 15) << (4 * i);
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t t = fma2(v[i], inv2, round2);
+      const uint64_t r = fma2(fma2(t, minus, round2), s2, v[i]);  // x - q s
+      float t0, t1, r0, r1;
+      unpair(t, t0, t1);
+      unpair(r, r0, r1);
+      tied |= fabsf(r0) == tie || fabsf(r1) == tie;
+      // the low 16 bits: the float's own bits above the code are multiples of 2^22
+      c += (__float_as_uint(t0) + 16u * __float_as_uint(t1)) << (8 * i);
+    }
+    if (tied) {
+      float v0, v1, v2, v3;
+      unpair(v[0], v0, v1);
+      unpair(v[1], v2, v3);
+      c = codes_with_ties(v0, v1, v2, v3, s, inv);
     }
     half[j] = c;
   }
   if (!store) return;
   if constexpr (G == 4) {
-    *reinterpret_cast<uint2*>(codes + 8 * g) =
-        make_uint2(half[0] | half[1] << 16, half[2] | half[3] << 16);
+    *reinterpret_cast<uint2*>(codes + 8 * g) = make_uint2(__byte_perm(half[0], half[1], 0x5410),
+                                                          __byte_perm(half[2], half[3], 0x5410));
     if (g == 0)
       *reinterpret_cast<uint2*>(scales) =
           make_uint2(sbits[0] | sbits[1] << 16, sbits[2] | sbits[3] << 16);
   } else {
-    *reinterpret_cast<uint32_t*>(codes + 4 * g) = half[0] | half[1] << 16;
+    *reinterpret_cast<uint32_t*>(codes + 4 * g) = __byte_perm(half[0], half[1], 0x5410);
     if (g == 0) *reinterpret_cast<uint32_t*>(scales) = sbits[0] | sbits[1] << 16;
+  }
+}
+
+// Largest magnitudes of the row's groups as integers (NaN > infinity > every finite value), two
+// groups to a word, over the 8 lanes.
+template <int G>
+__device__ __forceinline__ void largest(const uint2 (&x)[G], uint32_t (&top)[G / 2]) {
+#pragma unroll
+  for (int j = 0; j < G; j += 2) {
+    const uint32_t a = __vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu);
+    const uint32_t b = __vmaxu2(x[j + 1].x & 0x7fff7fffu, x[j + 1].y & 0x7fff7fffu);
+    uint32_t m = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+    for (int k = 1; k < 8; k <<= 1) m = __vmaxu2(m, __shfl_xor_sync(kFull, m, k));
+    top[j / 2] = m;
   }
 }
 
@@ -90,9 +135,9 @@ __global__ void __launch_bounds__(kWriteThreads) write_q4_kernel(WriteArgs a) {
   pdl_wait();
   const int g = threadIdx.x & 7;
   const int64_t item = ((int64_t)blockIdx.x * kWriteThreads + threadIdx.x) >> 3;
-  const int H = a.at.kv_heads, T = a.at.block_size;
+  const int H = a.at.kv_heads;
   const bool in = item < (int64_t)a.num_tokens * H;
-  const int64_t t = in ? item / H : 0;
+  const int64_t t = !in ? 0 : item <= INT32_MAX ? (uint32_t)item / (uint32_t)H : item / H;
   const int h = (int)(item - t * H);
   uint2 k[G], v[G];
 #pragma unroll
@@ -109,13 +154,14 @@ __global__ void __launch_bounds__(kWriteThreads) write_q4_kernel(WriteArgs a) {
   const int64_t s = in ? a.slots[t] : -1;
   bool store = false;
   if (s >= 0) {
-    const int64_t b = s / T;
+    int64_t b, rest;
+    a.div.divmod(s, b, rest);
     if (b == kNull) {
       err |= KV_ERR_NULL_WRITE;
     } else if (b >= a.at.num_blocks) {
       err |= KV_ERR_BAD_SLOT;
     } else {
-      const int32_t off = (int32_t)(s - b * T);
+      const int32_t off = (int32_t)rest;
       const int64_t rec = a.at.record(b, h);
       kc = a.k_cache + rec + a.at.codes(off);
       vc = a.v_cache + rec + a.at.codes(off);
@@ -124,16 +170,21 @@ __global__ void __launch_bounds__(kWriteThreads) write_q4_kernel(WriteArgs a) {
       store = true;
     }
   }
-  quantise_row<G>(k, kc, ks, g, store);
-  quantise_row<G>(v, vc, vs, g, store);
+  uint32_t k_top[G / 2], v_top[G / 2];
+  largest<G>(k, k_top);
+  largest<G>(v, v_top);
+  quantise_row<G>(k, k_top, kc, ks, g, store);
+  quantise_row<G>(v, v_top, vc, vs, g, store);
   report(a.err, err);
 }
 
 // ---------------------------------------------------------------------------
-// Gather.  As the bf16 gather: every CTA scans the span lengths into packed
-// output offsets, then warps walk the output rows, kGatherRows at a time: lane
-// i resolves the slot of row i, and 8 lanes turn one (row, head) of K and of V
-// into bf16.
+// Gather.  As the bf16 gather: every CTA scans the span lengths into packed output offsets,
+// then warps walk the output rows, kGatherRows at a time.  Eight lanes stand for two of the
+// rows and go through their heads, so the block and the position in it are resolved once per
+// row and a head is one addition to each address.  The output's bytes bound it (256 of 328 a
+// head at 128 channels); what stood in the way was the conversion, at 11 instructions for two
+// values one by one (86 us for 75k rows of 8 x 128, K and V): now 5, in bf16 pairs.
 
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 8;
@@ -143,6 +194,7 @@ struct GatherArgs {
   const uint8_t* k_cache;
   const uint8_t* v_cache;
   Q4Layout at;
+  BlockDiv div;
   const int32_t* table;
   int32_t stride;
   const int32_t* g0;
@@ -154,37 +206,52 @@ struct GatherArgs {
   int32_t* err;
 };
 
-// Two codes (nibbles 4 i and 4 i + 4 of c) as bf16 values times scale s.
-__device__ __forceinline__ uint32_t value2(uint32_t c, int i, float s) {
-  const float lo = (float)((int)((c >> (4 * i)) & 15u) - 8) * s;
-  const float hi = (float)((int)((c >> (4 * i + 4)) & 15u) - 8) * s;
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
+// The four codes of h (16 bits) times scale s (bf16, in both halves), as two bf16 pairs.  A
+// nibble under the exponent of 128 is 128 + u; less 136 it is u - 8, both exact, and the product
+// is the only rounding.
+__device__ __forceinline__ uint2 values4(uint32_t h, uint32_t s, uint32_t exponent) {
+  const uint32_t t = h | h << 12;  // nibbles 1 and 3 again, where the upper half has 0 and 2
+  uint32_t a, b;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(a) : "r"(t), "r"(exponent));
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(b) : "r"(t >> 8), "r"(exponent));
+  const __nv_bfloat162 off = __floats2bfloat162_rn(-136.f, -136.f);
+  const __nv_bfloat162 scale = *reinterpret_cast<const __nv_bfloat162*>(&s);
+  const __nv_bfloat162 x = __hmul2_rn(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), off), scale);
+  const __nv_bfloat162 y = __hmul2_rn(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&b), off), scale);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
+// One row of one head by 8 lanes: lane l holds the codes of g = 2 (l & 3) and the next g, of
+// which it stores the groups j = l >> 2 and j + 2: 8 channels, 16 bytes, each, so that the 8
+// lanes write whole 128-byte lines.
 template <int G>
 struct PackedRow {
-  uint32_t c[G / 2], s[G / 2];
-  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int g) {
+  uint32_t c[G], s[G / 2];
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales) {
     if constexpr (G == 4) {
-      const uint2 u = *reinterpret_cast<const uint2*>(codes + 8 * g);
+      const uint4 u = *reinterpret_cast<const uint4*>(codes);
       const uint2 w = *reinterpret_cast<const uint2*>(scales);
-      c[0] = u.x, c[1] = u.y, s[0] = w.x, s[1] = w.y;
+      c[0] = u.x, c[1] = u.y, c[2] = u.z, c[3] = u.w, s[0] = w.x, s[1] = w.y;
     } else {
-      c[0] = *reinterpret_cast<const uint32_t*>(codes + 4 * g);
+      const uint2 u = *reinterpret_cast<const uint2*>(codes);
+      c[0] = u.x, c[1] = u.y;
       s[0] = *reinterpret_cast<const uint32_t*>(scales);
     }
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < G / 2; ++i) c[i] = 0x88888888u, s[i] = 0u;
-  }
-  __device__ __forceinline__ void store(__nv_bfloat16* row, int g) const {
+    for (int i = 0; i < G; ++i) c[i] = 0x88888888u;
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const uint32_t h = j & 1 ? c[j / 2] >> 16 : c[j / 2] & 0xffffu;
-      const float f = __uint_as_float(j & 1 ? s[j / 2] & 0xffff0000u : s[j / 2] << 16);
-      *reinterpret_cast<uint2*>(row + 32 * j + 4 * g) = make_uint2(value2(h, 0, f), value2(h, 2, f));
+    for (int i = 0; i < G / 2; ++i) s[i] = 0u;
+  }
+  // high: this lane's groups are in the words' upper halves
+  __device__ __forceinline__ void store(__nv_bfloat16* row, bool high, uint32_t exponent) const {
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) {
+      const uint32_t f = __byte_perm(s[i], 0, high ? 0x3232 : 0x1010);
+      const uint2 x = values4(__byte_perm(c[i], 0, high ? 0x4432 : 0x4410), f, exponent);
+      const uint2 y = values4(__byte_perm(c[G / 2 + i], 0, high ? 0x4432 : 0x4410), f, exponent);
+      st_stream(reinterpret_cast<uint4*>(row + 64 * i), make_uint4(x.x, x.y, y.x, y.y));
     }
   }
 };
@@ -231,55 +298,74 @@ __global__ void __launch_bounds__(kGatherThreads) gather_q4_kernel(GatherArgs a)
   }
   const int64_t rows = total < a.out_rows ? total : a.out_rows;
 
-  const int H = a.at.kv_heads, T = a.at.block_size, g = lane & 7;
+  const int H = a.at.kv_heads;
+  const bool high = lane & 4;
+  const int channel = (high ? 32 : 0) + 8 * (lane & 3);  // this lane's first
+  const int64_t rec = a.at.record_bytes();
+  uint32_t exponent;  // 128 in both halves; opaque, so that it stays one operand of a lop3
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(exponent));
   const int64_t warp0 = ((int64_t)blockIdx.x * kGatherThreads + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * kGatherThreads) >> 5;
   for (int64_t o0 = warp0 * kGatherRows; o0 < rows; o0 += nwarps * kGatherRows) {
     const int nr = (int)(rows - o0 < kGatherRows ? rows - o0 : kGatherRows);
-    int64_t slot = -1;  // lane i < nr: the slot of row o0 + i, or -1 for a zero row
-    if (lane < nr) {
-      const int64_t o = o0 + lane;
+    // rows lane / 8 and lane / 8 + 4: where their codes and scales are for head 0, or zero rows
+    const uint8_t *kc[2], *vc[2];
+    int64_t to_scales[2];
+    bool in[2], full[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int64_t o = o0 + (lane >> 3) + 4 * n;
+      in[n] = (lane >> 3) + 4 * n < nr;
+      full[n] = false;
+      kc[n] = vc[n] = nullptr;
+      to_scales[n] = 0;
+      if (!in[n]) continue;
       const int r = find_span64(s_off, R, o);
       const int64_t p = (int64_t)s_start[r] + (o - s_off[r]);
-      const int64_t lb = p / T;
+      int64_t lb, off;
+      a.div.divmod(p, lb, off);
       if (lb >= a.stride) {
         err |= KV_ERR_BAD_POSITION;
-      } else {
-        const int64_t b = a.table[(int64_t)r * a.stride + lb];
-        if (b != kNull) {
-          if (b < 0 || b >= a.at.num_blocks) err |= KV_ERR_BAD_BLOCK;
-          else slot = b * T + (p - lb * T);
-        }
+        continue;
       }
+      const int64_t b = a.table[(int64_t)r * a.stride + lb];
+      if (b == kNull) continue;
+      if (b < 0 || b >= a.at.num_blocks) {
+        err |= KV_ERR_BAD_BLOCK;
+        continue;
+      }
+      full[n] = true;
+      const int64_t at = a.at.record(b, 0) + a.at.codes((int32_t)off) + 4 * G * (lane & 3);
+      kc[n] = a.k_cache + at;
+      vc[n] = a.v_cache + at;
+      to_scales[n] = a.at.scales((int32_t)off) - a.at.codes((int32_t)off) - 4 * G * (lane & 3);
     }
-    const int items = nr * H;
-    for (int i0 = 0; i0 < items; i0 += 8) {  // two (row, head) of K and V per 8 lanes
+    __nv_bfloat16* ko = a.k_out + (o0 + (lane >> 3)) * H * (32 * G) + channel;
+    __nv_bfloat16* vo = a.v_out + (o0 + (lane >> 3)) * H * (32 * G) + channel;
+    const int64_t four = (int64_t)4 * H * (32 * G);
+#pragma unroll 2
+    for (int h = 0; h < H; ++h) {
       PackedRow<G> k[2], v[2];
-      int row[2], head[2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        const int i = i0 + 4 * n + (lane >> 3);
-        row[n] = i / H;
-        head[n] = i - row[n] * H;
-        const int64_t s = __shfl_sync(kFull, slot, row[n] & 31);
         k[n].zero();
         v[n].zero();
-        if (i < items && s >= 0) {
-          const int64_t b = s / T;
-          const int32_t off = (int32_t)(s - b * T);
-          const int64_t rec = a.at.record(b, head[n]);
-          k[n].load(a.k_cache + rec + a.at.codes(off), a.k_cache + rec + a.at.scales(off), g);
-          v[n].load(a.v_cache + rec + a.at.codes(off), a.v_cache + rec + a.at.scales(off), g);
+        if (full[n]) {
+          k[n].load(kc[n], kc[n] + to_scales[n]);
+          v[n].load(vc[n], vc[n] + to_scales[n]);
+          kc[n] += rec;
+          vc[n] += rec;
         }
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        const int i = i0 + 4 * n + (lane >> 3);
-        if (i >= items) continue;
-        const int64_t at = ((o0 + row[n]) * H + head[n]) * (32 * G);
-        k[n].store(a.k_out + at, g);
-        v[n].store(a.v_out + at, g);
+        if (in[n]) {
+          k[n].store(ko + n * four, high, exponent);
+          v[n].store(vo + n * four, high, exponent);
+        }
       }
+      ko += 32 * G;
+      vo += 32 * G;
     }
   }
   report(a.err, err);
@@ -314,7 +400,7 @@ extern "C" int kv_cache_write_q4(const void* key, int64_t key_stride, const void
               key_stride, value_stride, static_cast<uint8_t*>(k_cache),
               static_cast<uint8_t*>(v_cache), slot_mapping, num_tokens,
               Q4Layout{(int64_t)layer * num_blocks, num_blocks, block_size, num_kv_heads, head_dim},
-              d_err};
+              BlockDiv::make(block_size), d_err};
   return launch_pdl(head_dim == 128 ? write_q4_kernel<4> : write_q4_kernel<2>, (unsigned)ctas,
                     kWriteThreads, 0, stream, a);
 }
@@ -341,7 +427,7 @@ extern "C" int kv_cache_gather_q4(const void* k_cache, const void* v_cache, int3
     return KV_EINVAL;
   GatherArgs a{static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
                Q4Layout{(int64_t)layer * num_blocks, num_blocks, block_size, num_kv_heads, head_dim},
-               block_table, table_stride, gather_start, gather_end, num_reqs,
+               BlockDiv::make(block_size), block_table, table_stride, gather_start, gather_end, num_reqs,
                static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), out_rows,
                d_err};
   auto kernel = head_dim == 128 ? gather_q4_kernel<4> : gather_q4_kernel<2>;

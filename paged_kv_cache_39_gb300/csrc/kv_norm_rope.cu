@@ -99,7 +99,7 @@ __device__ __forceinline__ void store_pairs(__nv_bfloat16* row, int ca, int cb, 
 // kLanes: lanes per head (8, 16, 32: head_dim / 8 rounded up to a power of two).  kAll: every
 // channel is rotated.
 template <int kLanes, bool kInterleaved, bool kAll, int kSteps>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 10) norm_rope_kernel(NormRopeArgs a) {
   pdl_allow_next();
   pdl_wait();
   constexpr int kHeads = 32 / kLanes;        // heads of a warp step

@@ -17,11 +17,18 @@ storage must not.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional, Tuple
 
 import torch
 
-from ._lib import check, load
+from ._lib import KV_OK, check, load
+
+try:  # the current stream's handle, without a Stream object around it (about 1 us less)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    def _raw_stream(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
 
 __all__ = [
     "Prepared",
@@ -52,7 +59,11 @@ class Prepared:
     __slots__ = ("name", "_fn", "_args", "_device", "_keep", "result")
 
     def __init__(self, name, fn, args, device, keep, result):
-        self.name, self._fn, self._args, self._device = name, fn, args, device
+        # the arguments as C values once, and a function object that does not convert them
+        # again (29 arguments: 2.2 instead of 3.4 us a call)
+        self.name, self._device = name, device
+        self._fn = load()[name]
+        self._args = tuple(t(v) for t, v in zip(fn.argtypes, args))
         self._keep, self.result = keep, result
 
     def __call__(self):
@@ -60,13 +71,19 @@ class Prepared:
         return self.result
 
 
+def _stream(device: int) -> ctypes.c_void_p:
+    return ctypes.c_void_p(_raw_stream(device))
+
+
 def _launch(name: str, fn, args: tuple, device: int) -> None:
     """The C call on the current stream of the tensors' device."""
     if torch.cuda.current_device() == device:
-        check(name, fn(*args, torch.cuda.current_stream(device).cuda_stream))
-        return
-    with torch.cuda.device(device):
-        check(name, fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        status = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device))
+    if status != KV_OK:
+        check(name, status)
 
 
 def _run(name: str, args: tuple, device: int, keep: tuple, result, prepare: bool):

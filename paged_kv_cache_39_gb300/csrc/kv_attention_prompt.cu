@@ -162,10 +162,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   uint32_t err = 0;
   {
     __shared__ int warp_sum[kThreads / 32];
-    int* keys_of = reinterpret_cast<int*>(smem);  // [num_reqs], where Q's tiles will be
-    int* ranked = keys_of + kThreads;             // [num_reqs]
+    int* keys_of = reinterpret_cast<int*>(smem);                     // [num_reqs], and
+    int4* ranked = reinterpret_cast<int4*>(smem + kThreads * sizeof(int));  // the same: where Q will be
     const int pair = 2 * a.tq;
-    const bool rank = a.num_reqs <= kThreads;
+    const bool rank = a.num_reqs > 1 && a.num_reqs <= kThreads;
     const int per = (a.num_reqs + kThreads - 1) / kThreads;
     const int r_lo = min(a.num_reqs, tid * per), r_hi = min(a.num_reqs, r_lo + per);
     auto describe = [&](int r) {  // request r, or one without rows where it is not valid
@@ -187,11 +187,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         int before = 0;
         for (int r = 0; r < a.num_reqs; ++r)
           before += keys_of[r] > mine.n || (keys_of[r] == mine.n && r < tid);
-        ranked[before] = tid;
+        ranked[before] = make_int4(mine.q0, mine.k0, mine.m, mine.n);
       }
       __syncthreads();
       if (tid < a.num_reqs) {
-        mine = describe(ranked[tid]);
+        const int4 x = ranked[tid];
+        mine = Work{x.x, x.y, x.z, x.w, 0};
         count = pairs(mine);
       }
       fence_proxy_async_smem();  // before TMA writes Q there
@@ -367,37 +368,45 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         const int slot = (2 * j + 1) % L::kSlots;
         if (!mbar_wait_role(&edge[j - whole], 0, abort)) break;
         unsigned char* tile = smem + L::kRing + slot * L::kTileBytes;
+#pragma unroll 1
         for (int r = st; r < kTile; r += kScrubThreads) {
           const int key = j * kTile + r;
+          // the row's 16-byte pieces, the row's own one first: no two of 8 rows share a bank
+          auto piece = [&](int i) {
+            return reinterpret_cast<uint4*>(tile + (i / 8) * (kTile * 128) + r * 128 + ((i + r) & 7) * 16);
+          };
+          if (key >= w.n) {
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) *piece(i) = make_uint4(0, 0, 0, 0);
+            continue;
+          }
+          uint32_t most = 0;  // the largest magnitudes, two to a word; 0x7f80 and up: not finite
+#pragma unroll
           for (int i = 0; i < DP / 8; ++i) {
-            const int c = (i / 8) * 8 + ((i + r) & 7);  // 16-byte chunk, banks spread by row
-            uint4* p = reinterpret_cast<uint4*>(tile + (c / 8) * (kTile * 128) + r * 128 +
-                                                ((c & 7) ^ (r & 7)) * 16);
-            if (key >= w.n) {
-              *p = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 x = *p;
+            const uint4 x = *piece(i);
+            most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+          }
+          if ((most & 0xffffu) < 0x7f80u && most < 0x7f800000u) continue;
+#pragma unroll 1
+          for (int i = 0; i < DP / 8; ++i) {
+            uint4 x = *piece(i);
             uint32_t* e = reinterpret_cast<uint32_t*>(&x);
-            bool hit = false;
+            const int channel = (i / 8) * 64 + (((i + r) & 7) ^ (r & 7)) * 8;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               if ((e[q] & 0x7f80u) == 0x7f80u) {
-                atomicMin(&bad[c * 8 + 2 * q], key);
+                atomicMin(&bad[channel + 2 * q], key);
                 e[q] &= 0xffff0000u;
-                hit = true;
               }
               if ((e[q] & 0x7f800000u) == 0x7f800000u) {
-                atomicMin(&bad[c * 8 + 2 * q + 1], key);
+                atomicMin(&bad[channel + 2 * q + 1], key);
                 e[q] &= 0xffffu;
-                hit = true;
               }
             }
-            if (hit) {
-              *p = x;
-              *any_bad = 1;
-            }
+            *piece(i) = x;
           }
+          *any_bad = 1;
         }
         fence_proxy_async_smem();
         mbar_arrive(&v_ok[j - whole]);

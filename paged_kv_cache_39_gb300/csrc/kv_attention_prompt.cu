@@ -43,6 +43,7 @@ constexpr int kThreads = 384;
 constexpr int kScrubThreads = 64;
 constexpr int kEdges = 3;                  // K/V tiles a CTA's rows see in part: 256 tokens span at most 3
 constexpr float kLazy = 8.0f;              // log2 of the most a weight may pass the reference
+constexpr float kRefStart = -1e30f;        // of a row with no finite logit yet: below every other
 // Registers: 384 threads x 168 at launch = 256 x 208 + 128 x 88.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 
@@ -451,7 +452,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
           for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[x + y]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         if (j == 0) {
-          ref = top > -INFINITY ? top : 0.f;
+          ref = top > -INFINITY ? top : kRefStart;
         } else {
           const bool raise = top > ref + kLazy;
           if (__any_sync(kFull, raise)) {

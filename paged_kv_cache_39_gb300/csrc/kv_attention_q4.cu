@@ -81,6 +81,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -635,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
         const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]}, a1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint32_t b0 = kPack ? b[j][n][0] & keep : b[j][n][0];
-          const uint32_t b1 = kPack ? b[j][n][1] & keep : b[j][n][1];
+          const uint32_t b0 = kPack ? times(b[j][n][0], keep) : b[j][n][0];
+          const uint32_t b1 = kPack ? times(b[j][n][1], keep) : b[j][n][1];
           mma16816(o[n][2 * j], a0, b0, b1);
           mma16816(o[n][2 * j + 1], a1, b0, b1);
         }
@@ -649,8 +653,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
       logits(0, 0, acc, true);
       logits(1, 1, acc, false);
       weights(half_tok, acc, b);
-      values(0, b, half_mask);
-      values(1, b, ~half_mask);
+      values(0, b, half_mask & 0x3c003c00u);
+      values(1, b, ~half_mask & 0x3c003c00u);
     } else {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {

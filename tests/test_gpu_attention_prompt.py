@@ -130,6 +130,39 @@ def test_keys_out_of_sight_may_hold_anything():
             assert torch.isfinite(later).all()
 
 
+def test_logits_of_minus_infinity_before_finite_ones():
+    """Keys whose logits are -inf for a whole tile, then ordinary ones far below 0."""
+    n, d = 300, 64
+    q = torch.ones((n, 1, d), device=dev()).to(BF16)
+    k = torch.full((n, 1, d), -40.0, device=dev()).to(BF16)
+    k[:160, 0, 5] = -float("inf")
+    v = normal((n, 1, d), 3)
+    got = kv.kv_attention_prompt(q, k, v, i32([0, n]))
+    for i in (160, 200, 299):   # equal logits: the mean of the values behind the infinite ones
+        want = v[160:i + 1].to(ref.F64).mean(0)
+        size = v[160:i + 1].to(ref.F64).abs().mean(0)
+        # equal weights are exactly 1: the sum's roundings (2^-24 each) and the output's
+        ref.check(got[i], want, want.abs() * 2.0 ** -8 + size * n * 2.0 ** -23)
+
+
+def test_no_key_at_all():
+    q, none = normal((70, 8, 128), 1), torch.empty((0, 2, 128), dtype=BF16, device=dev())
+    out = torch.full_like(q, 7.0)
+    err = kv.new_error_word(dev())
+    kv.kv_attention_prompt(q, none, none, i32([0, 60, 65]), i32([0, 0, 0]), out=out, err=err)
+    assert not out[:65].any() and (out[65:] == 7).all() and err.item() == 0
+    assert kv.kv_attention_prompt(none[:, :2], none, none, i32([0])).shape == (0, 2, 128)
+
+
+def test_more_requests_than_a_block_ranks():
+    """Up to 384 requests are ordered by their keys, more are taken as they come."""
+    rng = np.random.default_rng(11)
+    for count in (383, 384, 385, 1200):
+        new = rng.integers(0, 4, count)
+        total = new + rng.integers(0, 40, count)
+        run(list(new), list(total), 4, 2, 64, seed=count)
+
+
 def test_sequences_that_are_refused():
     q, k, v = normal((50, 4, 64), 1), normal((50, 1, 64), 2), normal((50, 1, 64), 3)
     good = kv.kv_attention_prompt(q, k, v, i32([0, 20, 50]))

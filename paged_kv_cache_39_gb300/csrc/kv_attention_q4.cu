@@ -38,9 +38,9 @@
 namespace kvp {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtas = 3;                  // per SM: 12 warps of 168 registers
+constexpr int kCtas = 1;                  // per SM: 12 warps of 168 registers, 3 per scheduler
 constexpr int kStages = 3;
 constexpr int kUnit = 32;                 // tokens of a unit
 constexpr int kWindow = 8 * kUnit;        // tokens of a table lookup
@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
     }
     __syncthreads();
   }
-  const int worker = blockIdx.x * kWarps + warp;
+  // neighbouring workers on neighbouring SMs: little work spreads over all of them
+  const int worker = warp * gridDim.x + blockIdx.x;
   // requests without a position: zeros
   for (int r = worker; r < a.num_reqs; r += gridDim.x * kWarps) {
     uint32_t ignore = 0;
@@ -751,34 +752,33 @@ __global__ void __launch_bounds__(256) join_q4_kernel(AttnArgs a) {
     return parts + (2 * (i * a.gang + (seg - round * a.gang)) + (i == i0 ? 1 : 0)) * kPart;
   };
 
-  float top = kRefStart;
-  for (int64_t i = i0 + threadIdx.x; i <= i1; i += blockDim.x) top = fmaxf(top, part(i)[D]);
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-  if (warps > 1) {
-    if (lane == 0) s_top[warp] = top;
-    __syncthreads();
-    for (int w = 0; w < warps; ++w) top = fmaxf(top, s_top[w]);
-  }
-  float acc[G] = {}, l = 0.f;
+  // one pass: a part's reference, sum and values are loaded together
+  float acc[G] = {}, l = 0.f, top = kRefStart;
 #pragma unroll 4
   for (int64_t i = i0 + warp; i <= i1; i += warps) {
     const float* p = part(i);
-    const float f = ex2(p[D] - top);
-    l += f * p[D + 1];
+    const float ref = p[D], more = p[D + 1];
+    const float up = fmaxf(top, ref), f = ex2(top - up), g = ex2(ref - up);
+    top = up;
+    l = l * f + more * g;
 #pragma unroll
-    for (int j = 0; j < G; ++j) acc[j] += f * p[32 * j + lane];
+    for (int j = 0; j < G; ++j) acc[j] = acc[j] * f + p[32 * j + lane] * g;
   }
   if (warps > 1) {
+    if (lane == 0) s_top[warp] = top, s_l[warp] = l;
 #pragma unroll
     for (int j = 0; j < G; ++j) s_o[warp][32 * j + lane] = acc[j];
-    if (lane == 0) s_l[warp] = l;
     __syncthreads();
     if (warp != 0) return;
-    for (int w = 1; w < warps; ++w) {
-      l += s_l[w];
+    for (int w = 1; w < warps; ++w) top = fmaxf(top, s_top[w]);
+    l = 0.f;
 #pragma unroll
-      for (int j = 0; j < G; ++j) acc[j] += s_o[w][32 * j + lane];
+    for (int j = 0; j < G; ++j) acc[j] = 0.f;
+    for (int w = 0; w < warps; ++w) {
+      const float f = ex2(s_top[w] - top);
+      l += f * s_l[w];
+#pragma unroll
+      for (int j = 0; j < G; ++j) acc[j] += f * s_o[w][32 * j + lane];
     }
   }
   const float inv = l == 0.f ? 0.f : kCentred / l;

@@ -93,7 +93,8 @@ enum kv_error_bits {
 
 /*
  * Bounded waits.  Only the two bulk-copy calls (kv_cache_gather_bulk,
- * kv_copy_blocks_bulk) wait on the copy engine, and every such wait gives up
+ * kv_copy_blocks_bulk) wait on the copy engine, and kv_attention_prompt on it
+ * and on the matrix unit; every such wait gives up
  * after 1 s of GPU time (the global nanosecond timer) or 2^22 tries,
  * whichever comes first; a CTA that gave up waits once more, with the same
  * bound, for each of its own loads still in flight, then ends.  A healthy
@@ -532,12 +533,13 @@ int kv_qk_norm_rope_write(const void* query, int64_t query_stride, const void* k
  * With m query and n key rows, query i sees the keys j <= i + n - m:
  *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j.
  * A query that sees no key gets zeros.  Keys a query does not see contribute
- * nothing to it, whatever they hold; a NaN or infinity in a value row that some
- * query of the same 128-key tile does not see makes the outputs of those that
- * do see it NaN in that channel.  Query rows of no request are left
- * as they were.  A request whose rows are out of order or out of range sets
- * KV_ERR_BAD_QSL and is skipped.  Products and sums are held in 32 bits; the
- * weights are rounded to bf16 for their product with V.
+ * nothing to it, whatever they hold.  A NaN or an infinity in a value row makes
+ * that channel NaN or infinite for the queries that see the row.  Query rows of
+ * no request are left as they were.  A request whose rows are out of order or
+ * out of range sets KV_ERR_BAD_QSL and is skipped; query rows that two requests
+ * claim hold either's result.  Products and sums are held in 32 bits; the
+ * weights are rounded to bf16 for their product with V.  Every wait of the
+ * kernel is bounded (see "Bounded waits").
  * Errors: KV_EINVAL for null or misaligned pointers, negative sizes, a stride
  * below the row, num_q_heads not a multiple of num_kv_heads, a scale that is
  * not positive and finite, out overlapping an input; KV_EUNSUPPORTED for head_dim
@@ -616,8 +618,11 @@ int kv_cache_gather_q4(const void* k_cache, const void* v_cache, int32_t layer,
  * positions past the table row with KV_ERR_BAD_POSITION.  A request with no
  * position left, or with start < 0 or end < start (KV_ERR_BAD_POSITION), gets
  * zeros.
+ * Queries of 2^100 and more and value scales above 2^100 may give infinities or
+ * NaN.  The same call gives the same bits every time.
  * Errors: as kv_attention_prompt and the 4-bit cache; KV_EINVAL for a workspace
- * that is missing, misaligned or too small.
+ * that is missing, misaligned or too small; KV_EUNSUPPORTED for a layer of more
+ * than 2^36 bytes in one cache.
  */
 int kv_attention_q4(const void* query, int64_t query_stride, const void* k_cache,
                     const void* v_cache, int32_t layer, int32_t num_layers, int64_t num_blocks,

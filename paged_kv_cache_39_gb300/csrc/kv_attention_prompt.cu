@@ -27,10 +27,17 @@
 // CTA per SM.
 //
 // Hidden keys.  A hidden logit is replaced, so a NaN there is gone, but 0 * NaN in
-// P V is NaN.  So in the tiles where some key is hidden from some row (one or two
+// P V is NaN.  So in the tiles where some key is hidden from some row (one to three
 // per CTA), V values that are not finite are set to 0 in shared memory, and the
 // first key that held one is kept per channel: rows that see that key
 // get NaN in the epilogue.  Rows behind the sequence are set to 0 outright.
+//
+// Measured (32 query heads, 8 KV heads of 128 channels): one prompt of 32768 tokens 5.5 ms (1600
+// TFLOP/s, at the card's power limit, 1.92 GHz), 16 chunks of 9 to 1855 tokens behind up to 7685
+// 383 us (1310 TFLOP/s: the 7 CTAs that an SM runs one after another each take 4 us to start
+// and to write, and the last wave is not full), 77 tokens 8.5 us.  Per 128 keys a CTA's two tiles
+// take 3000 cycles: 2048 of matrix instructions; a tile's softmax is 1140, beside the other
+// tile's products.
 #include <cuda_bf16.h>
 
 #include "kv_tc.cuh"

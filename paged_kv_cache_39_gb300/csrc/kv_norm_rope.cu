@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 10) norm_rope_kernel(NormRopeArgs a)
   constexpr int kUnit = kSteps * kHeads;     // heads of a warp
   const int lane = threadIdx.x & 31;
   const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int64_t t = unit / a.units;
+  const int64_t t = unit <= INT32_MAX ? (uint32_t)unit / (uint32_t)a.units : unit / a.units;
   if (t >= a.num_tokens) return;
   // which heads: query units, then key units, then value units
   int u = (int)(unit - t * a.units);

@@ -8,6 +8,8 @@
 // 2^-10 away from every one, and the integer q nearest to x times an approximate 1 / s (within
 // 2^-22) is right unless x / s is a tie.  Then, and only then, 2 |x - q s| == s, which is exact in
 // 32 bits; groups with a tie are done again value by value.  No clamp is needed.
+// 8 lanes quantise a head's K and V rows: 8192 tokens of 8 x 128 take 18 us (43 MB), bound by the
+// instructions (800 a warp; 1290 and 25 us with divisions and value by value).
 #include "kv_q4.cuh"
 
 namespace kvp {
@@ -183,8 +185,9 @@ __global__ void __launch_bounds__(kWriteThreads) write_q4_kernel(WriteArgs a) {
 // then warps walk the output rows, kGatherRows at a time.  Eight lanes stand for two of the
 // rows and go through their heads, so the block and the position in it are resolved once per
 // row and a head is one addition to each address.  The output's bytes bound it (256 of 328 a
-// head at 128 channels); what stood in the way was the conversion, at 11 instructions for two
-// values one by one (86 us for 75k rows of 8 x 128, K and V): now 5, in bf16 pairs.
+// head at 128 channels): 75k rows of 8 x 128, K and V, take 81 us, 4.9 TB/s of these bytes, where
+// a plain stream that writes four bytes for one it reads reaches 5.6 to 5.85.  The conversion is
+// 5 instructions for two values, in bf16 pairs (11 one by one, and 86 us).
 
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 8;

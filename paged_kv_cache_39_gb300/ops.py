@@ -684,7 +684,8 @@ def kv_attention_q4(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     of its 4-bit cache, found through its block table.
 
     query [R, q_heads, D] bf16, any token stride; ``scale`` defaults to D ** -0.5.  The
-    workspace the split needs is allocated here, once per call (or prepared call).
+    workspace the split needs is allocated here, once per call; a prepared call keeps one
+    with its output, so give each stream (or graph) that runs beside another its own.
     Returns out [R, q_heads, D]; a request without a visible position gets zeros."""
     dev = _device_of(query, "query")
     R, Hq, D, qs = _rows_of(query, "query", dev)

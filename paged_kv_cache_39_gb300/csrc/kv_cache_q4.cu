@@ -206,6 +206,7 @@ struct GatherArgs {
   __nv_bfloat16* k_out;
   __nv_bfloat16* v_out;
   int64_t out_rows;
+  int32_t part_log2, part_heads;  // 2^part_log2 warps share a group of rows, part_heads each
   int32_t* err;
 };
 
@@ -309,9 +310,13 @@ __global__ void __launch_bounds__(kGatherThreads) gather_q4_kernel(GatherArgs a)
   asm volatile("mov.b32 %0, 0x43004300;" : "=r"(exponent));
   const int64_t warp0 = ((int64_t)blockIdx.x * kGatherThreads + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * kGatherThreads) >> 5;
-  for (int64_t o0 = warp0 * kGatherRows; o0 < rows; o0 += nwarps * kGatherRows) {
+  const int64_t items = ((rows + kGatherRows - 1) / kGatherRows) << a.part_log2;
+  for (int64_t item = warp0; item < items; item += nwarps) {
+    const int64_t o0 = (item >> a.part_log2) * kGatherRows;
+    const int h0 = (int)(item & ((1 << a.part_log2) - 1)) * a.part_heads;
+    const int h1 = min(H, h0 + a.part_heads);
     const int nr = (int)(rows - o0 < kGatherRows ? rows - o0 : kGatherRows);
-    // rows lane / 8 and lane / 8 + 4: where their codes and scales are for head 0, or zero rows
+    // rows lane / 8 and lane / 8 + 4: where their codes and scales are for head h0, or zero rows
     const uint8_t *kc[2], *vc[2];
     int64_t to_scales[2];
     bool in[2], full[2];
@@ -338,16 +343,16 @@ __global__ void __launch_bounds__(kGatherThreads) gather_q4_kernel(GatherArgs a)
         continue;
       }
       full[n] = true;
-      const int64_t at = a.at.record(b, 0) + a.at.codes((int32_t)off) + 4 * G * (lane & 3);
+      const int64_t at = a.at.record(b, h0) + a.at.codes((int32_t)off) + 4 * G * (lane & 3);
       kc[n] = a.k_cache + at;
       vc[n] = a.v_cache + at;
       to_scales[n] = a.at.scales((int32_t)off) - a.at.codes((int32_t)off) - 4 * G * (lane & 3);
     }
-    __nv_bfloat16* ko = a.k_out + (o0 + (lane >> 3)) * H * (32 * G) + channel;
-    __nv_bfloat16* vo = a.v_out + (o0 + (lane >> 3)) * H * (32 * G) + channel;
+    __nv_bfloat16* ko = a.k_out + ((o0 + (lane >> 3)) * H + h0) * (32 * G) + channel;
+    __nv_bfloat16* vo = a.v_out + ((o0 + (lane >> 3)) * H + h0) * (32 * G) + channel;
     const int64_t four = (int64_t)4 * H * (32 * G);
 #pragma unroll 2
-    for (int h = 0; h < H; ++h) {
+    for (int h = h0; h < h1; ++h) {
       PackedRow<G> k[2], v[2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -432,13 +437,18 @@ extern "C" int kv_cache_gather_q4(const void* k_cache, const void* v_cache, int3
                Q4Layout{(int64_t)layer * num_blocks, num_blocks, block_size, num_kv_heads, head_dim},
                BlockDiv::make(block_size), block_table, table_stride, gather_start, gather_end, num_reqs,
                static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), out_rows,
-               d_err};
+               0, 0, d_err};
   auto kernel = head_dim == 128 ? gather_q4_kernel<4> : gather_q4_kernel<2>;
   const size_t smem = sizeof(int64_t) * (num_reqs + 1) + sizeof(int32_t) * num_reqs;
   const int64_t rows_per_cta = (kGatherThreads / 32) * kGatherRows;
   const int64_t need = (out_rows + rows_per_cta - 1) / rows_per_cta;
   const int64_t cap = (int64_t)sm_count() * (2048 / kGatherThreads);
-  const int grid = (int)(need < 1 ? 1 : (need < cap ? need : cap));
+  // Few rows: their heads are spread over more warps, until the GPU is full or a warp has one
+  // (256 rows of 8 heads: 8.3 -> 3.9 us).
+  while ((2 << a.part_log2) <= num_kv_heads && (need << a.part_log2) * 2 <= cap) ++a.part_log2;
+  a.part_heads = (num_kv_heads + (1 << a.part_log2) - 1) >> a.part_log2;
+  const int64_t parts = need << a.part_log2;
+  const int grid = (int)(need < 1 ? 1 : (parts < cap ? parts : cap));
   if (smem + kGatherStaticSmem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
           cudaSuccess)

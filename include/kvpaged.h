@@ -537,14 +537,16 @@ int kv_qk_norm_rope_write(const void* query, int64_t query_stride, const void* k
  * that channel NaN or infinite for the queries that see the row.  Query rows of
  * no request are left as they were.  A request whose rows are out of order or
  * out of range sets KV_ERR_BAD_QSL and is skipped; query rows that two requests
- * claim hold either's result.  Products and sums are held in 32 bits; the
+ * claim (with such a one between them) hold either's result, and where the requests
+ * claim more than num_q_tokens rows together, some are left as they were.  Products and sums are held in 32 bits; the
  * weights are rounded to bf16 for their product with V.  Every wait of the
  * kernel is bounded (see "Bounded waits").
  * Errors: KV_EINVAL for null or misaligned pointers, negative sizes, a stride
  * below the row, num_q_heads not a multiple of num_kv_heads, a scale that is
  * not positive and finite, out overlapping an input; KV_EUNSUPPORTED for head_dim
  * above 128 or not a multiple of 8, a stride not a multiple of 8, more than 128
- * query heads per KV head, num_q_heads > 4096, num_reqs > KV_MAX_GATHER_REQS.
+ * query heads per KV head, num_q_heads > 4096, num_reqs > KV_MAX_GATHER_REQS, more
+ * than KV_MAX_TOKENS query or key rows.
  */
 int kv_attention_prompt(const void* query, int64_t query_stride, const void* key,
                         int64_t key_stride, const void* value, int64_t value_stride,

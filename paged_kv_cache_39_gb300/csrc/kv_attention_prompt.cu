@@ -32,6 +32,13 @@
 // first key that held one is kept per channel: rows that see that key
 // get NaN in the epilogue.  Rows behind the sequence are set to 0 outright.
 //
+// Few rows behind many keys.  Where the tile pairs leave SMs idle, a cluster of up to 16 CTAs
+// takes a pair, each CTA a run of its key tiles.  The CTAs then leave their accumulators, references
+// and sums in their own shared memory, and each joins a share of the rows from all of them:
+//   o_i = sum_c f_c O_c / sum_c f_c s_c,  f_c = 2^(ref_c - max ref).
+// No workspace, no atomics: the same call gives the same bits.  The join costs 3 us; 16 tokens
+// behind 8192 take 15 us instead of 74, behind 65536 58 instead of 558.
+//
 // Measured (32 query heads, 8 KV heads of 128 channels): one prompt of 32768 tokens 5.5 ms (1600
 // TFLOP/s, at the card's power limit, 1.92 GHz), 16 chunks of 9 to 1855 tokens behind up to 7685
 // 383 us (1310 TFLOP/s: the 7 CTAs that an SM runs one after another each take 4 us to start
@@ -39,6 +46,9 @@
 // take 3000 cycles: 2048 of matrix instructions; a tile's softmax is 1140, beside the other
 // tile's products.
 #include <cuda_bf16.h>
+
+#include <mutex>
+#include <type_traits>
 
 #include "kv_tc.cuh"
 
@@ -49,10 +59,13 @@ constexpr int kTile = 128;                 // query rows of a tile, keys of a K/
 constexpr int kThreads = 384;
 constexpr int kScrubThreads = 64;
 constexpr int kEdges = 3;                  // K/V tiles a CTA's rows see in part: 256 tokens span at most 3
+constexpr int kSplitMax = 16;              // the largest cluster
+constexpr int kSplitFrom = 6;              // K/V tiles from which on a split pays for its join (3 us)
+constexpr int kSplitTiles = 2;             // least of them that a CTA takes
 constexpr float kLazy = 8.0f;              // log2 of the most a weight may pass the reference
 constexpr float kRefStart = -1e30f;        // of a row with no finite logit yet: below every other
-// Registers: 384 threads x 168 at launch = 256 x 208 + 128 x 88.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+// Registers: 384 threads x 168 at launch = 256 x 200 + 128 x 104.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 
 struct PromptArgs {
   const int32_t* q_start;
@@ -60,6 +73,7 @@ struct PromptArgs {
   int32_t num_reqs, nq, nk, q_heads, kv_heads, head_dim;
   int32_t group, tq;       // query heads per KV head, tokens per tile
   int32_t items;           // upper bound of (request, tile pair), the grid's extent per head
+  int32_t split;           // CTAs of a cluster, which share a tile pair's keys
   float scale_log2;
   __nv_bfloat16* out;
   int32_t* err;
@@ -80,6 +94,10 @@ struct Smem {
   static constexpr int kBad = kBars + kNumBars * 8;         // int[DP]: first key not finite
   static constexpr int kMisc = kBad + DP * 4;
   static constexpr int kBytes = kMisc + 64 + 1024;          // + alignment of the base
+  // for the join of a split: fp32 accumulators and (reference, sum) of 2 x 128 rows, where Q, K
+  // and V were
+  static constexpr int kStats = 2 * kTile * DP * 4;
+  static_assert(kStats + 2 * kTile * 8 <= kBars, "");
 };
 
 struct Work {
@@ -98,7 +116,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-template <int DP>
+// kSplit: in clusters of `split` CTAs (a kernel of its own, so that the other has neither the
+// join's registers nor its code in its way: 5.46 against 5.63 ms at 32768 tokens).
+template <int DP, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map, PromptArgs a) {
@@ -147,12 +167,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     mbar_fence_init();
     *abort = 0;
     *any_bad = 0;
-    s_work->m = 0;
+    *s_work = Work{0, 0, 0, 0, 0};  // of a CTA that no pair is left for
   }
   if (tid < DP) bad[tid] = INT32_MAX;
-  if (warp == 9) tmem_alloc(tmem_ptr, 512);
   pdl_allow_next();
   pdl_wait();
+  if (warp == 9) tmem_alloc(tmem_ptr, 512);  // not before: what runs ahead may need it to end
 
   // Which pair of tiles is this?  The pairs are numbered by request, those with the most keys
   // first (as long as a thread can rank each of them), and inside a request from its last
@@ -165,11 +185,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   // that one head's K and V (16.8 MB at 32768 tokens) serve all CTAs at a time (5.60 against
   // 5.66 ms).
   const bool single = a.num_reqs == 1;
-  const int head = single ? blockIdx.x / a.items : blockIdx.x % a.kv_heads;
-  const int want = single ? blockIdx.x % a.items : blockIdx.x / a.kv_heads;
+  const int block = kSplit ? (int)(blockIdx.x / (unsigned)a.split) : (int)blockIdx.x;
+  const int rank_in = kSplit ? (int)blockIdx.x - block * a.split : 0;
+  const int head = single ? block / a.items : block % a.kv_heads;
+  const int want = single ? block % a.items : block / a.kv_heads;
   uint32_t err = 0;
   {
-    __shared__ int warp_sum[kThreads / 32];
+    __shared__ int64_t warp_sum[kThreads / 32];
     int* keys_of = reinterpret_cast<int*>(smem);                     // [num_reqs], and
     int4* ranked = reinterpret_cast<int4*>(smem + kThreads * sizeof(int));  // the same: where Q will be
     const int pair = 2 * a.tq;
@@ -184,7 +206,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     };
     auto pairs = [&](const Work& x) { return (int)(((int64_t)x.m + pair - 1) / pair); };
     Work mine = {0, 0, 0, 0, 0};  // with `rank`: the request of this thread's rank
-    int count = 0;
+    int64_t count = 0;  // 64 bits: requests that claim the same rows may count more than there are
     if (rank) {
       if (tid < a.num_reqs) {
         mine = describe(tid);
@@ -207,17 +229,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     } else {
       for (int r = r_lo; r < r_hi; ++r) count += pairs(describe(r));
     }
-    const int incl = warp_inclusive_scan<int>(count);
+    const int64_t incl = warp_inclusive_scan<int64_t>(count);
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int at = incl - count;
+    int64_t at = incl - count;
     for (int w = 0; w < warp; ++w) at += warp_sum[w];
     if (want >= at && want < at + count) {
       if (!rank) {
         int r = r_lo;
         for (mine = describe(r); want >= at + pairs(mine); mine = describe(++r)) at += pairs(mine);
       }
-      mine.t0 = (pairs(mine) - 1 - (want - at)) * pair;
+      mine.t0 = (pairs(mine) - 1 - (int)(want - at)) * pair;
       *s_work = mine;
     }
     __syncthreads();
@@ -233,15 +255,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   const int last = min(w.t0 + 2 * a.tq, w.m) - 1;                 // last token here
   const int keys = max(0, min(w.n, ahead + last + 1));            // keys the last token sees
   const int tiles = (keys + kTile - 1) / kTile;
+  // this CTA's share of them: [first, end)
+  const int parts = kSplit && tiles >= kSplitFrom ? min(a.split, tiles / kSplitTiles) : 1;
+  const int first = kSplit && rank_in < parts ? tiles * rank_in / parts : 0;
+  const int end = !kSplit ? tiles : rank_in < parts ? tiles * (rank_in + 1) / parts : 0;
   const int whole = max(0, ahead + w.t0 + 1) / kTile;             // tiles every row sees whole
   const bool two = w.t0 + a.tq < w.m;
-  const bool work = w.m > 0 && tiles > 0;
+  const bool work = w.m > 0 && end > first;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, *tmem_ptr, 0);
 
-  if (w.m > 0 && tiles == 0) {  // no query here sees a key
+  if (w.m > 0 && tiles == 0 && rank_in == 0) {  // no query here sees a key
     const int64_t row = (int64_t)a.group * a.head_dim;
     const int vecs = (int)(row / 8);
     for (int64_t i = tid; i < (int64_t)(last + 1 - w.t0) * vecs; i += kThreads) {
@@ -269,15 +295,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       }
       int u = 0, slot = 0, turn = 0;  // K and V tiles alternate in the ring
 #pragma unroll 1
-      for (; u < 2 * tiles; ++u) {
+      for (; u < 2 * (end - first); ++u) {
         if (turn > 0 && !mbar_wait_role(&empty[slot], (turn - 1) & 1, abort)) break;
         const bool is_v = u & 1;
-        uint64_t* bar = is_v && (u >> 1) >= whole ? &edge[(u >> 1) - whole] : &full[slot];
+        const int j = first + (u >> 1);
+        uint64_t* bar = is_v && j >= whole ? &edge[j - whole] : &full[slot];
         if (leader) {
           mbar_arrive_expect_tx(bar, L::kTileBytes);
           for (int c = 0; c < DP / 64; ++c)
             tma_load_3d(smem + L::kRing + slot * L::kTileBytes + c * (kTile * 128),
-                        is_v ? &v_map : &k_map, 64 * c, head, w.k0 + (u >> 1) * kTile, bar);
+                        is_v ? &v_map : &k_map, 64 * c, head, w.k0 + j * kTile, bar);
         }
         if (++slot == L::kSlots) {
           slot = 0;
@@ -287,7 +314,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       if (*abort != 0) {  // bounded wait for the copies still in flight
         mbar_wait_bounded(q_full, 0);
         for (int x = max(0, u - L::kSlots); x < u; ++x) {
-          if ((x & 1) && (x >> 1) >= whole) mbar_wait_bounded(&edge[(x >> 1) - whole], 0);
+          if ((x & 1) && first + (x >> 1) >= whole) mbar_wait_bounded(&edge[first + (x >> 1) - whole], 0);
           else mbar_wait_bounded(&full[x % L::kSlots], (x / L::kSlots) & 1);
         }
       }
@@ -330,19 +357,20 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       }
       int sv = 1, sk = 2, pv = 0, pk = 0;  // slots of V_j and K_{j+1}, parities of their phases
 #pragma unroll 1
-      for (int j = 0; ok && j < tiles; ++j) {
-        const bool more = j + 1 < tiles;
+      for (int j = first; ok && j < end; ++j) {
+        const bool more = j + 1 < end;
+        const uint32_t phase = (j - first) & 1;
         // at the causal edge V is waited for through the warps that check it
         ok = j < whole ? mbar_wait_role(&full[sv], pv, abort)
                        : mbar_wait_role(&v_ok[j - whole], 0, abort);
         if (ok && more) ok = mbar_wait_role(&full[sk], pk, abort);
 #pragma unroll 1
         for (int t = 0; ok && t < nt; ++t) {
-          ok = mbar_wait_role(&p_full[2 * t], j & 1, abort);
+          ok = mbar_wait_role(&p_full[2 * t], phase, abort);
           if (!ok) break;
           tc_fence_after();
-          values(t, sv, j > 0, 0);
-          ok = mbar_wait_role(&p_full[2 * t + 1], j & 1, abort);
+          values(t, sv, j > first, 0);
+          ok = mbar_wait_role(&p_full[2 * t + 1], phase, abort);
           if (!ok) break;
           tc_fence_after();
           values(t, sv, true, 1);
@@ -372,8 +400,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     } else if (warp >= 10 && work) {
       // -------------------------------------------------------------- V at the causal edge
       const int st = tid - 10 * 32;
-      for (int j = whole; j < tiles; ++j) {
-        const int slot = (2 * j + 1) % L::kSlots;
+      for (int j = max(first, whole); j < end; ++j) {
+        const int slot = (2 * (j - first) + 1) % L::kSlots;
         if (!mbar_wait_role(&edge[j - whole], 0, abort)) break;
         unsigned char* tile = smem + L::kRing + slot * L::kTileBytes;
 #pragma unroll 1
@@ -421,6 +449,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       }
       mbar_arrive(scrubbed);
     }
+    if constexpr (kSplit) {  // the softmax warps' join
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = warp >> 2;  // the tile
@@ -437,8 +469,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       float ref = 0.f;
       uint64_t part[2] = {0, 0};  // sums of weights, two by two
       bool ok = true;
-      for (int j = 0; j < tiles; ++j) {
-        ok = mbar_wait_role(&s_full[t], j & 1, abort);
+      for (int j = first; j < end; ++j) {
+        ok = mbar_wait_role(&s_full[t], (j - first) & 1, abort);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         tc_fence_after();
@@ -458,7 +490,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
 #pragma unroll
           for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[x + y]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        if (j == 0) {
+        if (j == first) {
           ref = top > -INFINITY ? top : kRefStart;
         } else {
           const bool raise = top > ref + kLazy;
@@ -514,6 +546,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       // -------------------------------------------------------------- epilogue
       if (ok) ok = __all_sync(kFull, mbar_wait_role(&o_full[t], 0, abort));
       if (ok) ok = __all_sync(kFull, mbar_wait_role(scrubbed, 0, abort));
+      // a split's accumulators go where the other tile's products may still read K and V
+      if (ok && parts > 1 && two) ok = __all_sync(kFull, mbar_wait_role(&o_full[1], 0, abort));
       if (ok) {
         tc_fence_after();
         const bool check = *any_bad != 0;
@@ -529,6 +563,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             for (int x = 0; x < 32; ++x)
               if (seen > bad[32 * b + x]) o[x] = 0x7fc00000u;
           }
+          if (parts > 1) {  // 16-byte piece x of a row at (x + row): no bank twice in 8 rows
+            float4* to = reinterpret_cast<float4*>(smem) + (t * kTile + row) * (DP / 4);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              to[(8 * b + x + row) & (DP / 4 - 1)] =
+                  make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                              __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+            continue;
+          }
 #pragma unroll
           for (int x = 0; x < 32; x += 8) {
             uint4 y;
@@ -540,7 +583,70 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
               *reinterpret_cast<uint4*>(out + 32 * b + x) = y;
           }
         }
+        if (parts > 1)
+          reinterpret_cast<float2*>(smem + L::kStats)[t * kTile + row] = make_float2(ref, sum);
       }
+    }
+    if constexpr (kSplit) {
+      // -------------------------------------------------------------- join of a split
+      cluster_sync();
+      if (parts > 1 && w.m > 0) {
+        // rows rank_in, rank_in + CTAs, .., B to a warp at a time, 4 channels to a lane; all of
+        // their parts are asked for (a far read takes about 0.5 us) before the first is used
+        const int rows = two ? 2 * kTile : kTile;
+        const int piece = lane & (DP / 4 - 1);
+        auto join = [&](auto at_once) {
+          constexpr int B = decltype(at_once)::value, C = kSplitMax / B;
+          for (int x0 = warp; x0 * a.split + rank_in < rows; x0 += 8 * B) {
+            float2 rs[B][C];
+            float4 o[B][C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+              const uint32_t base = cluster_addr(smem, min(c, parts - 1));
+#pragma unroll
+              for (int b = 0; b < B; ++b) {
+                const int x = (x0 + 8 * b) * a.split + rank_in;
+                rs[b][c] = make_float2(kRefStart, 0.f);
+                o[b][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c < parts && x < rows) {
+                  rs[b][c] = cluster_ld2(base + L::kStats + x * 8);
+                  o[b][c] = cluster_ld4(base + (x * (DP / 4) + ((piece + x) & (DP / 4 - 1))) * 16);
+                }
+              }
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+              const int x = (x0 + 8 * b) * a.split + rank_in;
+              const int row = x & (kTile - 1), tok = row / a.group, g = row - tok * a.group;
+              const int i = w.t0 + (x >> 7) * a.tq + tok;
+              if (x >= rows || tok >= a.tq || i >= w.m) continue;
+              float top = rs[b][0].x;
+#pragma unroll
+              for (int c = 1; c < C; ++c) top = fmaxf(top, rs[b][c].x);
+              float sum = 0.f;
+              uint64_t y[2] = {};
+#pragma unroll
+              for (int c = 0; c < C; ++c) {  // absent parts: nothing times at most 1
+                const float f = ex2(rs[b][c].x - top);
+                sum = fmaf(f, rs[b][c].y, sum);
+                y[0] = fma2(pair(f, f), pair(o[b][c].x, o[b][c].y), y[0]);
+                y[1] = fma2(pair(f, f), pair(o[b][c].z, o[b][c].w), y[1]);
+              }
+              const float inv = sum == 0.f ? 0.f : 1.f / sum;
+              float z[4];
+              unpair(y[0], z[0], z[1]);
+              unpair(y[1], z[2], z[3]);
+              if (lane < DP / 4 && 4 * piece < a.head_dim)
+                *reinterpret_cast<uint2*>(
+                    a.out + ((int64_t)(w.q0 + i) * a.q_heads + head * a.group + g) * a.head_dim + 4 * piece) =
+                    make_uint2(pack_bf16(z[0] * inv, z[1] * inv), pack_bf16(z[2] * inv, z[3] * inv));
+            }
+          }
+        };
+        if (parts > 4) join(std::integral_constant<int, 1>{});
+        else join(std::integral_constant<int, 4>{});
+      }
+      cluster_sync();  // no CTA ends while another reads its shared memory
     }
   }
   __syncwarp();
@@ -553,16 +659,75 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   }
 }
 
+// How many clusters of each size run at once on the current device: the SMs come in groups of
+// 16 to 20, of which a cluster takes its CTAs (152 SMs hold fewer than 19 clusters of 8).
 template <int DP>
+int clusters_at_once(int size) {
+  static std::mutex mu;
+  static int cached[64][kSplitMax + 1] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = cached[dev][size];
+  if (n == 0) {
+    auto kernel = prompt_kernel<DP, true>;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<DP>::kBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int found = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem<DP>::kBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&found, kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      found = 0;
+    }
+    n = found > 0 ? found : -1;
+  }
+  return n;
+}
+
+// CTAs of a cluster: as many as let all `pairs` run at once and would have kSplitTiles each in a
+// request that had all of the keys.
+template <int DP>
+int choose_split(int64_t pairs, int64_t keys) {
+  const int64_t tiles = (keys + kTile - 1) / kTile;
+  if (tiles < kSplitFrom || 2 * pairs > sm_count()) return 1;
+  int64_t split = tiles / kSplitTiles < kSplitMax ? tiles / kSplitTiles : kSplitMax;
+  if (split > sm_count() / pairs) split = sm_count() / pairs;
+  while (split > 1 && clusters_at_once<DP>((int)split) < pairs) --split;
+  return (int)split;
+}
+
+template <int DP, bool kSplit>
 int launch(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
            cudaStream_t stream) {
-  auto kernel = prompt_kernel<DP>;
+  auto kernel = prompt_kernel<DP, kSplit>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Smem<DP>::kBytes) != cudaSuccess)
     return KV_ECUDA;
-  const int64_t ctas = (int64_t)a.items * a.kv_heads;
+  if (kSplit && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                    cudaSuccess)
+    return KV_ECUDA;
+  const int64_t ctas = (int64_t)a.items * a.kv_heads * a.split;
   if (ctas > INT32_MAX) return KV_EUNSUPPORTED;
-  return launch_pdl(kernel, (unsigned)ctas, kThreads, Smem<DP>::kBytes, stream, q, k, v, a);
+  return launch_pdl_clusters(kernel, (unsigned)ctas, (unsigned)a.split, kThreads,
+                             Smem<DP>::kBytes, stream, q, k, v, a);
+}
+
+template <int DP>
+int launch(PromptArgs a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+           cudaStream_t stream) {
+  a.split = choose_split<DP>((int64_t)a.items * a.kv_heads, a.nk);
+  return a.split > 1 ? launch<DP, true>(a, q, k, v, stream) : launch<DP, false>(a, q, k, v, stream);
 }
 
 }  // namespace
@@ -581,7 +746,8 @@ extern "C" int kv_attention_prompt(const void* query, int64_t query_stride, cons
       !(scale > 0.f) || !(scale < INFINITY))
     return KV_EINVAL;
   if (head_dim % 8 != 0 || head_dim > 128 || num_q_heads / num_kv_heads > 128 ||
-      num_q_heads > 4096 || num_reqs > KV_MAX_GATHER_REQS)
+      num_q_heads > 4096 || num_reqs > KV_MAX_GATHER_REQS || num_q_tokens > KV_MAX_TOKENS ||
+      num_k_tokens > KV_MAX_TOKENS)
     return KV_EUNSUPPORTED;
   const int64_t q_row = (int64_t)num_q_heads * head_dim, k_row = (int64_t)num_kv_heads * head_dim;
   if (query_stride < q_row || key_stride < k_row || value_stride < k_row) return KV_EINVAL;
@@ -611,9 +777,11 @@ extern "C" int kv_attention_prompt(const void* query, int64_t query_stride, cons
                 keys ? num_k_tokens : num_q_tokens, keys ? num_kv_heads : num_q_heads, head_dim, 1,
                 kTile))
     return KV_ECUDA;
+  // sum of ceil(m_r / pair) over the requests with a row, of which there are `some` at most
+  const int some = num_reqs < num_q_tokens ? num_reqs : num_q_tokens;
+  const int64_t items = (int64_t)(num_q_tokens - some) / (2 * tq) + some;
   PromptArgs a{q_start_loc, k_start_loc, num_reqs, num_q_tokens, num_k_tokens, num_q_heads,
-               num_kv_heads, head_dim, group, tq,
-               (int32_t)((int64_t)num_q_tokens / (2 * tq) + num_reqs),
+               num_kv_heads, head_dim, group, tq, (int32_t)items, 1,
                scale * 1.44269504088896340736f, static_cast<__nv_bfloat16*>(out), d_err};
   return head_dim <= 64 ? launch<64>(a, q_map, k_map, v_map, stream)
                         : launch<128>(a, q_map, k_map, v_map, stream);

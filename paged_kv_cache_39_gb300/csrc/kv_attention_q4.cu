@@ -28,7 +28,7 @@
 //
 // Measured (32 query heads, 8 KV heads of 128 channels): 8 contexts of 131072 tokens 222 us
 // (1.21 GB, 5.4 TB/s), 256 contexts of 512 to 4096 tokens 130 us (0.64 GB, 4.9 TB/s), one of 1009
-// 10.9 us, of which the second kernel is 5.  A unit of 32 tokens of one head is 4608 bytes and about
+// 8.7 us, of which the second kernel is 2.5, one of 16384 13.6.  A unit of 32 tokens of one head is 4608 bytes and about
 // 600 instructions of a warp, half of them on the logic pipe (taking the codes apart); with 12
 // warps an SM issues 2.3 of 4 a cycle.  16 warps of 128 registers spill (253 us), 14 leave two
 // of the four schedulers one warp short (312 us).
@@ -38,6 +38,8 @@
 // t + 12 it holds of V.  K rows are stored in the order of rho and V's 16-byte pieces
 // are xor-ed with the token, which makes every shared-memory read free of bank conflicts.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "kv_q4.cuh"
 
@@ -731,65 +733,95 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
 }
 
 // Join: out = sum_i 2^(ref_i - top) o_i / sum_i 2^(ref_i - top) l_i over the parts the
-// workers left of one (request, query head).  Its warps take the parts in turn, each
-// lane D / 32 channels; which worker holds which part follows from the offsets alone.
-template <int G, int NQ>
-__global__ void __launch_bounds__(256) join_q4_kernel(AttnArgs a) {
-  constexpr int D = 32 * G;
-  __shared__ float s_o[8][D], s_l[8], s_top[8];
+// workers left of one (request, query head); which worker holds which part follows from the
+// offsets alone.  W warps take the parts in turn, the first kFirst of them and then 8 at a
+// time, so that a long row of parts costs few round trips: the 228 of one context of 16384
+// tokens take 4 us with 16 warps, 11 with 8 warps and 4 parts at a time.  Each lane has D / 32
+// channels.
+template <int G, int NQ, int W>
+__global__ void __launch_bounds__(32 * W) join_q4_kernel(AttnArgs a) {
+  constexpr int D = 32 * G, kFirst = W == 1 ? 2 : 4, kMore = 8;
+  __shared__ float s_o[W][D], s_l[W], s_top[W];
   pdl_allow_next();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = blockIdx.x / a.q_heads, qh = blockIdx.x - r * a.q_heads;
   const int rounds = a.at.kv_heads * a.passes / a.gang;
-  const int64_t at = a.offsets[r], total = a.offsets[a.num_reqs];
-  const int64_t units = (a.offsets[r + 1] - at) / rounds;
-  const int64_t share = (total + a.gangs - 1) / a.gangs;
-  if (units == 0) return;  // zeros, already written
+  const int64_t at = a.offsets[r], after = a.offsets[r + 1], total = a.offsets[a.num_reqs];
+  if (after == at) return;  // zeros, already written
   const int head = qh / a.group, qi = qh - head * a.group;
   const int seg = head * a.passes + qi / NQ, round = seg / a.gang;
-  const int64_t lo = at + round * units;
-  const int64_t i0 = lo / share, i1 = (lo + units - 1) / share;
+  int64_t i0, i1;
+  if (total <= INT32_MAX) {  // 32-bit divisions are a third of a microsecond faster
+    const uint32_t units = (uint32_t)(after - at) / (uint32_t)rounds;
+    const uint32_t share = ((uint32_t)total + a.gangs - 1) / (uint32_t)a.gangs;
+    const uint32_t lo = (uint32_t)at + round * units;
+    i0 = lo / share, i1 = (lo + units - 1) / share;
+  } else {
+    const int64_t units = (after - at) / rounds, share = (total + a.gangs - 1) / a.gangs;
+    const int64_t lo = at + round * units;
+    i0 = lo / share, i1 = (lo + units - 1) / share;
+  }
   if (i0 == i1) return;    // one worker saw it whole
   const float* parts = a.parts + (int64_t)(qi % NQ) * (D + 2);
   constexpr int64_t kPart = NQ * (D + 2);
-  auto part = [&](int64_t i) {
-    return parts + (2 * (i * a.gang + (seg - round * a.gang)) + (i == i0 ? 1 : 0)) * kPart;
-  };
 
-  // one pass: a part's reference, sum and values are loaded together
   float acc[G] = {}, l = 0.f, top = kRefStart;
-#pragma unroll 4
-  for (int64_t i = i0 + warp; i <= i1; i += warps) {
-    const float* p = part(i);
-    const float ref = p[D], more = p[D + 1];
-    const float up = fmaxf(top, ref), f = ex2(top - up), g = ex2(ref - up);
-    top = up;
-    l = l * f + more * g;
+  auto add = [&](auto batch, int64_t i) {  // the parts i, i + W, ..
+    constexpr int kBatch = decltype(batch)::value;
+    float ref[kBatch], sum[kBatch], v[kBatch][G];
 #pragma unroll
-    for (int j = 0; j < G; ++j) acc[j] = acc[j] * f + p[32 * j + lane] * g;
-  }
-  if (warps > 1) {
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t x = i + b * W;
+      const float* p = parts + (2 * (x * a.gang + (seg - round * a.gang)) + (x == i0 ? 1 : 0)) * kPart;
+      const bool in = x <= i1;
+      ref[b] = in ? p[D] : kRefStart;
+      sum[b] = in ? p[D + 1] : 0.f;
+#pragma unroll
+      for (int j = 0; j < G; ++j) v[b][j] = in ? p[32 * j + lane] : 0.f;
+    }
+    float up = top;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) up = fmaxf(up, ref[b]);
+    const float f = ex2(top - up);
+    top = up;
+    l *= f;
+#pragma unroll
+    for (int j = 0; j < G; ++j) acc[j] *= f;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const float g = ex2(ref[b] - up);
+      l = fmaf(sum[b], g, l);
+#pragma unroll
+      for (int j = 0; j < G; ++j) acc[j] = fmaf(v[b][j], g, acc[j]);
+    }
+  };
+  int64_t next = i0 + warp;
+  add(std::integral_constant<int, kFirst>{}, next);
+#pragma unroll 1
+  for (next += kFirst * W; next <= i1; next += kMore * W) add(std::integral_constant<int, kMore>{}, next);
+  __nv_bfloat16* out = a.out + ((int64_t)r * a.q_heads + qh) * D;
+  if constexpr (W == 1) {
+    const float inv = l == 0.f ? 0.f : kCentred / l;
+#pragma unroll
+    for (int j = 0; j < G; ++j) out[32 * j + lane] = __float2bfloat16_rn(acc[j] * inv);
+  } else {
     if (lane == 0) s_top[warp] = top, s_l[warp] = l;
 #pragma unroll
     for (int j = 0; j < G; ++j) s_o[warp][32 * j + lane] = acc[j];
     __syncthreads();
-    if (warp != 0) return;
-    for (int w = 1; w < warps; ++w) top = fmaxf(top, s_top[w]);
-    l = 0.f;
-#pragma unroll
-    for (int j = 0; j < G; ++j) acc[j] = 0.f;
-    for (int w = 0; w < warps; ++w) {
+    if (threadIdx.x >= D) return;
+    const int some = (int)min((int64_t)W, i1 - i0 + 1);  // warps that had a part
+    for (int w = 0; w < some; ++w) top = fmaxf(top, s_top[w]);
+    float sum = 0.f, o = 0.f;
+#pragma unroll 4
+    for (int w = 0; w < some; ++w) {
       const float f = ex2(s_top[w] - top);
-      l += f * s_l[w];
-#pragma unroll
-      for (int j = 0; j < G; ++j) acc[j] += f * s_o[w][32 * j + lane];
+      sum = fmaf(f, s_l[w], sum);
+      o = fmaf(f, s_o[w][threadIdx.x], o);
     }
+    out[threadIdx.x] = __float2bfloat16_rn(o * (sum == 0.f ? 0.f : kCentred / sum));
   }
-  const float inv = l == 0.f ? 0.f : kCentred / l;
-#pragma unroll
-  for (int j = 0; j < G; ++j)
-    a.out[((int64_t)r * a.q_heads + qh) * D + 32 * j + lane] = __float2bfloat16_rn(acc[j] * inv);
 }
 
 // Query heads a warp takes at once: 4, 8, or 16 (the cache is read once for all of them).
@@ -812,10 +844,12 @@ int launch(const AttnArgs& a, cudaStream_t stream) {
     return KV_ECUDA;
   const int rc = launch_pdl(kernel, worker_count() / kWarps, kThreads, smem, stream, a);
   if (rc != KV_OK) return rc;
-  // a row has about workers / (requests x KV heads) parts: more warps where that is long
-  const int64_t rows = (int64_t)a.num_reqs * a.q_heads;
-  const int warps = rows >= 2048 ? 1 : rows >= 512 ? 4 : 8;
-  return launch_pdl(join_q4_kernel<G, NQ>, (unsigned)rows, 32 * warps, 0, stream, a);
+  // about so many parts a row: more warps where they are many
+  const unsigned rows = (unsigned)a.num_reqs * (unsigned)a.q_heads;
+  const int parts = a.gangs / a.num_reqs;
+  if (parts >= 32) return launch_pdl(join_q4_kernel<G, NQ, 16>, rows, 32 * 16, 0, stream, a);
+  if (parts >= 8) return launch_pdl(join_q4_kernel<G, NQ, 8>, rows, 32 * 8, 0, stream, a);
+  return launch_pdl(join_q4_kernel<G, NQ, 1>, rows, 32, 0, stream, a);
 }
 
 template <int G>

@@ -217,3 +217,12 @@ def test_two_streams_and_a_graph():
         torch.cuda.synchronize()
         for c, w in zip(calls, want):
             assert torch.equal(c.result, w)
+
+
+@pytest.mark.parametrize("D,hq,h", [(128, 32, 8), (64, 16, 2), (128, 9, 1)])
+@pytest.mark.parametrize("count", [1, 7, 8, 28, 29, 60, 300])
+def test_one_long_context_among_short_ones(count, D, hq, h):
+    """Its parts are many for the few warps that join them, whatever the others need."""
+    ctx = [1 + 37 * i % 90 for i in range(count)]
+    ctx[count // 2] = 9001
+    run(ctx, 16, hq, h, D, seed=count + D)

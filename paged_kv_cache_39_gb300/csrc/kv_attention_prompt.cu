@@ -18,7 +18,7 @@
 // whatever the group is.  Roles by warp:
 //   0-3, 4-7  softmax of tile 0 / 1: one row per thread, so no shuffles; also the
 //             rescale and the epilogue of its tile
-//   8         TMA: Q once, then K and V tiles of 128 keys into a ring
+//   8         TMA: Q, then K and V tiles of 128 keys into a ring; finds the next pair
 //   9         issues the matrix instructions: S = Q K^T (both operands in shared
 //             memory), O += P V (P from tensor memory, over the S it came from)
 //   10, 11    check V tiles at the causal edge (below)
@@ -28,7 +28,7 @@
 //
 // Hidden keys.  A hidden logit is replaced, so a NaN there is gone, but 0 * NaN in
 // P V is NaN.  So in the tiles where some key is hidden from some row (one to three
-// per CTA), V values that are not finite are set to 0 in shared memory, and the
+// per pair), V values that are not finite are set to 0 in shared memory, and the
 // first key that held one is kept per channel: rows that see that key
 // get NaN in the epilogue.  Rows behind the sequence are set to 0 outright.
 //
@@ -37,14 +37,18 @@
 // and sums in their own shared memory, and each joins a share of the rows from all of them:
 //   o_i = sum_c f_c O_c / sum_c f_c s_c,  f_c = 2^(ref_c - max ref).
 // No workspace, no atomics: the same call gives the same bits.  The join costs 3 us; 16 tokens
-// behind 8192 take 15 us instead of 74, behind 65536 58 instead of 558.
+// behind 8192 take 15 us instead of 74, behind 65536 56 instead of 558.
 //
-// Measured (32 query heads, 8 KV heads of 128 channels): one prompt of 32768 tokens 5.5 ms (1600
-// TFLOP/s, at the card's power limit, 1.92 GHz), 16 chunks of 9 to 1855 tokens behind up to 7685
-// 383 us (1310 TFLOP/s: the 7 CTAs that an SM runs one after another each take 4 us to start
-// and to write, and the last wave is not full), 77 tokens 8.5 us.  Per 128 keys a CTA's two tiles
-// take 3000 cycles: 2048 of matrix instructions; a tile's softmax is 1140, beside the other
-// tile's products.
+// Many pairs.  A CTA that runs takes over the pairs of CTAs that wait (see kv_tc.cuh), so that
+// the start of the next pair (search, loads, first scores) overlaps the end of this one: 64 prompts
+// of 128 tokens 74 -> 47 us, 256 of 64 207 -> 85, and of a step's work nothing but the waits and the
+// instructions between them is left in the issuing warp's loop.
+//
+// Measured (32 query heads, 8 KV heads of 128 channels): one prompt of 32768 tokens 5.3 to 5.4 ms
+// (1630 to 1660 TFLOP/s, near the card's power limit, 1.92 GHz), 16 chunks of 9 to 1855 tokens behind
+// up to 7685 368 us (1360 TFLOP/s), 77 tokens 8.6 us.  Per 128 keys a CTA's two tiles take 2900
+// cycles: 2048 of matrix instructions; a tile's softmax is 1140, beside the other tile's products,
+// and its S, softmax and O follow one another with the barriers' times between them.
 #include <cuda_bf16.h>
 
 #include <mutex>
@@ -58,6 +62,7 @@ namespace {
 constexpr int kTile = 128;                 // query rows of a tile, keys of a K/V tile
 constexpr int kThreads = 384;
 constexpr int kScrubThreads = 64;
+constexpr int kReaders = 11;               // warps that a work description is passed on to
 constexpr int kEdges = 3;                  // K/V tiles a CTA's rows see in part: 256 tokens span at most 3
 constexpr int kSplitMax = 16;              // the largest cluster
 constexpr int kSplitFrom = 6;              // K/V tiles from which on a split pays for its join (3 us)
@@ -86,14 +91,17 @@ struct Smem {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTileBytes;
   static constexpr int kBars = kRing + kSlots * kTileBytes;
-  // an edge tile's slot is not used again (it would have to be kSlots loads later)
-  static_assert(kSlots >= 2 * kEdges - 1, "");
-  // full[slots], empty[slots], edge[3], v_ok[3], q_full, s_full[2], p_full[2][2], o_full[2],
-  // scrubbed, drain
-  static constexpr int kNumBars = 2 * kSlots + 2 * kEdges + 11;
+  // full[slots], empty[slots], edge[2][3], v_ok[2][3], q_full, q_free, s_full[2], p_full[2][2],
+  // o_full[2], scrubbed, written[2], ready, drain, stolen, work_full[2], work_free[2]
+  static constexpr int kNumBars = 2 * kSlots + 4 * kEdges + 20;
   static constexpr int kBad = kBars + kNumBars * 8;         // int[DP]: first key not finite
   static constexpr int kMisc = kBad + DP * 4;
-  static constexpr int kBytes = kMisc + 64 + 1024;          // + alignment of the base
+  static constexpr int kInFlight = kMisc + 16;              // uint32_t[8]: a slot's last barrier
+  static constexpr int kAnswer = kInFlight + 32;            // 16 bytes: the work taken over
+  static constexpr int kWork = kAnswer + 16;                // Work[2]
+  static constexpr int kOrder = kWork + 64;                 // uint16_t[kThreads]: requests by keys
+  static constexpr int kBytes = kOrder + kThreads * 2 + 1024;  // + alignment of the base
+  static_assert(kBars % 16 == 0 && kNumBars % 2 == 0 && kSlots <= 8, "");
   // for the join of a split: fp32 accumulators and (reference, sum) of 2 x 128 rows, where Q, K
   // and V were
   static constexpr int kStats = 2 * kTile * DP * 4;
@@ -101,8 +109,31 @@ struct Smem {
 };
 
 struct Work {
-  int32_t q0, k0, m, n;  // the request's first rows and lengths
+  int32_t q0, k0, m, n;  // the request's first rows and lengths; m = 0: no work
   int32_t t0;            // first token of the pair of tiles
+  int32_t head;
+};
+
+// What of it a CTA does.
+struct Item : Work {
+  int32_t ahead;       // keys before the first query's own
+  int32_t last;        // last token
+  int32_t tiles;       // K/V tiles that the last token sees
+  int32_t whole;       // of them, those that every row sees whole
+  int32_t parts;       // CTAs that share them
+  int32_t first, end;  // this CTA's
+  bool two;            // both tiles of the pair have tokens
+  __device__ __forceinline__ Item(const Work& w, const PromptArgs& a, int split, int rank) : Work(w) {
+    ahead = n - m;
+    last = min(t0 + 2 * a.tq, m) - 1;
+    const int keys = max(0, min(n, ahead + last + 1));
+    tiles = (keys + kTile - 1) / kTile;
+    whole = max(0, ahead + t0 + 1) / kTile;
+    parts = split > 1 && tiles >= kSplitFrom ? min(split, tiles / kSplitTiles) : 1;
+    first = rank < parts ? tiles * rank / parts : 0;
+    end = rank < parts ? tiles * (rank + 1) / parts : 0;
+    two = t0 + a.tq < m;
+  }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -116,58 +147,65 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// kSplit: in clusters of `split` CTAs (a kernel of its own, so that the other has neither the
-// join's registers nor its code in its way: 5.46 against 5.63 ms at 32768 tokens).
-template <int DP, bool kSplit>
+// Three kernels of one body, so that none has another's registers and code in its way (with the
+// join in all: 5.63 instead of 5.46 ms at 32768 tokens).
+enum Mode {
+  kOneWave,    // every CTA has one item
+  kManyWaves,  // those that run take over the work of those that wait
+  kClusters,   // `split` CTAs share an item
+};
+template <int DP, Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map, PromptArgs a) {
   using L = Smem<DP>;
+  constexpr bool kSplit = kMode == kClusters, kSteal = kMode == kManyWaves;
   extern __shared__ unsigned char raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* full = bars;
   uint64_t* empty = full + L::kSlots;
-  uint64_t* edge = empty + L::kSlots;
-  uint64_t* v_ok = edge + kEdges;
-  uint64_t* q_full = v_ok + kEdges;
-  uint64_t* s_full = q_full + 1;
+  uint64_t* edge = empty + L::kSlots;  // [item & 1][tile - whole]
+  uint64_t* v_ok = edge + 2 * kEdges;
+  uint64_t* q_full = v_ok + 2 * kEdges;
+  uint64_t* q_free = q_full + 1;
+  uint64_t* s_full = q_free + 1;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 4;
   uint64_t* scrubbed = o_full + 2;
-  uint64_t* drain = scrubbed + 1;
+  uint64_t* written = scrubbed + 1;
+  uint64_t* ready = written + 2;
+  uint64_t* drain = ready + 1;
+  uint64_t* stolen = drain + 1;
+  uint64_t* work_full = stolen + 1;  // [item & 1]
+  uint64_t* work_free = work_full + 2;
   int* bad = reinterpret_cast<int*>(smem + L::kBad);
   int* misc = reinterpret_cast<int*>(smem + L::kMisc);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort = misc + 1;
-  int* any_bad = misc + 2;
-  Work* s_work = reinterpret_cast<Work*>(misc + 4);
+  volatile int* any_bad = misc + 2;
+  uint32_t* in_flight = reinterpret_cast<uint32_t*>(smem + L::kInFlight);
+  Work* s_work = reinterpret_cast<Work*>(smem + L::kWork);
+  uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::kOrder);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform for the compiler, too
 
-  if (tid == 0) {
-    for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < kEdges; ++i) {
-      mbar_init(&edge[i], 1);
-      mbar_init(&v_ok[i], kScrubThreads);
-    }
-    mbar_init(q_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], kTile / 32);  // the first 64 keys' weights, one arrival a warp
-      mbar_init(&p_full[2 * i + 1], kTile / 32);
-      mbar_init(&o_full[i], 1);
-    }
-    mbar_init(scrubbed, kScrubThreads);
-    mbar_init(drain, 1);
+  if (tid < L::kNumBars) {
+    const uint64_t* b = &bars[tid];
+    int count = 1;
+    if (b >= v_ok && b < v_ok + 2 * kEdges) count = kScrubThreads;
+    if (b == scrubbed || b == ready) count = kScrubThreads;
+    if (b >= p_full && b < p_full + 4) count = kTile / 32;  // one arrival a warp
+    if (b >= written && b < written + 2) count = kTile / 32;
+    if (b >= work_free && b < work_free + 2) count = kReaders;
+    mbar_init(&bars[tid], count);
     mbar_fence_init();
+  }
+  if (tid == 0) {
     *abort = 0;
     *any_bad = 0;
-    *s_work = Work{0, 0, 0, 0, 0};  // of a CTA that no pair is left for
+    s_work[0] = Work{0, 0, 0, 0, 0, 0};  // of a CTA that no pair is left for
   }
   if (tid < DP) bad[tid] = INT32_MAX;
   pdl_allow_next();
@@ -185,27 +223,28 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   // that one head's K and V (16.8 MB at 32768 tokens) serve all CTAs at a time (5.60 against
   // 5.66 ms).
   const bool single = a.num_reqs == 1;
-  const int block = kSplit ? (int)(blockIdx.x / (unsigned)a.split) : (int)blockIdx.x;
-  const int rank_in = kSplit ? (int)blockIdx.x - block * a.split : 0;
-  const int head = single ? block / a.items : block % a.kv_heads;
-  const int want = single ? block % a.items : block / a.kv_heads;
+  const bool rank = a.num_reqs > 1 && a.num_reqs <= kThreads;
+  const int pair_tokens = 2 * a.tq;
+  const int split = kSplit ? a.split : 1;
+  const int rank_in = kSplit ? (int)(blockIdx.x % (unsigned)split) : 0;
+  auto head_of = [&](int block) { return single ? block / a.items : block % a.kv_heads; };
+  auto want_of = [&](int block) { return single ? block % a.items : block / a.kv_heads; };
+  auto pairs = [&](const Work& x) { return (int)(((int64_t)x.m + pair_tokens - 1) / pair_tokens); };
   uint32_t err = 0;
+  auto describe = [&](int r) {  // request r, or one without rows where it is not valid
+    const int q0 = a.q_start[r], q1 = a.q_start[r + 1], k0 = a.k_start[r], k1 = a.k_start[r + 1];
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.nq && k0 >= 0 && k1 >= k0 && k1 <= a.nk;
+    if (!ok) err |= KV_ERR_BAD_QSL;
+    return ok ? Work{q0, k0, q1 - q0, k1 - k0, 0, 0} : Work{0, 0, 0, 0, 0, 0};
+  };
   {
     __shared__ int64_t warp_sum[kThreads / 32];
+    const int block = (int)(blockIdx.x / (unsigned)split), want = want_of(block);
     int* keys_of = reinterpret_cast<int*>(smem);                     // [num_reqs], and
     int4* ranked = reinterpret_cast<int4*>(smem + kThreads * sizeof(int));  // the same: where Q will be
-    const int pair = 2 * a.tq;
-    const bool rank = a.num_reqs > 1 && a.num_reqs <= kThreads;
     const int per = (a.num_reqs + kThreads - 1) / kThreads;
     const int r_lo = min(a.num_reqs, tid * per), r_hi = min(a.num_reqs, r_lo + per);
-    auto describe = [&](int r) {  // request r, or one without rows where it is not valid
-      const int q0 = a.q_start[r], q1 = a.q_start[r + 1], k0 = a.k_start[r], k1 = a.k_start[r + 1];
-      const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.nq && k0 >= 0 && k1 >= k0 && k1 <= a.nk;
-      if (!ok) err |= KV_ERR_BAD_QSL;
-      return ok ? Work{q0, k0, q1 - q0, k1 - k0, 0} : Work{0, 0, 0, 0, 0};
-    };
-    auto pairs = [&](const Work& x) { return (int)(((int64_t)x.m + pair - 1) / pair); };
-    Work mine = {0, 0, 0, 0, 0};  // with `rank`: the request of this thread's rank
+    Work mine = {0, 0, 0, 0, 0, 0};  // with `rank`: the request of this thread's rank
     int64_t count = 0;  // 64 bits: requests that claim the same rows may count more than there are
     if (rank) {
       if (tid < a.num_reqs) {
@@ -218,11 +257,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         for (int r = 0; r < a.num_reqs; ++r)
           before += keys_of[r] > mine.n || (keys_of[r] == mine.n && r < tid);
         ranked[before] = make_int4(mine.q0, mine.k0, mine.m, mine.n);
+        order[before] = (uint16_t)tid;
       }
       __syncthreads();
       if (tid < a.num_reqs) {
         const int4 x = ranked[tid];
-        mine = Work{x.x, x.y, x.z, x.w, 0};
+        mine = Work{x.x, x.y, x.z, x.w, 0, 0};
         count = pairs(mine);
       }
       fence_proxy_async_smem();  // before TMA writes Q there
@@ -239,86 +279,163 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         int r = r_lo;
         for (mine = describe(r); want >= at + pairs(mine); mine = describe(++r)) at += pairs(mine);
       }
-      mine.t0 = (pairs(mine) - 1 - (int)(want - at)) * pair;
-      *s_work = mine;
+      mine.t0 = (pairs(mine) - 1 - (int)(want - at)) * pair_tokens;
+      mine.head = head_of(block);
+      s_work[0] = mine;
     }
-    __syncthreads();
     if (blockIdx.x == 0) report(a.err, err);
   }
-  Work w = *s_work;  // the same in every lane: tell the compiler
-  w.q0 = __shfl_sync(kFull, w.q0, 0);
-  w.k0 = __shfl_sync(kFull, w.k0, 0);
-  w.m = __shfl_sync(kFull, w.m, 0);
-  w.n = __shfl_sync(kFull, w.n, 0);
-  w.t0 = __shfl_sync(kFull, w.t0, 0);
-  const int ahead = w.n - w.m;                                    // keys before the first query's own
-  const int last = min(w.t0 + 2 * a.tq, w.m) - 1;                 // last token here
-  const int keys = max(0, min(w.n, ahead + last + 1));            // keys the last token sees
-  const int tiles = (keys + kTile - 1) / kTile;
-  // this CTA's share of them: [first, end)
-  const int parts = kSplit && tiles >= kSplitFrom ? min(a.split, tiles / kSplitTiles) : 1;
-  const int first = kSplit && rank_in < parts ? tiles * rank_in / parts : 0;
-  const int end = !kSplit ? tiles : rank_in < parts ? tiles * (rank_in + 1) / parts : 0;
-  const int whole = max(0, ahead + w.t0 + 1) / kTile;             // tiles every row sees whole
-  const bool two = w.t0 + a.tq < w.m;
-  const bool work = w.m > 0 && end > first;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, *tmem_ptr, 0);
 
-  if (w.m > 0 && tiles == 0 && rank_in == 0) {  // no query here sees a key
-    const int64_t row = (int64_t)a.group * a.head_dim;
-    const int vecs = (int)(row / 8);
-    for (int64_t i = tid; i < (int64_t)(last + 1 - w.t0) * vecs; i += kThreads) {
-      const int64_t t = w.q0 + w.t0 + i / vecs;
-      reinterpret_cast<uint4*>(a.out + t * a.q_heads * a.head_dim + head * row)[i % vecs] =
-          make_uint4(0, 0, 0, 0);
-    }
-  }
+  // A CTA goes on with the work of CTAs that have not started: the loading warp takes it over
+  // (the hardware hands a CTA that waits to another one only once, in launch order) while the
+  // others still compute, and passes it on in s_work[item & 1].  All barriers' phases run on from
+  // item to item, so the next item's Q, K and V are loaded and its first scores computed while this
+  // one's last weights and outputs are.
+  auto read = [&](int item) {  // the same in every lane: tell the compiler
+    const Work* p = &s_work[item & 1];
+    Work w;
+    w.q0 = __shfl_sync(kFull, p->q0, 0);
+    w.k0 = __shfl_sync(kFull, p->k0, 0);
+    w.m = __shfl_sync(kFull, p->m, 0);
+    w.n = __shfl_sync(kFull, p->n, 0);
+    w.t0 = __shfl_sync(kFull, p->t0, 0);
+    w.head = __shfl_sync(kFull, p->head, 0);
+    return w;
+  };
+  // Readers: the item after `item`, m = 0 behind the last one (or when a wait ran out).
+  auto following = [&](int item) {
+    Work none = {0, 0, 0, 0, 0, 0};
+    if (!kSteal) return none;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&work_free[item & 1]);
+    const bool ok = mbar_wait_role(&work_full[(item + 1) & 1], (item >> 1) & 1, abort);
+    return __all_sync(kFull, ok) ? read(item + 1) : none;
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8 && work) {
+    if (warp == 8) {
       // -------------------------------------------------------------- TMA
       const bool leader = elect_one();
       if (leader) {
         tma_prefetch_map(&q_map);
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&v_map);
-        const uint32_t q_bytes = (uint32_t)(a.group * a.tq) * 128u * (DP / 64);
-        mbar_arrive_expect_tx(q_full, two ? 2 * q_bytes : q_bytes);
-        for (int t = 0; t < (two ? 2 : 1); ++t)
-          for (int c = 0; c < DP / 64; ++c)
-            tma_load_3d(smem + L::kQ + t * L::kTileBytes + c * (kTile * 128), &q_map, 64 * c,
-                        head * a.group, w.q0 + w.t0 + t * a.tq, q_full);
       }
-      int u = 0, slot = 0, turn = 0;  // K and V tiles alternate in the ring
+      int slot = 0, turn = 0, items = 0, loaded = 0;
+      uint32_t edge_at = 0;     // bits: parities of the next use
+      int base = 0;             // where the search for the next item goes on: requests and
+      int64_t base_at = 0;      // pairs before it
+      bool ok = true, asked = false;
+      Work w = read(0);
+      for (int item = 0; w.m > 0; ++item) {
+        const Item x(w, a, split, rank_in);
+        if (x.end > x.first) {
+          if (loaded > 0) ok = __all_sync(kFull, mbar_wait_role(q_free, (loaded - 1) & 1, abort));
+          if (!ok) break;
+          if (leader) {
+            const uint32_t q_bytes = (uint32_t)(a.group * a.tq) * 128u * (DP / 64);
+            mbar_arrive_expect_tx(q_full, x.two ? 2 * q_bytes : q_bytes);
+            for (int t = 0; t < (x.two ? 2 : 1); ++t)
+              for (int c = 0; c < DP / 64; ++c)
+                tma_load_3d(smem + L::kQ + t * L::kTileBytes + c * (kTile * 128), &q_map, 64 * c,
+                            x.head * a.group, x.q0 + x.t0 + t * a.tq, q_full);
+          }
+          ++loaded;
 #pragma unroll 1
-      for (; u < 2 * (end - first); ++u) {
-        if (turn > 0 && !mbar_wait_role(&empty[slot], (turn - 1) & 1, abort)) break;
-        const bool is_v = u & 1;
-        const int j = first + (u >> 1);
-        uint64_t* bar = is_v && j >= whole ? &edge[j - whole] : &full[slot];
+          for (int u = 2 * x.first; u < 2 * x.end; ++u) {  // K and V tiles alternate in the ring
+            if (turn > 0) {
+              ok = __all_sync(kFull, mbar_wait_role(&empty[slot], (turn - 1) & 1, abort));
+              if (!ok) break;
+            }
+            const bool is_v = u & 1;
+            const int j = u >> 1;
+            const int e = is_v && j >= x.whole ? (item & 1) * kEdges + j - x.whole : -1;
+            uint64_t* bar = e >= 0 ? &edge[e] : &full[slot];
+            if (leader) {
+              in_flight[slot] = smem_addr(bar) | (e >= 0 ? (edge_at >> e) & 1 : turn & 1);
+              if (e >= 0) mbar_arrive(&full[slot]);  // its phases count the turns of the ring
+              mbar_arrive_expect_tx(bar, L::kTileBytes);
+              for (int c = 0; c < DP / 64; ++c)
+                tma_load_3d(smem + L::kRing + slot * L::kTileBytes + c * (kTile * 128),
+                            is_v ? &v_map : &k_map, 64 * c, x.head, x.k0 + j * kTile, bar);
+            }
+            if (e >= 0) edge_at ^= 1u << e;
+            if (++slot == L::kSlots) {
+              slot = 0;
+              ++turn;
+            }
+          }
+          if (!ok) break;
+        }
+        if (!kSteal) break;
+        // the next item: that of a CTA that waits, if any does
+        w.m = 0;
+        for (bool more = true; more && w.m == 0;) {
+          if (leader) {
+            fence_proxy_async_smem();  // the last answer was read
+            mbar_arrive_expect_tx(stolen, 16);
+            take_over(smem + L::kAnswer, stolen);
+          }
+          asked = true;
+          ok = mbar_wait_role(stolen, items & 1, abort);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          asked = false;
+          ++items;
+          int block;
+          more = __all_sync(kFull, taken_over(smem + L::kAnswer, &block));
+          block = __shfl_sync(kFull, block, 0);
+          if (!more) break;
+          const int want = want_of(block);
+          if (want < base_at) base = 0, base_at = 0;
+          for (; base < a.num_reqs; base += 32) {  // 32 requests at a time
+            Work mine = {0, 0, 0, 0, 0, 0};
+            if (base + lane < a.num_reqs) mine = describe(rank ? order[base + lane] : base + lane);
+            const int count = pairs(mine);
+            const int64_t incl = warp_inclusive_scan<int64_t>(count);
+            const int64_t at = base_at + incl - count;
+            const uint32_t found = __ballot_sync(kFull, want >= at && want < at + count);
+            if (found != 0) {
+              const int src = __ffs(found) - 1;
+              mine.t0 = (count - 1 - (int)(want - at)) * pair_tokens;
+              w.q0 = __shfl_sync(kFull, mine.q0, src);
+              w.k0 = __shfl_sync(kFull, mine.k0, src);
+              w.m = __shfl_sync(kFull, mine.m, src);
+              w.n = __shfl_sync(kFull, mine.n, src);
+              w.t0 = __shfl_sync(kFull, mine.t0, src);
+              w.head = head_of(block);
+              break;
+            }
+            base_at += __shfl_sync(kFull, incl, 31);
+          }
+        }
+        // s_work[..] is free once all have finished the item before this one
+        if (ok && item > 0) {
+          ok = mbar_wait_role(&work_free[(item - 1) & 1], ((item - 1) >> 1) & 1, abort);
+          ok = __all_sync(kFull, ok);
+        }
+        if (!ok) break;
         if (leader) {
-          mbar_arrive_expect_tx(bar, L::kTileBytes);
-          for (int c = 0; c < DP / 64; ++c)
-            tma_load_3d(smem + L::kRing + slot * L::kTileBytes + c * (kTile * 128),
-                        is_v ? &v_map : &k_map, 64 * c, head, w.k0 + j * kTile, bar);
+          s_work[(item + 1) & 1] = w;
+          mbar_arrive(&work_full[(item + 1) & 1]);
         }
-        if (++slot == L::kSlots) {
-          slot = 0;
-          ++turn;
-        }
+        __syncwarp();
       }
-      if (*abort != 0) {  // bounded wait for the copies still in flight
-        mbar_wait_bounded(q_full, 0);
-        for (int x = max(0, u - L::kSlots); x < u; ++x) {
-          if ((x & 1) && first + (x >> 1) >= whole) mbar_wait_bounded(&edge[first + (x >> 1) - whole], 0);
-          else mbar_wait_bounded(&full[x % L::kSlots], (x / L::kSlots) & 1);
-        }
+      if (__any_sync(kFull, *abort != 0)) {  // bounded wait for the copies still in flight
+        if (loaded > 0) mbar_wait_bounded(q_full, (loaded - 1) & 1);
+        if (asked) mbar_wait_bounded(stolen, items & 1);
+        __syncwarp();
+        for (int i = 0; i < L::kSlots; ++i)
+          if (turn > 0 || i < slot)
+            mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + ((in_flight[i] & ~1u) - smem_addr(smem))),
+                              in_flight[i] & 1u);
       }
-    } else if (warp == 9 && work) {
+    } else if (warp == 9) {
       // -------------------------------------------------------------- matrix instructions
       constexpr uint32_t s_desc = mma_desc(128, kTile, false), o_desc = mma_desc(128, DP, true);
       constexpr uint32_t kSlotStep = L::kTileBytes >> 4;  // descriptors count 16 bytes
@@ -347,107 +464,196 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             mma_ts(d, p + k * 8, vd + k * (2048 >> 4), o_desc, add || k > 0);
         }
       };
-      const int nt = two ? 2 : 1;
-      bool ok = mbar_wait_role(q_full, 0, abort) && mbar_wait_role(&full[0], 0, abort);
-      if (ok) {
-        tc_fence_after();
-        scores(0, 0);
-        if (two) scores(1, 0);
-        if (leader) mma_commit(&empty[0]);
-      }
-      int sv = 1, sk = 2, pv = 0, pk = 0;  // slots of V_j and K_{j+1}, parities of their phases
-#pragma unroll 1
-      for (int j = first; ok && j < end; ++j) {
-        const bool more = j + 1 < end;
-        const uint32_t phase = (j - first) & 1;
-        // at the causal edge V is waited for through the warps that check it
-        ok = j < whole ? mbar_wait_role(&full[sv], pv, abort)
-                       : mbar_wait_role(&v_ok[j - whole], 0, abort);
-        if (ok && more) ok = mbar_wait_role(&full[sk], pk, abort);
-#pragma unroll 1
-        for (int t = 0; ok && t < nt; ++t) {
-          ok = mbar_wait_role(&p_full[2 * t], phase, abort);
+      int sv = 0, sk = 0, pv = 0, pk = 0;  // slots of V and the next K, parities of their phases
+      int loaded = 0;
+      uint32_t p_at = 0, v_ok_at = 0;      // bits: parities of the next waits (p_full: per tile)
+      bool ok = true;
+      Work w = read(0);
+      for (int item = 0; w.m > 0; ++item) {
+        const Item x(w, a, split, rank_in);
+        if (x.end > x.first) {
+          ok = mbar_wait_role(q_full, loaded & 1, abort) && mbar_wait_role(&full[sk], pk, abort);
+          ok = __all_sync(kFull, ok);
           if (!ok) break;
+          ++loaded;
           tc_fence_after();
-          values(t, sv, j > first, 0);
-          ok = mbar_wait_role(&p_full[2 * t + 1], phase, abort);
+          scores(0, sk);
+          if (x.two) scores(1, sk);
+          if (leader) {
+            mma_commit(&empty[sk]);
+            if (x.end - x.first == 1) mma_commit(q_free);
+          }
+          const int nt = x.two ? 2 : 1;
+          auto step = [](int& slot, int& phase) {
+            if (++slot == L::kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
+          };
+          sv = sk, pv = pk;
+          step(sv, pv);
+          sk = sv, pk = pv;
+          step(sk, pk);
+          auto advance = [&]() {
+            sv += 2;
+            sk += 2;
+            if (sv >= L::kSlots) {
+              sv -= L::kSlots;
+              pv ^= 1;
+            }
+            if (sk >= L::kSlots) {
+              sk -= L::kSlots;
+              pk ^= 1;
+            }
+          };
+          auto tile = [&](int t, uint32_t phase, bool add, bool more) {
+            if (!mbar_wait_role(&p_full[2 * t], phase, abort)) return false;
+            tc_fence_after();
+            values(t, sv, add, 0);
+            if (!mbar_wait_role(&p_full[2 * t + 1], phase, abort)) return false;
+            tc_fence_after();
+            values(t, sv, true, 1);
+            if (more) scores(t, sk);  // in issue order behind the P V that reads what it overwrites
+            else if (leader) mma_commit(&o_full[t]);
+            return true;
+          };
+          int j = x.first;
+          bool add = false;
+          // the usual step by itself, with as little as can be between the waits: what the issue
+          // takes longer, the matrix unit waits (6.2 ms at 32768 tokens with the loop below alone)
+          if (x.two) {
+#pragma unroll 1
+            for (; j + 2 < x.end && j < x.whole; ++j) {
+              ok = mbar_wait_role(&full[sv], pv, abort) && mbar_wait_role(&full[sk], pk, abort) &&
+                   tile(0, p_at & 1, add, true) && tile(1, p_at >> 1, add, true);
+              ok = __all_sync(kFull, ok);  // also keeps the lanes within one step of each other
+              if (!ok) break;
+              if (leader) {
+                mma_commit(&empty[sv]);
+                mma_commit(&empty[sk]);
+              }
+              p_at ^= 3;
+              add = true;
+              advance();
+            }
+          }
+#pragma unroll 1
+          for (; ok && j < x.end; ++j) {
+            const bool more = j + 1 < x.end;
+            // at the causal edge V is waited for through the warps that check it
+            if (j < x.whole) {
+              ok = mbar_wait_role(&full[sv], pv, abort);
+            } else {
+              const int e = (item & 1) * kEdges + j - x.whole;
+              ok = mbar_wait_role(&v_ok[e], (v_ok_at >> e) & 1, abort);
+              v_ok_at ^= 1u << e;
+            }
+            if (ok && more) ok = mbar_wait_role(&full[sk], pk, abort);
+#pragma unroll 1
+            for (int t = 0; ok && t < nt; ++t) ok = tile(t, (p_at >> t) & 1, add, more);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            if (leader) {
+              mma_commit(&empty[sv]);
+              if (more) mma_commit(&empty[sk]);
+              if (more && j + 2 == x.end) mma_commit(q_free);
+            }
+            p_at ^= x.two ? 3 : 1;
+            add = true;
+            if (more) advance();  // else sk is the next item's first K
+          }
           if (!ok) break;
-          tc_fence_after();
-          values(t, sv, true, 1);
-          if (more) scores(t, sk);  // in issue order behind the P V that reads what it overwrites
-          else if (leader) mma_commit(&o_full[t]);
         }
-        if (!ok) break;
-        if (leader) {
-          mma_commit(&empty[sv]);
-          if (more) mma_commit(&empty[sk]);
-        }
-        sv += 2;
-        sk += 2;
-        if (sv >= L::kSlots) {
-          sv -= L::kSlots;
-          pv ^= 1;
-        }
-        if (sk >= L::kSlots) {
-          sk -= L::kSlots;
-          pk ^= 1;
-        }
+        w = following(item);
       }
-      if (!ok) {  // bounded wait for the matrix instructions in flight
-        if (leader) mma_commit(drain);
-        mbar_wait_bounded(drain, 0);
-      }
-    } else if (warp >= 10 && work) {
+      // The matrix unit arrives on barriers on its own time: none of its arrivals (the last slots',
+      // which nobody waits for) may come after the CTA's shared memory has gone to another.  It
+      // takes them in order, so the last one stands for all.
+      __syncwarp();
+      if (leader) mma_commit(drain);
+      mbar_wait_bounded(drain, 0);
+    } else {
       // -------------------------------------------------------------- V at the causal edge
       const int st = tid - 10 * 32;
-      for (int j = max(first, whole); j < end; ++j) {
-        const int slot = (2 * (j - first) + 1) % L::kSlots;
-        if (!mbar_wait_role(&edge[j - whole], 0, abort)) break;
-        unsigned char* tile = smem + L::kRing + slot * L::kTileBytes;
-#pragma unroll 1
-        for (int r = st; r < kTile; r += kScrubThreads) {
-          const int key = j * kTile + r;
-          // the row's 16-byte pieces, the row's own one first: no two of 8 rows share a bank
-          auto piece = [&](int i) {
-            return reinterpret_cast<uint4*>(tile + (i / 8) * (kTile * 128) + r * 128 + ((i + r) & 7) * 16);
-          };
-          if (key >= w.n) {
-#pragma unroll
-            for (int i = 0; i < DP / 8; ++i) *piece(i) = make_uint4(0, 0, 0, 0);
-            continue;
+      int slot = 0, done = 0;
+      uint32_t edge_at = 0, written_at = 0;
+      bool both = false;  // the item before had two tiles
+      Work w = read(0);
+      for (int item = 0; w.m > 0; ++item) {
+        const Item x(w, a, split, rank_in);
+        if (x.end > x.first) {
+          bool ok = true;
+          if (done > 0) {  // the item before is written: its `bad` goes
+            ok = mbar_wait_role(&written[0], written_at & 1, abort);
+            if (ok && both) ok = mbar_wait_role(&written[1], written_at >> 1, abort);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            written_at ^= both ? 3 : 1;
+            for (int i = st; i < DP; i += kScrubThreads) bad[i] = INT32_MAX;
+            if (st == 0) *any_bad = 0;
+            mbar_arrive(ready);
+            ok = __all_sync(kFull, mbar_wait_role(ready, (done - 1) & 1, abort));
+            if (!ok) break;
           }
-          uint32_t most = 0;  // the largest magnitudes, two to a word; 0x7f80 and up: not finite
-#pragma unroll
-          for (int i = 0; i < DP / 8; ++i) {
-            const uint4 x = *piece(i);
-            most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-          }
-          if ((most & 0xffffu) < 0x7f80u && most < 0x7f800000u) continue;
+          ++done;
+          both = x.two;
+          for (int j = max(x.first, x.whole); j < x.end; ++j) {
+            const int e = (item & 1) * kEdges + j - x.whole;
+            ok = mbar_wait_role(&edge[e], (edge_at >> e) & 1, abort);
+            edge_at ^= 1u << e;
+            if (!ok) break;
+            unsigned char* tile =
+                smem + L::kRing + ((slot + 2 * (j - x.first) + 1) % L::kSlots) * L::kTileBytes;
 #pragma unroll 1
-          for (int i = 0; i < DP / 8; ++i) {
-            uint4 x = *piece(i);
-            uint32_t* e = reinterpret_cast<uint32_t*>(&x);
-            const int channel = (i / 8) * 64 + (((i + r) & 7) ^ (r & 7)) * 8;
+            for (int r = st; r < kTile; r += kScrubThreads) {
+              const int key = j * kTile + r;
+              // the row's 16-byte pieces, the row's own one first: no two of 8 rows share a bank
+              auto piece = [&](int i) {
+                return reinterpret_cast<uint4*>(tile + (i / 8) * (kTile * 128) + r * 128 + ((i + r) & 7) * 16);
+              };
+              if (key >= x.n) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if ((e[q] & 0x7f80u) == 0x7f80u) {
-                atomicMin(&bad[channel + 2 * q], key);
-                e[q] &= 0xffff0000u;
+                for (int i = 0; i < DP / 8; ++i) *piece(i) = make_uint4(0, 0, 0, 0);
+                continue;
               }
-              if ((e[q] & 0x7f800000u) == 0x7f800000u) {
-                atomicMin(&bad[channel + 2 * q + 1], key);
-                e[q] &= 0xffffu;
+              uint32_t most = 0;  // the largest magnitudes, two to a word; 0x7f80 and up: not finite
+#pragma unroll
+              for (int i = 0; i < DP / 8; ++i) {
+                const uint4 y = *piece(i);
+                most = __vmaxu2(most, __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
+                                               __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
               }
+              if ((most & 0xffffu) < 0x7f80u && most < 0x7f800000u) continue;
+#pragma unroll 1
+              for (int i = 0; i < DP / 8; ++i) {
+                uint4 y = *piece(i);
+                uint32_t* q = reinterpret_cast<uint32_t*>(&y);
+                const int channel = (i / 8) * 64 + (((i + r) & 7) ^ (r & 7)) * 8;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  if ((q[c] & 0x7f80u) == 0x7f80u) {
+                    atomicMin(&bad[channel + 2 * c], key);
+                    q[c] &= 0xffff0000u;
+                  }
+                  if ((q[c] & 0x7f800000u) == 0x7f800000u) {
+                    atomicMin(&bad[channel + 2 * c + 1], key);
+                    q[c] &= 0xffffu;
+                  }
+                }
+                *piece(i) = y;
+              }
+              *any_bad = 1;
             }
-            *piece(i) = x;
+            fence_proxy_async_smem();
+            mbar_arrive(&v_ok[e]);
           }
-          *any_bad = 1;
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          mbar_arrive(scrubbed);
+          slot = (slot + 2 * (x.end - x.first)) % L::kSlots;
         }
-        fence_proxy_async_smem();
-        mbar_arrive(&v_ok[j - whole]);
+        w = following(item);
       }
-      mbar_arrive(scrubbed);
     }
     if constexpr (kSplit) {  // the softmax warps' join
       cluster_sync();
@@ -456,144 +662,172 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = warp >> 2;  // the tile
-    if (work && (t == 0 || two)) {
-      // -------------------------------------------------------------- softmax
-      const int row = tid & 127;
-      const int tok = row / a.group, g = row - tok * a.group;
-      const int i = w.t0 + t * a.tq + tok;  // token in the request
-      const bool mine = tok < a.tq && i < w.m;
-      const int seen = min(w.n, ahead + i + 1);
-      const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes, in bits 16..
-      const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 2 * kTile + t * DP;
-      const float c = a.scale_log2;
-      float ref = 0.f;
-      uint64_t part[2] = {0, 0};  // sums of weights, two by two
-      bool ok = true;
-      for (int j = first; j < end; ++j) {
-        ok = mbar_wait_role(&s_full[t], (j - first) & 1, abort);
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t s[kTile];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, s + 32 * b);
-        tmem_wait_ld();
-        if (j >= whole) {
-          const int left = seen - j * kTile;  // keys of this tile the row sees
-#pragma unroll
-          for (int x = 0; x < kTile; ++x)
-            if (x >= left) s[x] = 0xff800000u;
+    const int row = tid & 127;
+    const int tok = row / a.group, g = row - tok * a.group;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes, in bits 16..
+    const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + 2 * kTile + t * DP;
+    const float c = a.scale_log2;
+    uint32_t s_phase = 0, o_phase = 0;
+    int done = 0;
+    Work w = read(0);
+    for (int item = 0; w.m > 0; ++item) {
+      const Item x(w, a, split, rank_in);
+      const bool work = x.end > x.first;
+      if (x.tiles == 0 && rank_in == 0) {  // no query here sees a key
+        const int64_t dense = (int64_t)a.group * a.head_dim;
+        const int vecs = (int)(dense / 8);
+        for (int64_t i = tid; i < (int64_t)(x.last + 1 - x.t0) * vecs; i += 256) {
+          const int64_t at = x.q0 + x.t0 + i / vecs;
+          reinterpret_cast<uint4*>(a.out + at * a.q_heads * a.head_dim + x.head * dense)[i % vecs] =
+              make_uint4(0, 0, 0, 0);
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      }
+      if (work && (t == 0 || x.two)) {
+        // ------------------------------------------------------------ softmax
+        const int i = x.t0 + t * a.tq + tok;  // token in the request
+        const bool mine = tok < a.tq && i < x.m;
+        const int seen = min(x.n, x.ahead + i + 1);
+        s_phase -= x.first;
+        float ref = 0.f;
+        uint64_t part[2] = {0, 0};  // sums of weights, two by two
+        bool ok = true;
+        for (int j = x.first; j < x.end; ++j) {
+          ok = mbar_wait_role(&s_full[t], (s_phase + j) & 1, abort);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t s[kTile];
 #pragma unroll
-        for (int x = 0; x < kTile; x += 4)
+          for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, s + 32 * b);
+          tmem_wait_ld();
+          if (j >= x.whole) {
+            const int left = seen - j * kTile;  // keys of this tile the row sees
 #pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[x + y]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        if (j == first) {
-          ref = top > -INFINITY ? top : kRefStart;
-        } else {
-          const bool raise = top > ref + kLazy;
-          if (__any_sync(kFull, raise)) {
-            // P V of the earlier tiles is done: S of this tile was issued behind it
-            const float f = raise ? ex2(ref - top) : 1.f;
-            if (raise) ref = top;
-            part[0] = mul2(part[0], pair(f, f));
-            part[1] = mul2(part[1], pair(f, f));
+            for (int y = 0; y < kTile; ++y)
+              if (y >= left) s[y] = 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int z = 0; z < kTile; z += 4)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[z + y]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          if (j == x.first) {
+            ref = top > -INFINITY ? top : kRefStart;
+          } else {
+            const bool raise = top > ref + kLazy;
+            if (__any_sync(kFull, raise)) {
+              // P V of the earlier tiles is done: S of this tile was issued behind it
+              const float f = raise ? ex2(ref - top) : 1.f;
+              if (raise) ref = top;
+              part[0] = mul2(part[0], pair(f, f));
+              part[1] = mul2(part[1], pair(f, f));
 #pragma unroll 1
-            for (int b = 0; b < DP / 32; ++b) {
-              uint32_t o[32];
-              tmem_ld32(o_at + 32 * b, o);
-              tmem_wait_ld();
+              for (int b = 0; b < DP / 32; ++b) {
+                uint32_t o[32];
+                tmem_ld32(o_at + 32 * b, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st32(o_at + 32 * b, o);
+                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                tmem_st32(o_at + 32 * b, o);
+              }
+            }
+          }
+          // 2^(c s - ref) two at a time; half of the weights go to the matrix unit while the other
+          // half is computed
+          const uint64_t c2 = pair(c, c), r2 = pair(-ref, -ref);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            uint32_t p[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              float e0, e1;
+              unpair(fma2(pair(__uint_as_float(s[32 * b + 2 * y]), __uint_as_float(s[32 * b + 2 * y + 1])),
+                          c2, r2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              part[y & 1] = add2(part[y & 1], pair(e0, e1));
+              p[y] = pack_bf16(e0, e1);
+            }
+            tmem_st16(s_at + 16 * b, p);
+            if (b & 1) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[2 * t + (b >> 1)]);
             }
           }
         }
-        // 2^(c s - ref) two at a time; half of the weights go to the matrix unit while the other
-        // half is computed
-        const uint64_t c2 = pair(c, c), r2 = pair(-ref, -ref);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t p[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float e0, e1;
-            unpair(fma2(pair(__uint_as_float(s[32 * b + 2 * x]), __uint_as_float(s[32 * b + 2 * x + 1])),
-                        c2, r2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            part[x & 1] = add2(part[x & 1], pair(e0, e1));
-            p[x] = pack_bf16(e0, e1);
-          }
-          tmem_st16(s_at + 16 * b, p);
-          if (b & 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * t + (b >> 1)]);
-          }
+        s_phase += x.end;
+        float sum;
+        {
+          float a0, a1, b0, b1;
+          unpair(part[0], a0, a1);
+          unpair(part[1], b0, b1);
+          sum = (a0 + a1) + (b0 + b1);
         }
-      }
-      float sum;
-      {
-        float a0, a1, b0, b1;
-        unpair(part[0], a0, a1);
-        unpair(part[1], b0, b1);
-        sum = (a0 + a1) + (b0 + b1);
-      }
-      // -------------------------------------------------------------- epilogue
-      if (ok) ok = __all_sync(kFull, mbar_wait_role(&o_full[t], 0, abort));
-      if (ok) ok = __all_sync(kFull, mbar_wait_role(scrubbed, 0, abort));
-      // a split's accumulators go where the other tile's products may still read K and V
-      if (ok && parts > 1 && two) ok = __all_sync(kFull, mbar_wait_role(&o_full[1], 0, abort));
-      if (ok) {
-        tc_fence_after();
-        const bool check = *any_bad != 0;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: zeros
-        __nv_bfloat16* out = a.out + ((int64_t)(w.q0 + i) * a.q_heads + head * a.group + g) * a.head_dim;
+        // ------------------------------------------------------------ epilogue
+        if (ok) ok = __all_sync(kFull, mbar_wait_role(&o_full[t], o_phase, abort));
+        o_phase ^= 1;
+        if (ok) ok = __all_sync(kFull, mbar_wait_role(scrubbed, done & 1, abort));
+        // a split's accumulators go where the other tile's products may still read K and V
+        if (kSplit && ok && x.parts > 1 && x.two) ok = __all_sync(kFull, mbar_wait_role(&o_full[1], 0, abort));
+        if (!kSplit && !ok) break;
+        if (ok) {
+          tc_fence_after();
+          const bool check = *any_bad != 0;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: zeros
+          __nv_bfloat16* out =
+              a.out + ((int64_t)(x.q0 + i) * a.q_heads + x.head * a.group + g) * a.head_dim;
 #pragma unroll 1
-        for (int b = 0; b < DP / 32; ++b) {
-          uint32_t o[32];
-          tmem_ld32(o_at + 32 * b, o);
-          tmem_wait_ld();
-          if (check) {
+          for (int b = 0; b < DP / 32; ++b) {
+            uint32_t o[32];
+            tmem_ld32(o_at + 32 * b, o);
+            tmem_wait_ld();
+            if (check) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (seen > bad[32 * b + x]) o[x] = 0x7fc00000u;
-          }
-          if (parts > 1) {  // 16-byte piece x of a row at (x + row): no bank twice in 8 rows
-            float4* to = reinterpret_cast<float4*>(smem) + (t * kTile + row) * (DP / 4);
+              for (int y = 0; y < 32; ++y)
+                if (seen > bad[32 * b + y]) o[y] = 0x7fc00000u;
+            }
+            if (kSplit && x.parts > 1) {  // 16-byte piece y of a row at (y + row): no bank twice in 8 rows
+              float4* to = reinterpret_cast<float4*>(smem) + (t * kTile + row) * (DP / 4);
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              to[(8 * b + x + row) & (DP / 4 - 1)] =
-                  make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                              __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
-            continue;
-          }
+              for (int y = 0; y < 8; ++y)
+                to[(8 * b + y + row) & (DP / 4 - 1)] =
+                    make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
+                                __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
+              continue;
+            }
 #pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            uint4 y;
-            y.x = pack_bf16(__uint_as_float(o[x]) * inv, __uint_as_float(o[x + 1]) * inv);
-            y.y = pack_bf16(__uint_as_float(o[x + 2]) * inv, __uint_as_float(o[x + 3]) * inv);
-            y.z = pack_bf16(__uint_as_float(o[x + 4]) * inv, __uint_as_float(o[x + 5]) * inv);
-            y.w = pack_bf16(__uint_as_float(o[x + 6]) * inv, __uint_as_float(o[x + 7]) * inv);
-            if (mine && 32 * b + x < a.head_dim)
-              *reinterpret_cast<uint4*>(out + 32 * b + x) = y;
+            for (int y = 0; y < 32; y += 8) {
+              uint4 z;
+              z.x = pack_bf16(__uint_as_float(o[y]) * inv, __uint_as_float(o[y + 1]) * inv);
+              z.y = pack_bf16(__uint_as_float(o[y + 2]) * inv, __uint_as_float(o[y + 3]) * inv);
+              z.z = pack_bf16(__uint_as_float(o[y + 4]) * inv, __uint_as_float(o[y + 5]) * inv);
+              z.w = pack_bf16(__uint_as_float(o[y + 6]) * inv, __uint_as_float(o[y + 7]) * inv);
+              if (mine && 32 * b + y < a.head_dim)
+                *reinterpret_cast<uint4*>(out + 32 * b + y) = z;
+            }
           }
+          if (kSplit && x.parts > 1)
+            reinterpret_cast<float2*>(smem + L::kStats)[t * kTile + row] = make_float2(ref, sum);
         }
-        if (parts > 1)
-          reinterpret_cast<float2*>(smem + L::kStats)[t * kTile + row] = make_float2(ref, sum);
+        // each tile for itself: the warps of a tile without work would be items ahead
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&written[t]);
       }
+      done += work;
+      w = following(item);
     }
     if constexpr (kSplit) {
       // -------------------------------------------------------------- join of a split
+      const Item x(read(0), a, split, rank_in);
       cluster_sync();
-      if (parts > 1 && w.m > 0) {
+      if (x.parts > 1 && x.m > 0) {
         // rows rank_in, rank_in + CTAs, .., B to a warp at a time, 4 channels to a lane; all of
         // their parts are asked for (a far read takes about 0.5 us) before the first is used
-        const int rows = two ? 2 * kTile : kTile;
+        const int rows = x.two ? 2 * kTile : kTile;
         const int piece = lane & (DP / 4 - 1);
         auto join = [&](auto at_once) {
           constexpr int B = decltype(at_once)::value, C = kSplitMax / B;
@@ -602,24 +836,24 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             float4 o[B][C];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-              const uint32_t base = cluster_addr(smem, min(c, parts - 1));
+              const uint32_t base = cluster_addr(smem, min(c, x.parts - 1));
 #pragma unroll
               for (int b = 0; b < B; ++b) {
-                const int x = (x0 + 8 * b) * a.split + rank_in;
+                const int at = (x0 + 8 * b) * a.split + rank_in;
                 rs[b][c] = make_float2(kRefStart, 0.f);
                 o[b][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c < parts && x < rows) {
-                  rs[b][c] = cluster_ld2(base + L::kStats + x * 8);
-                  o[b][c] = cluster_ld4(base + (x * (DP / 4) + ((piece + x) & (DP / 4 - 1))) * 16);
+                if (c < x.parts && at < rows) {
+                  rs[b][c] = cluster_ld2(base + L::kStats + at * 8);
+                  o[b][c] = cluster_ld4(base + (at * (DP / 4) + ((piece + at) & (DP / 4 - 1))) * 16);
                 }
               }
             }
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-              const int x = (x0 + 8 * b) * a.split + rank_in;
-              const int row = x & (kTile - 1), tok = row / a.group, g = row - tok * a.group;
-              const int i = w.t0 + (x >> 7) * a.tq + tok;
-              if (x >= rows || tok >= a.tq || i >= w.m) continue;
+              const int at = (x0 + 8 * b) * a.split + rank_in;
+              const int row = at & (kTile - 1), tok = row / a.group, g = row - tok * a.group;
+              const int i = x.t0 + (at >> 7) * a.tq + tok;
+              if (at >= rows || tok >= a.tq || i >= x.m) continue;
               float top = rs[b][0].x;
 #pragma unroll
               for (int c = 1; c < C; ++c) top = fmaxf(top, rs[b][c].x);
@@ -638,12 +872,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
               unpair(y[1], z[2], z[3]);
               if (lane < DP / 4 && 4 * piece < a.head_dim)
                 *reinterpret_cast<uint2*>(
-                    a.out + ((int64_t)(w.q0 + i) * a.q_heads + head * a.group + g) * a.head_dim + 4 * piece) =
+                    a.out + ((int64_t)(x.q0 + i) * a.q_heads + x.head * a.group + g) * a.head_dim + 4 * piece) =
                     make_uint2(pack_bf16(z[0] * inv, z[1] * inv), pack_bf16(z[2] * inv, z[3] * inv));
             }
           }
         };
-        if (parts > 4) join(std::integral_constant<int, 1>{});
+        if (x.parts > 4) join(std::integral_constant<int, 1>{});
         else join(std::integral_constant<int, 4>{});
       }
       cluster_sync();  // no CTA ends while another reads its shared memory
@@ -670,7 +904,7 @@ int clusters_at_once(int size) {
   std::lock_guard<std::mutex> lock(mu);
   int& n = cached[dev][size];
   if (n == 0) {
-    auto kernel = prompt_kernel<DP, true>;
+    auto kernel = prompt_kernel<DP, kClusters>;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)size;
@@ -707,14 +941,15 @@ int choose_split(int64_t pairs, int64_t keys) {
   return (int)split;
 }
 
-template <int DP, bool kSplit>
+template <int DP, Mode kMode>
 int launch(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
            cudaStream_t stream) {
-  auto kernel = prompt_kernel<DP, kSplit>;
+  auto kernel = prompt_kernel<DP, kMode>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Smem<DP>::kBytes) != cudaSuccess)
     return KV_ECUDA;
-  if (kSplit && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+  if (kMode == kClusters &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                     cudaSuccess)
     return KV_ECUDA;
   const int64_t ctas = (int64_t)a.items * a.kv_heads * a.split;
@@ -727,7 +962,9 @@ template <int DP>
 int launch(PromptArgs a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
            cudaStream_t stream) {
   a.split = choose_split<DP>((int64_t)a.items * a.kv_heads, a.nk);
-  return a.split > 1 ? launch<DP, true>(a, q, k, v, stream) : launch<DP, false>(a, q, k, v, stream);
+  if (a.split > 1) return launch<DP, kClusters>(a, q, k, v, stream);
+  return (int64_t)a.items * a.kv_heads > sm_count() ? launch<DP, kManyWaves>(a, q, k, v, stream)
+                                                    : launch<DP, kOneWave>(a, q, k, v, stream);
 }
 
 }  // namespace

@@ -173,6 +173,32 @@ __device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
   return v;
 }
 
+// ---------------------------------------------------------------------------
+// Work stealing.  take_over() asks the hardware for a CTA of this grid that has not started (one
+// thread; 16 bytes of answer, counted by `bar`, 16-byte aligned); if it gives one, that CTA never
+// starts and its work is the asker's.  After a refusal no more is asked for.
+
+__device__ __forceinline__ void take_over(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(smem_addr(answer)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ bool taken_over(const void* answer, int* block) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n .reg .b128 h;\n .reg .pred p;\n .reg .b64 lo, hi;\n"
+      " ld.shared.v2.b64 {lo, hi}, [%2];\n mov.b128 h, {lo, hi};\n mov.u32 %1, 0;\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}\n"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  *block = (int)x;
+  return ok != 0;
+}
+
 // Tensor map of bf16 rows [tokens, heads, head_dim] (`stride` elements between tokens) in boxes
 // of 64 channels x box_heads x box_tokens, 128-byte swizzle, zeros outside.  False when the
 // driver offers no encoder or refuses.

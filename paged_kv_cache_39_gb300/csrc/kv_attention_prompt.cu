@@ -41,12 +41,11 @@
 //
 // Many pairs.  A CTA that runs takes over the pairs of CTAs that wait (see kv_tc.cuh), so that
 // the start of the next pair (search, loads, first scores) overlaps the end of this one: 64 prompts
-// of 128 tokens 74 -> 47 us, 256 of 64 207 -> 85, and of a step's work nothing but the waits and the
-// instructions between them is left in the issuing warp's loop.
+// of 128 tokens 74 -> 47 us, 256 of 64 207 -> 85.
 //
 // Measured (32 query heads, 8 KV heads of 128 channels): one prompt of 32768 tokens 5.3 to 5.4 ms
 // (1630 to 1660 TFLOP/s, near the card's power limit, 1.92 GHz), 16 chunks of 9 to 1855 tokens behind
-// up to 7685 368 us (1360 TFLOP/s), 77 tokens 8.6 us.  Per 128 keys a CTA's two tiles take 2900
+// up to 7685 370 us (1350 TFLOP/s), 77 tokens 8.6 us.  Per 128 keys a CTA's two tiles take 2900
 // cycles: 2048 of matrix instructions; a tile's softmax is 1140, beside the other tile's products,
 // and its S, softmax and O follow one another with the barriers' times between them.
 #include <cuda_bf16.h>

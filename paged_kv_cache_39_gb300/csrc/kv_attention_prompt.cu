@@ -921,7 +921,7 @@ int clusters_at_once(int size) {
             cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&found, kernel, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
-      found = 0;
+      return 0;
     }
     n = found > 0 ? found : -1;
   }

@@ -122,3 +122,24 @@ def test_sequences_that_are_refused():
         assert err.item() == kv.ERR_BITS["BAD_QSL"]
         assert torch.equal(out[:20], good[:20]) and (out[20:] == 7).all()
     assert np.isfinite(good.float().cpu().numpy()).all()
+
+
+def test_rows_past_two_billion_elements():
+    """Key rows and query rows whose elements are counted past 2^31."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24 << 30:
+        pytest.skip("needs 20 GB")
+    m, n, h, d = 30, 1000, 8, 128
+    far = 2 ** 31 // (h * d) + 5
+    kv_rows = torch.empty((far + n, h, d), dtype=BF16, device=dev())
+    kv_rows[far:] = normal((n, h, d), 1)
+    q = normal((m, 2 * h, d), 2)
+    got = kv.kv_attention_prompt(q, kv_rows, kv_rows, i32([0, m]), i32([far, far + n]))
+    o, b = expect(q, kv_rows[far:], kv_rows[far:], starts([m]), starts([n]), d ** -0.5)
+    ref.check(got, o, b)
+    far = 2 ** 31 // (2 * h * d) + 3
+    rows = torch.empty((far + m, 2 * h, d), dtype=BF16, device=dev())
+    rows[far:] = q
+    out = torch.empty_like(rows)
+    kv.kv_attention_prompt(rows, kv_rows[-n:], kv_rows[-n:], i32([far, far + m]), i32([0, n]), out=out)
+    ref.check(out[far:], o, b)

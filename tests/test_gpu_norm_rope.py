@@ -166,3 +166,28 @@ def test_binding_refusals():
     q = c["q"].contiguous()
     with pytest.raises(kv.KVError):   # q_out one row into query: another head's rows
         kv.kv_qk_norm_rope_write(q[:3], c["k"][:3], None, c["qw"], c["kw"], c["pos"], c["cs"], q_out=q[1:])
+
+
+def test_rows_past_two_billion_elements():
+    """Token strides and slots whose elements are counted past 2^31."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 30 GB")
+    n, hq, h, d, T = 3, 8, 8, 128, 16
+    c = case(n, hq, h, d, d, seed=3, packed=False)
+    (wq, bq), (wk, bk) = want(c, d, False, 1e-6)
+    stride = 2 ** 30 + 8                               # the last token's row starts past 2^31
+    far = {}
+    for name in ("q", "k", "v"):
+        buffer = torch.empty(2 * stride + h * d, dtype=BF16, device=dev())
+        far[name] = buffer.as_strided((n, h, d), (stride, d, 1))
+        far[name].copy_(c[name])
+    blocks = 2 ** 31 // (T * h * d) + 2
+    kc = torch.empty((1, blocks, T, h, d), dtype=BF16, device=dev())
+    vc = torch.empty_like(kc)
+    slots = torch.arange(n, device=dev()) + (blocks - 1) * T + 5
+    q_out, k_out = kv.kv_qk_norm_rope_write(far["q"], far["k"], far["v"], c["qw"], c["kw"], c["pos"], c["cs"],
+                                            k_cache=kc, v_cache=vc, slot_mapping=slots)
+    ref.check(q_out, wq, bq, "q")
+    ref.check(k_out, wk, bk, "k")
+    assert torch.equal(kc[0, -1, 5:5 + n], k_out) and torch.equal(vc[0, -1, 5:5 + n], c["v"])

@@ -27,7 +27,7 @@
 // (request, head) leaves its sums in the workspace; a second kernel joins those.
 //
 // Measured (32 query heads, 8 KV heads of 128 channels): 8 contexts of 131072 tokens 222 us
-// (1.21 GB, 5.4 TB/s), 256 contexts of 512 to 4096 tokens 130 us (0.64 GB, 4.9 TB/s), one of 1009
+// (1.21 GB, 5.4 TB/s), 256 contexts of 512 to 4096 tokens 132 us (0.64 GB, 4.9 TB/s), one of 1009
 // 8.7 us, of which the second kernel is 2.5, one of 16384 13.6.  A unit of 32 tokens of one head is 4608 bytes and about
 // 600 instructions of a warp, half of them on the logic pipe (taking the codes apart); with 12
 // warps an SM issues 2.3 of 4 a cycle.  16 warps of 128 registers spill (253 us), 14 leave two
@@ -52,6 +52,7 @@ constexpr int kCtas = 1;                  // per SM: 12 warps of 168 registers, 
 constexpr int kStages = 3;
 constexpr int kUnit = 32;                 // tokens of a unit
 constexpr int kWindow = 8 * kUnit;        // tokens of a table lookup
+constexpr int kJoinRows = 4;              // rows of a CTA of the join, where a warp takes one
 constexpr float kRefStart = -1e30f;       // below every logit, and finite
 constexpr float kLimit = 256.0f;          // a weight times its scale above this raises the reference
 constexpr float kUnitMin = 7.888609e-31f, kUnitMax = 1.2676506e30f;  // 2^-100, 2^100
@@ -739,13 +740,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
 // tokens take 4 us with 16 warps, 11 with 8 warps and 4 parts at a time.  Each lane has D / 32
 // channels.
 template <int G, int NQ, int W>
-__global__ void __launch_bounds__(32 * W) join_q4_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(W == 1 ? 32 * kJoinRows : 32 * W) join_q4_kernel(AttnArgs a) {
   constexpr int D = 32 * G, kFirst = W == 1 ? 2 : 4, kMore = 8;
   __shared__ float s_o[W][D], s_l[W], s_top[W];
   pdl_allow_next();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.x / a.q_heads, qh = blockIdx.x - r * a.q_heads;
+  const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
+  const unsigned row = W == 1 ? blockIdx.x * kJoinRows + (threadIdx.x >> 5) : blockIdx.x;
+  if (W == 1 && row >= (unsigned)a.num_reqs * (unsigned)a.q_heads) return;
+  const int r = row / (unsigned)a.q_heads, qh = row - r * a.q_heads;
   const int rounds = a.at.kv_heads * a.passes / a.gang;
   const int64_t at = a.offsets[r], after = a.offsets[r + 1], total = a.offsets[a.num_reqs];
   if (after == at) return;  // zeros, already written
@@ -849,7 +852,8 @@ int launch(const AttnArgs& a, cudaStream_t stream) {
   const int parts = a.gangs / a.num_reqs;
   if (parts >= 32) return launch_pdl(join_q4_kernel<G, NQ, 16>, rows, 32 * 16, 0, stream, a);
   if (parts >= 8) return launch_pdl(join_q4_kernel<G, NQ, 8>, rows, 32 * 8, 0, stream, a);
-  return launch_pdl(join_q4_kernel<G, NQ, 1>, rows, 32, 0, stream, a);
+  return launch_pdl(join_q4_kernel<G, NQ, 1>, (rows + kJoinRows - 1) / kJoinRows, 32 * kJoinRows,
+                    0, stream, a);
 }
 
 template <int G>

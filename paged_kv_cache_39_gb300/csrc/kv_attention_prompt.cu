@@ -41,11 +41,11 @@
 //
 // Many pairs.  A CTA that runs takes over the pairs of CTAs that wait (see kv_tc.cuh), so that
 // the start of the next pair (search, loads, first scores) overlaps the end of this one: 64 prompts
-// of 128 tokens 74 -> 47 us, 256 of 64 207 -> 85.
+// of 128 tokens 74 -> 41 us, 256 of 64 207 -> 72.
 //
 // Measured (32 query heads, 8 KV heads of 128 channels): one prompt of 32768 tokens 5.3 to 5.4 ms
 // (1630 to 1660 TFLOP/s, near the card's power limit, 1.92 GHz), 16 chunks of 9 to 1855 tokens behind
-// up to 7685 370 us (1350 TFLOP/s), 77 tokens 8.6 us.  Per 128 keys a CTA's two tiles take 2900
+// up to 7685 367 us (1370 TFLOP/s), 77 tokens 7.6 us.  Per 128 keys a CTA's two tiles take 2900
 // cycles: 2048 of matrix instructions; a tile's softmax is 1140, beside the other tile's products,
 // and its S, softmax and O follow one another with the barriers' times between them.
 #include <cuda_bf16.h>
@@ -82,6 +82,20 @@ struct PromptArgs {
   __nv_bfloat16* out;
   int32_t* err;
 };
+
+// One step of a transposition over lanes: with the lane `mask` away, a for its b (the lower of the
+// two lanes keeps its a, the higher its b).
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b, bool high, int mask) {
+  const uint32_t got = __shfl_xor_sync(kFull, high ? a : b, mask);
+  a = high ? got : a;
+  b = high ? b : got;
+}
+__device__ __forceinline__ void exchange(uint4& a, uint4& b, bool high, int mask) {
+  exchange(a.x, b.x, high, mask);
+  exchange(a.y, b.y, high, mask);
+  exchange(a.z, b.z, high, mask);
+  exchange(a.w, b.w, high, mask);
+}
 
 template <int DP>
 struct Smem {
@@ -776,8 +790,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
           tc_fence_after();
           const bool check = *any_bad != 0;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key seen: zeros
+          // 4 lanes hold 4 rows; they exchange 16-byte pieces, so that a store writes 64 bytes of
+          // each of 8 rows (a row a lane, 16 bytes of 32 rows at a time, took 2 us a pair)
           __nv_bfloat16* out =
-              a.out + ((int64_t)(x.q0 + i) * a.q_heads + x.head * a.group + g) * a.head_dim;
+              a.out + ((int64_t)(x.q0 + x.t0 + t * a.tq) * a.q_heads + x.head * a.group) * a.head_dim +
+              8 * (lane & 3);
+          const int own = mine ? (tok * a.q_heads + g) * a.head_dim : -1;
+          int to[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) to[y] = __shfl_sync(kFull, own, (lane & 28) + y);
 #pragma unroll 1
           for (int b = 0; b < DP / 32; ++b) {
             uint32_t o[32];
@@ -797,16 +818,25 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
                                 __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
               continue;
             }
+            uint4 z[4];
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              uint4 z;
-              z.x = pack_bf16(__uint_as_float(o[y]) * inv, __uint_as_float(o[y + 1]) * inv);
-              z.y = pack_bf16(__uint_as_float(o[y + 2]) * inv, __uint_as_float(o[y + 3]) * inv);
-              z.z = pack_bf16(__uint_as_float(o[y + 4]) * inv, __uint_as_float(o[y + 5]) * inv);
-              z.w = pack_bf16(__uint_as_float(o[y + 6]) * inv, __uint_as_float(o[y + 7]) * inv);
-              if (mine && 32 * b + y < a.head_dim)
-                *reinterpret_cast<uint4*>(out + 32 * b + y) = z;
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t* e = o + 8 * y;
+              auto two = [&](int k) { return pack_bf16(__uint_as_float(e[k]) * inv, __uint_as_float(e[k + 1]) * inv); };
+              z[y] = make_uint4(two(0), two(2), two(4), two(6));
             }
+#pragma unroll
+            for (int m = 1; m < 4; m <<= 1) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if (y & m) continue;
+                exchange(z[y], z[y + m], lane & m, m);
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (to[y] >= 0 && 32 * b + 8 * (lane & 3) < a.head_dim)
+                *reinterpret_cast<uint4*>(out + to[y] + 32 * b) = z[y];
           }
           if (kSplit && x.parts > 1)
             reinterpret_cast<float2*>(smem + L::kStats)[t * kTile + row] = make_float2(ref, sum);

@@ -148,3 +148,8 @@ def test_binding_refuses_cpu_tensors_and_bad_caches():
         kv.new_q4_cache(1, 4, 16, 8, 96, device="cpu")
     c = kv.new_q4_cache(2, 4, 16, 8, 128, device="cpu")
     assert tuple(c.shape) == (2, 4, 8, 16 * 72) and c.dtype == torch.uint8
+
+
+@pytest.mark.parametrize("change", [dict(nq=2 ** 31 - 60000), dict(nk=2 ** 31 - 1)])
+def test_prompt_attention_refuses_rows_past_its_indices(lib, change):
+    assert lib.kv_attention_prompt(*{**PROMPT, **change}.values()) == -2

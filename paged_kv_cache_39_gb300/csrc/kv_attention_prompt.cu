@@ -63,6 +63,7 @@ constexpr int kThreads = 384;
 constexpr int kScrubThreads = 64;
 constexpr int kReaders = 11;               // warps that a work description is passed on to
 constexpr int kEdges = 3;                  // K/V tiles a CTA's rows see in part: 256 tokens span at most 3
+constexpr int kL2Share = 48 << 20;        // K and V of all heads stay in the L2 up to this (of 129 MB)
 constexpr int kSplitMax = 16;              // the largest cluster
 constexpr int kSplitFrom = 6;              // K/V tiles from which on a split pays for its join (3 us)
 constexpr int kSplitTiles = 2;             // least of them that a CTA takes
@@ -78,6 +79,7 @@ struct PromptArgs {
   int32_t group, tq;       // query heads per KV head, tokens per tile
   int32_t items;           // upper bound of (request, tile pair), the grid's extent per head
   int32_t split;           // CTAs of a cluster, which share a tile pair's keys
+  int32_t by_head;         // all pairs of one head come before the next head's
   float scale_log2;
   __nv_bfloat16* out;
   int32_t* err;
@@ -232,16 +234,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   // pair are neighbours, so the request's K and V are in L2 for all of them.  Every thread
   // counts the pairs of its share of the requests, a block-wide scan places them, the thread
   // that owns pair `want` describes it.
-  // A single request has no others to be ranked with: its heads follow one another instead, so
-  // that one head's K and V (16.8 MB at 32768 tokens) serve all CTAs at a time (5.60 against
-  // 5.66 ms).
-  const bool single = a.num_reqs == 1;
   const bool rank = a.num_reqs > 1 && a.num_reqs <= kThreads;
   const int pair_tokens = 2 * a.tq;
   const int split = kSplit ? a.split : 1;
   const int rank_in = kSplit ? (int)(blockIdx.x % (unsigned)split) : 0;
-  auto head_of = [&](int block) { return single ? block / a.items : block % a.kv_heads; };
-  auto want_of = [&](int block) { return single ? block % a.items : block / a.kv_heads; };
+  auto head_of = [&](int block) { return a.by_head ? block / a.items : block % a.kv_heads; };
+  auto want_of = [&](int block) { return a.by_head ? block % a.items : block / a.kv_heads; };
   auto pairs = [&](const Work& x) { return (int)(((int64_t)x.m + pair_tokens - 1) / pair_tokens); };
   uint32_t err = 0;
   auto describe = [&](int r) {  // request r, or one without rows where it is not valid
@@ -1046,8 +1044,13 @@ extern "C" int kv_attention_prompt(const void* query, int64_t query_stride, cons
   // sum of ceil(m_r / pair) over the requests with a row, of which there are `some` at most
   const int some = num_reqs < num_q_tokens ? num_reqs : num_q_tokens;
   const int64_t items = (int64_t)(num_q_tokens - some) / (2 * tq) + some;
+  // A single request has no others to be ranked with, and where its K and V are more than the L2
+  // can be trusted with beside what else passes through it, its heads follow one another, so that one
+  // head's K and V serve all CTAs at a time: 5.44 against 5.56 ms at 32768 tokens (134 MB), the same
+  // at 12288 (50 MB); 111 against 92 us at 4096, where the longest pairs of all heads first count.
+  const bool by_head = num_reqs == 1 && num_k_tokens * k_row * 4 > (int64_t)kL2Share;
   PromptArgs a{q_start_loc, k_start_loc, num_reqs, num_q_tokens, num_k_tokens, num_q_heads,
-               num_kv_heads, head_dim, group, tq, (int32_t)items, 1,
+               num_kv_heads, head_dim, group, tq, (int32_t)items, 1, by_head,
                scale * 1.44269504088896340736f, static_cast<__nv_bfloat16*>(out), d_err};
   return head_dim <= 64 ? launch<64>(a, q_map, k_map, v_map, stream)
                         : launch<128>(a, q_map, k_map, v_map, stream);

@@ -536,10 +536,11 @@ int kv_qk_norm_rope_write(const void* query, int64_t query_stride, const void* k
  * nothing to it, whatever they hold.  A NaN or an infinity in a value row makes
  * that channel NaN or infinite for the queries that see the row.  Query rows of
  * no request are left as they were.  A request whose rows are out of order or
- * out of range sets KV_ERR_BAD_QSL and is skipped; query rows that two requests
- * claim (with such a one between them) hold either's result, and where the requests
- * claim more than num_q_tokens rows together, some are left as they were.  Products and sums are held in 32 bits; the
- * weights are rounded to bf16 for their product with V.  Every wait of the
+ * out of range, or that has more than 2^24 key rows, sets KV_ERR_BAD_QSL and is
+ * skipped; query rows that two requests claim (with such a one between them) hold
+ * either's result, and where the requests claim more than num_q_tokens rows
+ * together, some are left as they were.  Products and sums are held in 32 bits;
+ * the weights are rounded to bf16 for their product with V.  Every wait of the
  * kernel is bounded (see "Bounded waits").
  * Errors: KV_EINVAL for null or misaligned pointers, negative sizes, a stride
  * below the row, num_q_heads not a multiple of num_kv_heads, a scale that is

@@ -63,6 +63,8 @@ constexpr int kThreads = 384;
 constexpr int kScrubThreads = 64;
 constexpr int kReaders = 11;               // warps that a work description is passed on to
 constexpr int kEdges = 3;                  // K/V tiles a CTA's rows see in part: 256 tokens span at most 3
+constexpr int kMaxKeys = 1 << 24;         // of a request: the longest wait in a CTA is the edge's, for all
+                                          // tiles before it, 0.2 s at this length; waits end at 1 s
 constexpr int kL2Share = 48 << 20;        // K and V of all heads stay in the L2 up to this (of 129 MB)
 constexpr int kSplitMax = 16;              // the largest cluster
 constexpr int kSplitFrom = 6;              // K/V tiles from which on a split pays for its join (3 us)
@@ -244,7 +246,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   uint32_t err = 0;
   auto describe = [&](int r) {  // request r, or one without rows where it is not valid
     const int q0 = a.q_start[r], q1 = a.q_start[r + 1], k0 = a.k_start[r], k1 = a.k_start[r + 1];
-    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.nq && k0 >= 0 && k1 >= k0 && k1 <= a.nk;
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.nq && k0 >= 0 && k1 >= k0 && k1 <= a.nk &&
+                    k1 - k0 <= kMaxKeys;
     if (!ok) err |= KV_ERR_BAD_QSL;
     return ok ? Work{q0, k0, q1 - q0, k1 - k0, 0, 0} : Work{0, 0, 0, 0, 0, 0};
   };

@@ -143,3 +143,16 @@ def test_rows_past_two_billion_elements():
     out = torch.empty_like(rows)
     kv.kv_attention_prompt(rows, kv_rows[-n:], kv_rows[-n:], i32([far, far + m]), i32([0, n]), out=out)
     ref.check(out[far:], o, b)
+
+
+def test_the_longest_request_and_one_that_is_longer():
+    n = 2 ** 24
+    q = normal((5, 1, 8), 1)
+    k = torch.zeros((n + 1, 1, 8), dtype=BF16, device=dev())
+    v = torch.ones_like(k)
+    err = kv.new_error_word(dev())
+    got = kv.kv_attention_prompt(q, k, v, i32([0, 5]), i32([0, n]), err=err)
+    assert (got == 1).all() and err.item() == 0   # sums of ones: exact in 32 bits up to 2^24
+    out = torch.full_like(q, 7.0)
+    kv.kv_attention_prompt(q, k, v, i32([0, 5]), i32([0, n + 1]), out=out, err=err)
+    assert (out == 7).all() and err.item() == kv.ERR_BITS["BAD_QSL"]

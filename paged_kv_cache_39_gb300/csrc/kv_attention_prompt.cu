@@ -534,7 +534,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
           int j = x.first;
           bool add = false;
           // the usual step by itself, with as little as can be between the waits: what the issue
-          // takes longer, the matrix unit waits (6.2 ms at 32768 tokens with the loop below alone)
+          // takes longer, the matrix unit waits (5.9 ms at 32768 tokens with the loop below alone)
           if (x.two) {
 #pragma unroll 1
             for (; j + 2 < x.end && j < x.whole; ++j) {

@@ -8,8 +8,9 @@
 // 2^-10 away from every one, and the integer q nearest to x times an approximate 1 / s (within
 // 2^-22) is right unless x / s is a tie.  Then, and only then, 2 |x - q s| == s, which is exact in
 // 32 bits; groups with a tie are done again value by value.  No clamp is needed.
-// 8 lanes quantise a head's K and V rows: 8192 tokens of 8 x 128 take 18 us (43 MB), bound by the
-// instructions (800 a warp; 1290 and 25 us with divisions and value by value).
+// 8 lanes quantise a head's K and V rows, each lane finding one of the 8 groups' scales: 8192
+// tokens of 8 x 128 take 11.6 us (43 MB), bound by the instructions (14.3 with every scale found
+// by 8 lanes, 25 with divisions and value by value); 256 tokens 3.5 us.
 #include "kv_q4.cuh"
 
 namespace kvp {
@@ -61,23 +62,32 @@ __device__ __noinline__ uint32_t codes_with_ties(float v0, float v1, float v2, f
   return c;
 }
 
-// One row of one head by 8 lanes: lane g holds channels 32 j + 4 g .. + 3.  `top`: the largest
-// magnitudes of the groups as bf16 bits, two groups to a word.
+// The scale of the group whose largest magnitude has the bits m.
+struct Scale {
+  uint32_t bits;  // bf16
+  float half;     // half of it, or -1 where every code is 8 (zeros, or NaN and infinity)
+  float inv;      // about 1 / scale, or 0 there
+};
+__device__ __forceinline__ Scale scale_of(uint32_t m) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(over_seven(__uint_as_float(m)));
+  const float s = __bfloat162float(b);
+  Scale r{__bfloat16_as_ushort(b), 0.5f * s, 0.f};
+  if (s < 1.17549435e-38f) r.half = -1.f, r.bits = 0u;   // below the normal range: a group of zeros
+  if (m >= 0x7f800000u) r.half = -1.f, r.bits = 0x7fc0u;  // infinity or NaN: the group reads as NaN
+  if (r.half > 0.f) r.inv = rcp_approx(s);
+  return r;
+}
+
+// One row of one head by 8 lanes: lane g holds channels 32 j + 4 g .. + 3; lane `from` + j of the
+// warp holds the scale of group j.
 template <int G>
-__device__ __forceinline__ void quantise_row(const uint2 (&x)[G], const uint32_t (&top)[G / 2],
-                                             uint8_t* codes, uint8_t* scales, int g, bool store) {
+__device__ __forceinline__ void quantise_row(const uint2 (&x)[G], const Scale& mine, int from,
+                                             uint8_t* codes, int g, bool store) {
   uint32_t half[G];   // 4 codes of each group
-  uint32_t sbits[G];  // bf16 scales
 #pragma unroll
   for (int j = 0; j < G; ++j) {
-    const uint32_t m = j & 1 ? top[j / 2] & 0xffff0000u : top[j / 2] << 16;
-    const __nv_bfloat16 sb = __float2bfloat16_rn(over_seven(__uint_as_float(m)));
-    float s = __bfloat162float(sb);
-    sbits[j] = __bfloat16_as_ushort(sb);
-    if (s < 1.17549435e-38f) s = 0.f, sbits[j] = 0u;   // below the normal range: a group of zeros
-    if (m >= 0x7f800000u) s = 0.f, sbits[j] = 0x7fc0u;  // infinity or NaN: the group reads as NaN
-    const float inv = s > 0.f ? rcp_approx(s) : 0.f;
-    const float tie = s > 0.f ? 0.5f * s : -1.f;
+    const float tie = __shfl_sync(kFull, mine.half, from + j), s = tie + tie;
+    const float inv = __shfl_sync(kFull, mine.inv, from + j);
     const uint64_t v[2] = {pair(__uint_as_float(x[j].x << 16), __uint_as_float(x[j].x & 0xffff0000u)),
                            pair(__uint_as_float(x[j].y << 16), __uint_as_float(x[j].y & 0xffff0000u))};
     const uint64_t inv2 = pair(inv, inv), s2 = pair(s, s), round2 = pair(kRound, kRound);
@@ -104,16 +114,11 @@ __device__ __forceinline__ void quantise_row(const uint2 (&x)[G], const uint32_t
     half[j] = c;
   }
   if (!store) return;
-  if constexpr (G == 4) {
+  if constexpr (G == 4)
     *reinterpret_cast<uint2*>(codes + 8 * g) = make_uint2(__byte_perm(half[0], half[1], 0x5410),
                                                           __byte_perm(half[2], half[3], 0x5410));
-    if (g == 0)
-      *reinterpret_cast<uint2*>(scales) =
-          make_uint2(sbits[0] | sbits[1] << 16, sbits[2] | sbits[3] << 16);
-  } else {
+  else
     *reinterpret_cast<uint32_t*>(codes + 4 * g) = __byte_perm(half[0], half[1], 0x5410);
-    if (g == 0) *reinterpret_cast<uint32_t*>(scales) = sbits[0] | sbits[1] << 16;
-  }
 }
 
 // Largest magnitudes of the row's groups as integers (NaN > infinity > every finite value), two
@@ -175,8 +180,19 @@ __global__ void __launch_bounds__(kWriteThreads) write_q4_kernel(WriteArgs a) {
   uint32_t k_top[G / 2], v_top[G / 2];
   largest<G>(k, k_top);
   largest<G>(v, v_top);
-  quantise_row<G>(k, k_top, kc, ks, g, store);
-  quantise_row<G>(v, v_top, vc, vs, g, store);
+  // each lane finds one scale: K's groups in lanes 0 .. G - 1 of the 8, V's in the next G
+  const bool is_v = g & G;
+  const int group = g % G;
+  uint32_t word = is_v ? v_top[0] : k_top[0];
+  if constexpr (G == 4) {
+    if (group & 2) word = is_v ? v_top[1] : k_top[1];
+  }
+  const Scale mine = scale_of(group & 1 ? word & 0xffff0000u : word << 16);
+  if (store && g < 2 * G)
+    reinterpret_cast<uint16_t*>(is_v ? vs : ks)[group] = (uint16_t)mine.bits;
+  const int from = threadIdx.x & 24;
+  quantise_row<G>(k, mine, from, kc, g, store);
+  quantise_row<G>(v, mine, from + G, vc, g, store);
   report(a.err, err);
 }
 

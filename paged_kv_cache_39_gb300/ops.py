@@ -29,6 +29,10 @@ try:  # the current stream's handle, without a Stream object around it (about 1 
 except ImportError:
     def _raw_stream(device: int) -> int:
         return torch.cuda.current_stream(device).cuda_stream
+try:  # the tensors of a call exist, so CUDA is initialised
+    from torch._C import _cuda_getDevice as _current_device
+except ImportError:
+    _current_device = torch.cuda.current_device
 
 __all__ = [
     "Prepared",
@@ -71,13 +75,20 @@ class Prepared:
         return self.result
 
 
+_handles: dict = {}  # stream handles as C values
+
+
 def _stream(device: int) -> ctypes.c_void_p:
-    return ctypes.c_void_p(_raw_stream(device))
+    raw = _raw_stream(device)
+    handle = _handles.get(raw)
+    if handle is None:
+        handle = _handles[raw] = ctypes.c_void_p(raw)
+    return handle
 
 
 def _launch(name: str, fn, args: tuple, device: int) -> None:
     """The C call on the current stream of the tensors' device."""
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         status = fn(*args, _stream(device))
     else:
         with torch.cuda.device(device):

@@ -8,10 +8,13 @@
 // so the group scales never touch the codes: K's multiply the 32-bit partial sum of
 // their group, V's the weight.  u - 8 is exact in fp16, q is made exact by a power of
 // two per head (2^-24 of its largest channel is lost at most), w b is rounded to fp16
-// (2^-11 of a weight: fewer bits than that would double the output's own rounding
-// error).  ref is a running reference: the largest w b of a query was 1 when it was last
-// raised, and it is raised when one passes 2^8, so w b stays inside fp16 whatever the
-// scales are (between 2^-100 and 2^100); sums are held in 32 bits.
+// (2^-11 of it: fewer bits than that would double the output's own rounding error).  So that it
+// stays inside fp16 whatever the scales are, a query has a running reference, an integer at or
+// above its largest logit when last raised, and for each of its channel groups a power of two f_j:
+// the product's operand is w b f_j, the largest one of a group is 2^7 at least, and reference and f
+// are set anew when a weight or an operand passes 2^15.  An operand below 2^-14 keeps fewer bits,
+// at most 2^-32 of its own group's largest is lost then: groups and tokens of very different scales
+// do not cost each other bits.  f_j is taken off when a segment ends; sums are held in 32 bits.
 //
 // GPU shape.  The bytes of the cache bound this: 16 query rows at most read each of
 // them, far under a matrix unit tile of 128 rows, so the products go through the warp's
@@ -54,8 +57,9 @@ constexpr int kUnit = 32;                 // tokens of a unit
 constexpr int kWindow = 8 * kUnit;        // tokens of a table lookup
 constexpr int kJoinRows = 4;              // rows of a CTA of the join, where a warp takes one
 constexpr float kRefStart = -1e30f;       // below every logit, and finite
-constexpr float kLimit = 256.0f;          // a weight times its scale above this raises the reference
-constexpr float kUnitMin = 7.888609e-31f, kUnitMax = 1.2676506e30f;  // 2^-100, 2^100
+constexpr float kLimit = 32768.0f;        // a weight or an operand above this sets references anew
+constexpr int kTarget = 7;                // log2 of what a group's largest operand is set to, at least
+constexpr int kFactorMax = 127 + 112;     // exponent field of the largest f: f times a weight is finite
 
 struct AttnArgs {
   const __nv_bfloat16* q;
@@ -94,6 +98,13 @@ __device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// A power of two by its exponent field.
+__device__ __forceinline__ float pow2(int field) { return __uint_as_float((uint32_t)field << 23); }
+// The powers of two of a lane's two columns, as bf16.
+__device__ __forceinline__ uint32_t pack_pow2(int field0, int field1) {
+  return (uint32_t)field0 << 7 | (uint32_t)field1 << 23;
+}
+__device__ __forceinline__ int field_of(uint32_t f, int k) { return (f >> (k ? 23 : 7)) & 0xff; }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -425,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
   float qs[NT][G][2];        // -8 2^-24 sum q of a group, for those columns
   float o[NT][2 * G][4];     // sums: rows = channels, columns = query heads
   float ref[NT][2], sum[NT][2];
+  uint32_t fj[NT][G];        // f of each group, for those columns
   bool fresh = true, from_start = false;
   const int tok = (g >> 1) + 4 * (g & 1);               // this lane's token of each 8
   const uint32_t half_mask = g < 4 ? kFull : 0u;        // kPack: columns of tokens 0-15
@@ -504,6 +516,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
           sum[n][k] = 0.f;
         }
 #pragma unroll
+        for (int j = 0; j < G; ++j) fj[n][j] = pack_pow2(kFactorMax, kFactorMax);
+#pragma unroll
         for (int m = 0; m < 2 * G; ++m)
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[n][m][k] = 0.f;
@@ -576,52 +590,83 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
             for (int n = 0; n < NT; ++n) s[n][2 * h] = s[n][2 * h + 1] = -INFINITY;
           }
       }
-      float unit[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float m = fmaxf(vs[h][0], vs[h][1]);
-        if constexpr (G == 4) m = fmaxf(m, fmaxf(vs[h][2], vs[h][3]));
-        unit[h] = fminf(fmaxf(m, kUnitMin), kUnitMax);
-      }
       float most = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           w[n][k] = ex2(fmaf(s[n][k], qc[n][k & 1], -ref[n][k & 1]));
-          most = fmaxf(most, w[n][k] * unit[k >> 1]);
+          most = fmaxf(most, w[n][k]);
         }
-      if (__any_sync(kFull, most > kLimit)) {
-        // raise the references to the largest logit + log2(scale) of these tokens
-        const float l0 = log2f(unit[0]), l1 = log2f(unit[1]);
+      // w b f as fp16; the largest magnitude of all in `top`
+      __half2 top = __float2half2_rn(0.f);
+      auto operands = [&]() {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const float f0 = __uint_as_float(fj[n][j] << 16), f1 = __uint_as_float(fj[n][j] & 0xffff0000u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              b[j][n][h] = pack_f16(w[n][2 * h] * f0 * vs[h][j], w[n][2 * h + 1] * f1 * vs[h][j]);
+              top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&b[j][n][h])));
+            }
+          }
+      };
+      operands();
+      if (__any_sync(kFull, most > kLimit || !__hble2(top, __float2half2_rn(kLimit)))) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          int drop[2];  // log2 of what a reference rises by
+#pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float z = fmaxf(fmaf(s[n][k], qc[n][k], l0), fmaf(s[n][k + 2], qc[n][k], l1));
+            float z = fmaxf(s[n][k] * qc[n][k], s[n][k + 2] * qc[n][k]);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) z = fmaxf(z, __shfl_xor_sync(kFull, z, d));
-            const float up = fmaxf(ref[n][k], z), f = ex2(ref[n][k] - up);
+            const float up = fmaxf(ref[n][k], ceilf(z)), by = up - ref[n][k];
+            drop[k] = by < 400.f ? (int)by : 400;
+            sum[n][k] *= ex2(-by);
             ref[n][k] = up;
-            sum[n][k] *= f;
-#pragma unroll
-            for (int m = 0; m < 2 * G; ++m) {
-              o[n][m][k] *= f;
-              o[n][m][k + 2] *= f;
-            }
             w[n][k] = ex2(fmaf(s[n][k], qc[n][k], -up));
             w[n][k + 2] = ex2(fmaf(s[n][k + 2], qc[n][k], -up));
           }
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            // the largest w b of these tokens, its upper 16 bits, of both columns
+            uint32_t m[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              m[k] = __float_as_uint(fmaxf(w[n][k] * fabsf(vs[0][j]), w[n][k + 2] * fabsf(vs[1][j])));
+            uint32_t both = __byte_perm(m[0], m[1], 0x7632);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) both = __vmaxu2(both, __shfl_xor_sync(kFull, both, d));
+            int field[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int was = field_of(fj[n][j], k);
+              // what leaves the sums as they are, unless the largest needs it lower
+              field[k] = min(min(was + drop[k], kFactorMax), 2 * 127 + kTarget - field_of(both, k));
+              const int by = field[k] - was - drop[k];  // <= 0
+              const float f = by > -127 ? pow2(127 + by) : 0.f;
+#pragma unroll
+              for (int m = 2 * j; m < 2 * j + 2; ++m) {
+                o[n][m][k] *= f;
+                o[n][m][k + 2] *= f;
+              }
+            }
+            fj[n][j] = pack_pow2(field[0], field[1]);
+          }
+        }
+        operands();
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         sum[n][0] += w[n][0] + w[n][2];
         sum[n][1] += w[n][1] + w[n][3];
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-          b[j][n][0] = transpose8x8(pack_f16(w[n][0] * vs[0][j], w[n][1] * vs[0][j]));
-          b[j][n][1] = transpose8x8(pack_f16(w[n][2] * vs[1][j], w[n][3] * vs[1][j]));
-        }
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) b[j][n][h] = transpose8x8(b[j][n][h]);
       }
     };
     // V codes of 16 tokens (half u) times weight fragments; columns outside `keep` count as 0
@@ -684,6 +729,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const float f = pow2(2 * 127 - field_of(fj[n][j], k));
+#pragma unroll
+            for (int m = 2 * j; m < 2 * j + 2; ++m) {
+              o[n][m][k] *= f;
+              o[n][m][k + 2] *= f;
+            }
+          }
           float l = sum[n][k];
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);

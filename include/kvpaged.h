@@ -96,7 +96,7 @@ enum kv_error_bits {
  * kv_copy_blocks_bulk) wait on the copy engine, and kv_attention_prompt on it
  * and on the matrix unit; every such wait gives up
  * after 1 s of GPU time (the global nanosecond timer) or 2^22 tries,
- * whichever comes first; a CTA that gave up waits once more, with the same
+ * whichever comes first (kv_attention_prompt's counts from the fifth try); a CTA that gave up waits once more, with the same
  * bound, for each of its own loads still in flight, then ends.  A healthy
  * copy completes in microseconds, so a timeout means the GPU is in trouble.
  * After a call has set KV_ERR_TIMEOUT:
@@ -655,6 +655,18 @@ int64_t kv_attention_q4_workspace(int32_t num_reqs, int32_t num_q_heads, int32_t
  * Errors: KV_EINVAL for a limit out of range or a null/misaligned d_err.
  */
 int kv_diag_bounded_wait(int32_t spin_limit, int32_t* d_err, kv_stream_t stream);
+
+/*
+ * kv_diag_role_wait -- the same for the wait that the roles of kv_attention_prompt share:
+ * four warps wait, each on a shared-memory barrier that nothing will complete.  The last
+ * one gives up after limit_ns; the others, whose own limit is 1 s, leave when it has.
+ *   limit_ns     0 .. 10^9.
+ *   d_waited_ns  int64 [4]: how long each warp waited.
+ *   d_err        int32 device word (required): KV_ERR_TIMEOUT.
+ * Errors: KV_EINVAL for a limit out of range or a null/misaligned pointer.
+ */
+int kv_diag_role_wait(int64_t limit_ns, int64_t* d_waited_ns, int32_t* d_err,
+                      kv_stream_t stream);
 
 /* Human-readable name of a kv_status value (static string). */
 const char* kv_status_string(int status);

@@ -60,8 +60,33 @@ __global__ void bounded_wait_probe_kernel(int64_t limit, int32_t* err) {
   if (!mbar_wait_bounded(&bar, 0u, limit)) atomicOr(err, KV_ERR_TIMEOUT);
 }
 
+// The same with the wait that the prompt attention's roles share: warp w waits for a barrier of
+// its own that never completes.  The first to give up makes the others leave.
+__global__ void role_wait_probe_kernel(int64_t limit_ns, int64_t* waited_ns, int32_t* err) {
+  __shared__ uint64_t bars[4];
+  __shared__ int abort;
+  if (threadIdx.x < 4) mbar_init(&bars[threadIdx.x], 1);
+  if (threadIdx.x == 0) abort = 0;
+  mbar_fence_init();
+  __syncthreads();
+  const int warp = threadIdx.x >> 5;
+  const uint64_t t0 = global_ns();
+  const bool ok = mbar_wait_role(&bars[warp], 0u, &abort, warp == 3 ? (uint64_t)limit_ns : kWaitLimitNs);
+  if ((threadIdx.x & 31) == 0) waited_ns[warp] = (int64_t)(global_ns() - t0);
+  if (!__any_sync(kFull, ok)) report(err, KV_ERR_TIMEOUT);
+}
+
 }  // namespace
 }  // namespace kvp
+
+extern "C" int kv_diag_role_wait(int64_t limit_ns, int64_t* d_waited_ns, int32_t* d_err,
+                                 kv_stream_t stream) {
+  if (limit_ns < 0 || limit_ns > (int64_t)kvp::kWaitLimitNs || d_waited_ns == nullptr ||
+      !kvp::aligned(d_waited_ns, 8) || d_err == nullptr || !kvp::aligned(d_err, 4))
+    return KV_EINVAL;
+  kvp::role_wait_probe_kernel<<<1, 128, 0, stream>>>(limit_ns, d_waited_ns, d_err);
+  return kvp::launch_status();
+}
 
 extern "C" int kv_diag_bounded_wait(int32_t spin_limit, int32_t* d_err, kv_stream_t stream) {
   if (spin_limit < 1 || spin_limit > (1 << 20) || d_err == nullptr ||

@@ -117,21 +117,22 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// Wait for a phase, bounded like mbar_wait_bounded, but with no timer on the usual path: the
-// timer starts after the first tries (a try suspends the thread for a while, so these pass in
-// milliseconds at most).  Gives up when another role of the CTA has (*abort), and tells the
-// others when it does.
-__device__ __forceinline__ bool mbar_wait_role(uint64_t* bar, uint32_t parity,
-                                               volatile int* abort) {
+// Wait for a phase, bounded like mbar_wait_bounded, but with no timer on the usual path: it
+// starts after kUntimedTries (a try may suspend the thread for as long as the hardware likes, so
+// only the timer bounds the time).  From then on every try is followed by a look at whether
+// another role of the CTA has given up (*abort); one that gives up tells the others.
+constexpr int kUntimedTries = 4;
+__device__ __forceinline__ bool mbar_wait_role(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                               uint64_t limit_ns = kWaitLimitNs) {
 #pragma unroll 1
-  for (int i = 0; i < 4096; ++i)
+  for (int i = 0; i < kUntimedTries; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
 #pragma unroll 1
   for (long i = 0; i < kSpinLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort != 0) return false;
-    if (global_ns() - t0 > kWaitLimitNs) break;
+    if (global_ns() - t0 > limit_ns) break;
   }
   *abort = 1;
   return false;

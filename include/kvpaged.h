@@ -668,6 +668,26 @@ int kv_diag_bounded_wait(int32_t spin_limit, int32_t* d_err, kv_stream_t stream)
 int kv_diag_role_wait(int64_t limit_ns, int64_t* d_waited_ns, int32_t* d_err,
                       kv_stream_t stream);
 
+/*
+ * kv_diag_attention_prompt_stall -- self-test of kv_attention_prompt's bounded waits, through
+ * its own kernels: in every CTA, as it starts on its work number `item` (counted from 0; a CTA
+ * without that much work runs on as usual), one role waits limit_ns for a barrier that nothing
+ * will complete, then gives up.  The CTA's other roles leave at their next wait, it waits for its
+ * copies and matrix instructions in flight and ends; KV_ERR_TIMEOUT arrives; the context stays
+ * usable.  The outputs are undefined.
+ *   role      0 copies, 1 matrix instructions, 2 check of values, 3 and 4 softmax.
+ *   limit_ns  0 .. 10^9.
+ *   d_err     required.
+ * Errors: those of kv_attention_prompt; KV_EINVAL for a role, item or limit out of range.
+ */
+int kv_diag_attention_prompt_stall(const void* query, int64_t query_stride, const void* key,
+                                   int64_t key_stride, const void* value, int64_t value_stride,
+                                   const int32_t* q_start_loc, const int32_t* k_start_loc,
+                                   int32_t num_reqs, int32_t num_q_tokens, int32_t num_k_tokens,
+                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   float scale, void* out, int32_t* d_err, int32_t role,
+                                   int32_t item, int64_t limit_ns, kv_stream_t stream);
+
 /* Human-readable name of a kv_status value (static string). */
 const char* kv_status_string(int status);
 

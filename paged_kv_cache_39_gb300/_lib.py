@@ -72,6 +72,9 @@ SIGNATURES = {
     "kv_attention_q4": ([_P, _I64, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _P, _I32, _P,
                          _P, _I32, _F32, _P, _P, _I64, _P, _P], ctypes.c_int),
     "kv_diag_bounded_wait": ([_I32, _P, _P], ctypes.c_int),
+    "kv_diag_attention_prompt_stall": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _I32, _I32,
+                                        _I32, _I32, _I32, _F32, _P, _P, _I32, _I32, _I64, _P],
+                                       ctypes.c_int),
     "kv_diag_role_wait": ([_I64, _P, _P, _P], ctypes.c_int),
     "kv_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "kv_abi_version": ([], ctypes.c_int),

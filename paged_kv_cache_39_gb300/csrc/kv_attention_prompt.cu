@@ -85,7 +85,11 @@ struct PromptArgs {
   float scale_log2;
   __nv_bfloat16* out;
   int32_t* err;
+  // the self-test's: which role waits for nothing, at which of its CTA's items, for how long
+  int32_t stall_role, stall_item;
+  int64_t stall_ns;
 };
+enum Role { kLoader, kIssuer, kChecker, kSoftmax };  // kSoftmax + tile
 
 // One step of a transposition over lanes: with the lane `mask` away, a for its b (the lower of the
 // two lanes keeps its a, the higher its b).
@@ -113,8 +117,7 @@ struct Smem {
   static constexpr int kNumBars = 2 * kSlots + 4 * kEdges + 20;
   static constexpr int kBad = kBars + kNumBars * 8;         // int[DP]: first key not finite
   static constexpr int kMisc = kBad + DP * 4;
-  static constexpr int kInFlight = kMisc + 16;              // uint32_t[8]: a slot's last barrier
-  static constexpr int kAnswer = kInFlight + 32;            // 16 bytes: the work taken over
+  static constexpr int kAnswer = kMisc + 16;                // 16 bytes: the work taken over
   static constexpr int kWork = kAnswer + 16;                // Work[2]
   static constexpr int kOrder = kWork + 64;                 // uint16_t[kThreads]: requests by keys
   static constexpr int kBytes = kOrder + kThreads * 2 + 1024;  // + alignment of the base
@@ -164,6 +167,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Behind a role's last wait, read and issue: all roles of the CTA have come so far.
+__device__ __forceinline__ void roles_met() {
+  tc_fence_before();
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+  tc_fence_after();
+}
+
 // Three kernels of one body, so that none has another's registers and code in its way (with the
 // join in all: 5.63 instead of 5.46 ms at 32768 tokens).
 enum Mode {
@@ -171,7 +182,7 @@ enum Mode {
   kManyWaves,  // those that run take over the work of those that wait
   kClusters,   // `split` CTAs share an item
 };
-template <int DP, Mode kMode>
+template <int DP, Mode kMode, bool kStall>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map, PromptArgs a) {
@@ -202,11 +213,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort = misc + 1;
   volatile int* any_bad = misc + 2;
-  uint32_t* in_flight = reinterpret_cast<uint32_t*>(smem + L::kInFlight);
   Work* s_work = reinterpret_cast<Work*>(smem + L::kWork);
   uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::kOrder);
+  __shared__ uint64_t nothing;  // kStall: a barrier that nobody arrives on
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform for the compiler, too
+  if constexpr (kStall) {
+    if (tid == 0) mbar_init(&nothing, 1);
+  }
 
   if (tid < L::kNumBars) {
     const uint64_t* b = &bars[tid];
@@ -330,6 +344,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     return __all_sync(kFull, ok) ? read(item + 1) : none;
   };
 
+  // The self-test: this role gives up at this item.
+  auto stalled = [&](int role, int item) {
+    if constexpr (kStall) {
+      if (role == a.stall_role && item == a.stall_item)
+        return !mbar_wait_role(&nothing, 0, abort, (uint64_t)a.stall_ns);
+    }
+    return false;
+  };
+
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
@@ -341,12 +364,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         tma_prefetch_map(&v_map);
       }
       int slot = 0, turn = 0, items = 0, loaded = 0;
-      uint32_t edge_at = 0;     // bits: parities of the next use
+      uint32_t edge_at = 0, edge_used = 0;  // bits: parities of the next use; used at all
       int base = 0;             // where the search for the next item goes on: requests and
       int64_t base_at = 0;      // pairs before it
       bool ok = true, asked = false;
       Work w = read(0);
       for (int item = 0; w.m > 0; ++item) {
+        if (stalled(kLoader, item)) break;
         const Item x(w, a, split, rank_in);
         if (x.end > x.first) {
           if (loaded > 0) ok = __all_sync(kFull, mbar_wait_role(q_free, (loaded - 1) & 1, abort));
@@ -371,14 +395,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
             const int e = is_v && j >= x.whole ? (item & 1) * kEdges + j - x.whole : -1;
             uint64_t* bar = e >= 0 ? &edge[e] : &full[slot];
             if (leader) {
-              in_flight[slot] = smem_addr(bar) | (e >= 0 ? (edge_at >> e) & 1 : turn & 1);
               if (e >= 0) mbar_arrive(&full[slot]);  // its phases count the turns of the ring
               mbar_arrive_expect_tx(bar, L::kTileBytes);
               for (int c = 0; c < DP / 64; ++c)
                 tma_load_3d(smem + L::kRing + slot * L::kTileBytes + c * (kTile * 128),
                             is_v ? &v_map : &k_map, 64 * c, x.head, x.k0 + j * kTile, bar);
             }
-            if (e >= 0) edge_at ^= 1u << e;
+            if (e >= 0) {
+              edge_at ^= 1u << e;
+              edge_used |= 1u << e;
+            }
             if (++slot == L::kSlots) {
               slot = 0;
               ++turn;
@@ -440,14 +466,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         }
         __syncwarp();
       }
-      if (__any_sync(kFull, *abort != 0)) {  // bounded wait for the copies still in flight
+      // Where a wait ran out, wait (with a bound) for the copies still in flight: only now, when
+      // the other roles have left, is it known that none did, and no shared memory is given up or
+      // written by a split's join before this.
+      roles_met();
+      if (__any_sync(kFull, *abort != 0)) {
         if (loaded > 0) mbar_wait_bounded(q_full, (loaded - 1) & 1);
         if (asked) mbar_wait_bounded(stolen, items & 1);
-        __syncwarp();
-        for (int i = 0; i < L::kSlots; ++i)
-          if (turn > 0 || i < slot)
-            mbar_wait_bounded(reinterpret_cast<uint64_t*>(smem + ((in_flight[i] & ~1u) - smem_addr(smem))),
-                              in_flight[i] & 1u);
+        for (int i = 0; i < L::kSlots; ++i) {
+          const int uses = turn + (i < slot ? 1 : 0);
+          if (uses > 0) mbar_wait_bounded(&full[i], (uses - 1) & 1);
+        }
+        for (int e = 0; e < 2 * kEdges; ++e)
+          if ((edge_used >> e) & 1u) mbar_wait_bounded(&edge[e], ((edge_at >> e) & 1u) ^ 1u);
       }
     } else if (warp == 9) {
       // -------------------------------------------------------------- matrix instructions
@@ -484,6 +515,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       bool ok = true;
       Work w = read(0);
       for (int item = 0; w.m > 0; ++item) {
+        if (stalled(kIssuer, item)) break;
         const Item x(w, a, split, rank_in);
         if (x.end > x.first) {
           ok = mbar_wait_role(q_full, loaded & 1, abort) && mbar_wait_role(&full[sk], pk, abort);
@@ -586,6 +618,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       __syncwarp();
       if (leader) mma_commit(drain);
       mbar_wait_bounded(drain, 0);
+      roles_met();
     } else {
       // -------------------------------------------------------------- V at the causal edge
       const int st = tid - 10 * 32;
@@ -594,6 +627,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       bool both = false;  // the item before had two tiles
       Work w = read(0);
       for (int item = 0; w.m > 0; ++item) {
+        if (stalled(kChecker, item)) break;
         const Item x(w, a, split, rank_in);
         if (x.end > x.first) {
           bool ok = true;
@@ -668,6 +702,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
         }
         w = following(item);
       }
+      roles_met();
     }
     if constexpr (kSplit) {  // the softmax warps' join
       cluster_sync();
@@ -685,6 +720,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
     int done = 0;
     Work w = read(0);
     for (int item = 0; w.m > 0; ++item) {
+      if (stalled(kSoftmax + t, item)) break;
       const Item x(w, a, split, rank_in);
       const bool work = x.end > x.first;
       if (x.tiles == 0 && rank_in == 0) {  // no query here sees a key
@@ -850,6 +886,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       done += work;
       w = following(item);
     }
+    roles_met();
     if constexpr (kSplit) {
       // -------------------------------------------------------------- join of a split
       const Item x(read(0), a, split, rank_in);
@@ -913,10 +950,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       cluster_sync();  // no CTA ends while another reads its shared memory
     }
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   if (warp == 9) {
     tmem_dealloc(tmem, 512);
     if (lane == 0 && *abort != 0 && a.err != nullptr) atomicOr(a.err, KV_ERR_TIMEOUT);
@@ -934,7 +967,7 @@ int clusters_at_once(int size) {
   std::lock_guard<std::mutex> lock(mu);
   int& n = cached[dev][size];
   if (n == 0) {
-    auto kernel = prompt_kernel<DP, kClusters>;
+    auto kernel = prompt_kernel<DP, kClusters, false>;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)size;
@@ -971,10 +1004,10 @@ int choose_split(int64_t pairs, int64_t keys) {
   return (int)split;
 }
 
-template <int DP, Mode kMode>
+template <int DP, Mode kMode, bool kStall>
 int launch(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
            cudaStream_t stream) {
-  auto kernel = prompt_kernel<DP, kMode>;
+  auto kernel = prompt_kernel<DP, kMode, kStall>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Smem<DP>::kBytes) != cudaSuccess)
     return KV_ECUDA;
@@ -988,26 +1021,24 @@ int launch(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, cons
                              Smem<DP>::kBytes, stream, q, k, v, a);
 }
 
-template <int DP>
+template <int DP, bool kStall = false>
 int launch(PromptArgs a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
            cudaStream_t stream) {
   a.split = choose_split<DP>((int64_t)a.items * a.kv_heads, a.nk);
-  if (a.split > 1) return launch<DP, kClusters>(a, q, k, v, stream);
-  return (int64_t)a.items * a.kv_heads > sm_count() ? launch<DP, kManyWaves>(a, q, k, v, stream)
-                                                    : launch<DP, kOneWave>(a, q, k, v, stream);
+  if (a.split > 1) return launch<DP, kClusters, kStall>(a, q, k, v, stream);
+  return (int64_t)a.items * a.kv_heads > sm_count()
+             ? launch<DP, kManyWaves, kStall>(a, q, k, v, stream)
+             : launch<DP, kOneWave, kStall>(a, q, k, v, stream);
 }
 
-}  // namespace
-}  // namespace kvp
-
-using namespace kvp;
-
-extern "C" int kv_attention_prompt(const void* query, int64_t query_stride, const void* key,
-                                   int64_t key_stride, const void* value, int64_t value_stride,
-                                   const int32_t* q_start_loc, const int32_t* k_start_loc,
-                                   int32_t num_reqs, int32_t num_q_tokens, int32_t num_k_tokens,
-                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                                   float scale, void* out, int32_t* d_err, kv_stream_t stream) {
+// kStall: the self-test, with `stall_*` as in PromptArgs.
+template <bool kStall>
+int prompt(const void* query, int64_t query_stride, const void* key, int64_t key_stride,
+           const void* value, int64_t value_stride, const int32_t* q_start_loc,
+           const int32_t* k_start_loc, int32_t num_reqs, int32_t num_q_tokens, int32_t num_k_tokens,
+           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale, void* out,
+           int32_t* d_err, int32_t stall_role, int32_t stall_item, int64_t stall_ns,
+           kv_stream_t stream) {
   if (num_reqs < 0 || num_q_tokens < 0 || num_k_tokens < 0 || num_q_heads <= 0 ||
       num_kv_heads <= 0 || head_dim <= 0 || num_q_heads % num_kv_heads != 0 ||
       !(scale > 0.f) || !(scale < INFINITY))
@@ -1054,7 +1085,39 @@ extern "C" int kv_attention_prompt(const void* query, int64_t query_stride, cons
   const bool by_head = num_reqs == 1 && num_k_tokens * k_row * 4 > (int64_t)kL2Share;
   PromptArgs a{q_start_loc, k_start_loc, num_reqs, num_q_tokens, num_k_tokens, num_q_heads,
                num_kv_heads, head_dim, group, tq, (int32_t)items, 1, by_head,
-               scale * 1.44269504088896340736f, static_cast<__nv_bfloat16*>(out), d_err};
+               scale * 1.44269504088896340736f, static_cast<__nv_bfloat16*>(out), d_err,
+               stall_role, stall_item, stall_ns};
+  if constexpr (kStall) return launch<128, true>(a, q_map, k_map, v_map, stream);
   return head_dim <= 64 ? launch<64>(a, q_map, k_map, v_map, stream)
                         : launch<128>(a, q_map, k_map, v_map, stream);
+}
+
+}  // namespace
+}  // namespace kvp
+
+using namespace kvp;
+
+extern "C" int kv_attention_prompt(const void* query, int64_t query_stride, const void* key,
+                                   int64_t key_stride, const void* value, int64_t value_stride,
+                                   const int32_t* q_start_loc, const int32_t* k_start_loc,
+                                   int32_t num_reqs, int32_t num_q_tokens, int32_t num_k_tokens,
+                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   float scale, void* out, int32_t* d_err, kv_stream_t stream) {
+  return prompt<false>(query, query_stride, key, key_stride, value, value_stride, q_start_loc,
+                       k_start_loc, num_reqs, num_q_tokens, num_k_tokens, num_q_heads, num_kv_heads,
+                       head_dim, scale, out, d_err, -1, 0, 0, stream);
+}
+
+extern "C" int kv_diag_attention_prompt_stall(
+    const void* query, int64_t query_stride, const void* key, int64_t key_stride, const void* value,
+    int64_t value_stride, const int32_t* q_start_loc, const int32_t* k_start_loc, int32_t num_reqs,
+    int32_t num_q_tokens, int32_t num_k_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, float scale, void* out, int32_t* d_err, int32_t role, int32_t item,
+    int64_t limit_ns, kv_stream_t stream) {
+  if (role < 0 || role > kSoftmax + 1 || item < 0 || limit_ns < 0 ||
+      limit_ns > (int64_t)kWaitLimitNs || d_err == nullptr)
+    return KV_EINVAL;
+  return prompt<true>(query, query_stride, key, key_stride, value, value_stride, q_start_loc,
+                      k_start_loc, num_reqs, num_q_tokens, num_k_tokens, num_q_heads, num_kv_heads,
+                      head_dim, scale, out, d_err, role, item, limit_ns, stream);
 }

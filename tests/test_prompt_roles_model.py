@@ -1,0 +1,383 @@
+"""The roles of a prompt attention CTA as a model on the CPU: loader, issuer, value check and two
+softmax groups, with their barriers, run under random schedules.  Checked: no barrier takes an
+arrival of another turn, no data is read before it is there or overwritten while it is read, every
+schedule ends, and nothing is in flight when the CTA ends, also where a role gave up on the way.
+
+A barrier is passed by the parity of its phase, as the hardware does it, so a role that fell two
+phases behind would be seen.  Copies complete in any order, matrix instructions in issue order."""
+import random
+
+import pytest
+
+KEYS_EDGE = 3
+
+
+class Bar:
+    def __init__(self, count=1):
+        self.count = self.pending = count
+        self.bytes = self.phase = 0
+
+    def _turn(self):
+        if self.pending == 0 and self.bytes == 0:
+            self.phase, self.pending = self.phase + 1, self.count
+
+    def arrive(self, expect=0):
+        assert self.pending > 0
+        self.pending, self.bytes = self.pending - 1, self.bytes + expect
+        self._turn()
+
+    def landed(self):
+        assert self.bytes > 0
+        self.bytes -= 1
+        self._turn()
+
+    def passed(self, parity):
+        return (self.phase & 1) != parity
+
+
+class Model:
+    """items: (tiles, tiles that every row sees whole, two tiles of queries?) of one CTA in turn."""
+
+    def __init__(self, rng, items, slots, stall=None, drain_late=True):
+        self.rng, self.items, self.slots, self.stall, self.drain_late = rng, items, slots, stall, drain_late
+        self.full, self.empty = [Bar() for _ in range(slots)], [Bar() for _ in range(slots)]
+        self.edge, self.v_ok = [Bar() for _ in range(2 * KEYS_EDGE)], [Bar() for _ in range(2 * KEYS_EDGE)]
+        self.q_full, self.q_free, self.scrubbed, self.ready = Bar(), Bar(), Bar(), Bar()
+        self.stolen, self.drain = Bar(), Bar()
+        self.s_full, self.o_full, self.written = [Bar(), Bar()], [Bar(), Bar()], [Bar(), Bar()]
+        self.p_full = [Bar() for _ in range(4)]
+        self.work_full, self.work_free = [Bar(), Bar()], [Bar(4), Bar(4)]
+        self.mail, self.q, self.bad = [0, None], None, None
+        self.ring, self.s, self.o = [None] * slots, [None, None], [None, None]
+        self.copies, self.queue, self.done = [], [], set()
+        self.abort, self.met = False, 0
+
+    # every wait gives up where another role has
+    def wait(self, bar, parity):
+        while not bar.passed(parity):
+            if self.abort and self.rng.random() < 0.5:
+                return False
+            yield
+        return True
+
+    def gives_up(self, role, item):
+        """The stalled role waits for nothing, for a while."""
+        if self.stall != (role, item):
+            return False
+        for _ in range(self.rng.choice([0, 3, 30, 300])):
+            if self.abort:
+                break
+            yield
+        self.abort = True
+        return True
+
+    def meet(self):
+        self.met += 1
+        while self.met < 5:
+            yield
+
+    def following(self, item):
+        self.work_free[item & 1].arrive()
+        yield
+        ok = yield from self.wait(self.work_full[(item + 1) & 1], (item >> 1) & 1)
+        return self.mail[(item + 1) & 1] if ok else None
+
+    def loader(self):
+        slot = turn = loaded = edge_at = asked = answers = 0
+        edge_used = 0
+
+        def drained():
+            if self.abort:
+                if loaded:
+                    yield from self.settle(self.q_full, (loaded - 1) & 1)
+                if asked:
+                    yield from self.settle(self.stolen, answers & 1)
+                for i in range(self.slots):
+                    uses = turn + (i < slot)
+                    if uses:
+                        yield from self.settle(self.full[i], (uses - 1) & 1)
+                for e in range(2 * KEYS_EDGE):
+                    if edge_used >> e & 1:
+                        yield from self.settle(self.edge[e], (edge_at >> e) & 1 ^ 1)
+
+        item, cur = 0, 0
+        while cur is not None:
+            if (yield from self.gives_up(0, item)):
+                break
+            n, whole, _ = self.items[cur]
+            ok = True
+            if n:
+                if loaded:
+                    ok = yield from self.wait(self.q_free, (loaded - 1) & 1)
+                if not ok:
+                    break
+                self.q = "loading"
+                self.q_full.arrive(1)
+
+                def q_landed(cur=cur):
+                    self.q = cur
+                    self.q_full.landed()
+                self.copies.append(q_landed)
+                loaded += 1
+                for u in range(2 * n):
+                    if turn:
+                        ok = yield from self.wait(self.empty[slot], (turn - 1) & 1)
+                        if not ok:
+                            break
+                    j = u >> 1
+                    e = (item & 1) * KEYS_EDGE + j - whole if u & 1 and j >= whole else -1
+                    bar = self.edge[e] if e >= 0 else self.full[slot]
+                    if e >= 0:
+                        self.full[slot].arrive()
+                    bar.arrive(1)
+                    self.ring[slot] = "loading"
+
+                    def tile_landed(slot=slot, what=(cur, u), bar=bar):
+                        assert self.ring[slot] == "loading"
+                        self.ring[slot] = what
+                        bar.landed()
+                    self.copies.append(tile_landed)
+                    if e >= 0:
+                        edge_at ^= 1 << e
+                        edge_used |= 1 << e
+                    slot, turn = (0, turn + 1) if slot + 1 == self.slots else (slot + 1, turn)
+                    yield
+                if not ok:
+                    break
+            self.stolen.arrive(1)
+            self.copies.append(self.stolen.landed)
+            asked = 1
+            ok = yield from self.wait(self.stolen, answers & 1)
+            if not ok:
+                break
+            asked, answers = 0, answers + 1
+            if item:
+                ok = yield from self.wait(self.work_free[(item - 1) & 1], ((item - 1) >> 1) & 1)
+                if not ok:
+                    break
+            cur = cur + 1 if cur + 1 < len(self.items) else None
+            self.mail[(item + 1) & 1] = cur
+            self.work_full[(item + 1) & 1].arrive()
+            item += 1
+            yield
+        if not self.drain_late:
+            yield from drained()
+        yield from self.meet()
+        if self.drain_late:
+            yield from drained()
+
+    def settle(self, bar, parity):
+        while not bar.passed(parity):
+            yield
+
+    def issuer(self):
+        sk = pk = loaded = p_at = v_ok_at = item = cur = 0
+
+        def step(slot, phase):
+            return (0, phase ^ 1) if slot + 1 == self.slots else (slot + 1, phase)
+
+        def scores(t, slot, cur, j):
+            def run():
+                assert self.abort or (self.q == cur and self.ring[slot] == (cur, 2 * j))
+                assert self.abort or self.s[t] in (None, "used")
+                self.s[t] = ("S", cur, j)
+            self.queue += [run, self.s_full[t].arrive]
+
+        def values(t, slot, cur, j, half):
+            def run():
+                if self.abort:
+                    return
+                assert self.ring[slot] == (cur, 2 * j + 1)
+                assert self.s[t][1:] == (cur, j) and self.s[t][0] in (("P0", "P1") if half == 0 else ("P1",))
+                if half == 0:
+                    assert self.o[t] is None if j == 0 else self.o[t] == (cur, j - 1)
+                else:
+                    self.o[t], self.s[t] = (cur, j), "used"
+            self.queue.append(run)
+
+        ok = True
+        while cur is not None:
+            if (yield from self.gives_up(1, item)):
+                break
+            n, whole, two = self.items[cur]
+            if n:
+                ok = (yield from self.wait(self.q_full, loaded & 1)) and (yield from self.wait(self.full[sk], pk))
+                if not ok:
+                    break
+                loaded += 1
+                tiles = (0, 1) if two else (0,)
+                for t in tiles:
+                    scores(t, sk, cur, 0)
+                self.queue.append(self.empty[sk].arrive)
+                if n == 1:
+                    self.queue.append(self.q_free.arrive)
+                sv, pv = step(sk, pk)
+                sk, pk = step(sv, pv)
+                for j in range(n):
+                    more = j + 1 < n
+                    if j < whole:
+                        ok = yield from self.wait(self.full[sv], pv)
+                    else:
+                        e = (item & 1) * KEYS_EDGE + j - whole
+                        ok = yield from self.wait(self.v_ok[e], (v_ok_at >> e) & 1)
+                        v_ok_at ^= 1 << e
+                    if ok and more:
+                        ok = yield from self.wait(self.full[sk], pk)
+                    for t in tiles:
+                        for half in (0, 1):
+                            ok = ok and (yield from self.wait(self.p_full[2 * t + half], (p_at >> t) & 1))
+                            if ok:
+                                values(t, sv, cur, j, half)
+                        if ok:
+                            if more:
+                                scores(t, sk, cur, j + 1)
+                            else:
+                                self.queue.append(self.o_full[t].arrive)
+                    if not ok:
+                        break
+                    self.queue.append(self.empty[sv].arrive)
+                    if more:
+                        self.queue.append(self.empty[sk].arrive)
+                        if j + 2 == n:
+                            self.queue.append(self.q_free.arrive)
+                    p_at ^= 3 if two else 1
+                    if more:
+                        sv, pv = step(*step(sv, pv))
+                        sk, pk = step(*step(sk, pk))
+                    yield
+                if not ok:
+                    break
+            cur = yield from self.following(item)
+            item += 1
+        self.queue.append(self.drain.arrive)
+        yield from self.settle(self.drain, 0)
+        yield from self.meet()
+
+    def checker(self):
+        slot = done = edge_at = written_at = item = cur = 0
+        both = False
+        while cur is not None:
+            if (yield from self.gives_up(2, item)):
+                break
+            n, whole, two = self.items[cur]
+            ok = True
+            if n:
+                if done:
+                    ok = yield from self.wait(self.written[0], written_at & 1)
+                    if ok and both:
+                        ok = yield from self.wait(self.written[1], written_at >> 1)
+                    if not ok:
+                        break
+                    written_at ^= 3 if both else 1
+                    self.bad = None
+                    self.ready.arrive()
+                    yield from self.settle(self.ready, (done - 1) & 1)
+                done, both = done + 1, two
+                for j in range(whole, n):
+                    e = (item & 1) * KEYS_EDGE + j - whole
+                    ok = yield from self.wait(self.edge[e], (edge_at >> e) & 1)
+                    edge_at ^= 1 << e
+                    if not ok:
+                        break
+                    at = (slot + 2 * j + 1) % self.slots
+                    assert self.ring[at] == (cur, 2 * j + 1) and self.bad in (None, cur)
+                    self.bad = cur
+                    yield
+                    assert self.ring[at] == (cur, 2 * j + 1)
+                    self.v_ok[e].arrive()
+                if not ok:
+                    break
+                self.scrubbed.arrive()
+                slot = (slot + 2 * n) % self.slots
+            cur = yield from self.following(item)
+            item += 1
+        yield from self.meet()
+
+    def softmax(self, t):
+        s_phase = o_phase = done = item = cur = 0
+        while cur is not None:
+            if (yield from self.gives_up(3 + t, item)):
+                break
+            n, whole, two = self.items[cur]
+            ok = True
+            if n and (t == 0 or two):
+                for j in range(n):
+                    ok = yield from self.wait(self.s_full[t], s_phase)
+                    if not ok:
+                        break
+                    s_phase ^= 1
+                    assert self.abort or self.s[t] == ("S", cur, j)
+                    yield
+                    for half in ("P0", "P1"):
+                        self.s[t] = (half, cur, j)
+                        self.p_full[2 * t + (half == "P1")].arrive()
+                        yield
+                ok = ok and (yield from self.wait(self.o_full[t], o_phase))
+                ok = ok and (yield from self.wait(self.scrubbed, done & 1))
+                if not ok:
+                    break
+                o_phase ^= 1
+                for _ in range(2):
+                    assert self.abort or self.o[t] == (cur, n - 1)
+                    assert self.abort or whole >= n or self.bad == cur
+                    yield
+                self.o[t] = None
+                self.done.add((cur, t))
+                self.written[t].arrive()
+            done += n > 0
+            cur = yield from self.following(item)
+            item += 1
+        yield from self.meet()
+
+    def run(self):
+        rng = self.rng
+        roles = [self.loader(), self.issuer(), self.checker(), self.softmax(0), self.softmax(1)]
+        pace = [rng.choice([1, 1, 3, 10]) for _ in roles] + [rng.choice([0.05, 1, 9, 30]) for _ in range(2)]
+        steps = 0
+        alive = list(range(5))
+        while alive:
+            k = rng.choices(alive + [5, 6], weights=[pace[i] for i in alive + [5, 6]])[0]
+            if k == 5:
+                if self.copies:
+                    self.copies.pop(rng.randrange(len(self.copies)))()
+            elif k == 6:
+                if self.queue:
+                    self.queue.pop(0)()
+            else:
+                try:
+                    next(roles[k])
+                except StopIteration:
+                    alive.remove(k)
+            steps += 1
+            assert steps < 400000, "a schedule that does not end"
+        if not self.abort:
+            for i, (n, _, two) in enumerate(self.items):
+                assert not n or ((i, 0) in self.done and (not two or (i, 1) in self.done))
+        return not self.copies and not self.queue
+
+
+def schedule(seed, stall, drain_late=True):
+    rng = random.Random(seed)
+    items = []
+    for _ in range(rng.randint(1, 7)):
+        n = rng.choice([0, 1, 1, 2, 3, 4, 6, 9])
+        items.append((n, max(0, n - rng.randint(0, KEYS_EDGE)), rng.random() < 0.6))
+    who = (rng.randrange(5), rng.randrange(len(items))) if stall else None
+    return Model(rng, items, rng.choice([5, 8]), who, drain_late).run()
+
+
+@pytest.mark.parametrize("part", range(4))
+def test_random_schedules(part):
+    for seed in range(100 * part, 100 * part + 100):
+        assert schedule(seed, False), f"in flight at the end: {seed}"
+
+
+@pytest.mark.parametrize("part", range(4))
+def test_a_role_that_gives_up(part):
+    for seed in range(100 * part, 100 * part + 100):
+        assert schedule(seed, True), f"in flight at the end: {seed}"
+
+
+def test_a_loader_that_drains_when_its_own_work_ends_is_caught():
+    """The mistake the model has to see: the last loads land after the CTA has ended."""
+    assert not all(schedule(seed, True, drain_late=False) for seed in range(200))

@@ -471,6 +471,9 @@ def kv_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_blocks: tor
     dev = _device_of(k_cache, "k_cache")
     if k_cache.dtype == torch.uint8:  # a block of a 4-bit cache is kv_heads whole records
         L, B, T, rec = _q4_dims(k_cache, v_cache, dev)
+        if rec % 288:  # 8 tokens of 64 channels, the least there is: 36 bytes each
+            raise ValueError("uint8 caches must be 4-bit caches (new_q4_cache): records of "
+                             "block_size * (head_dim/2 + head_dim/16) bytes")
         H, D = 1, rec // 2
     else:
         L, B, T, H, D = _cache_dims(k_cache, v_cache, dev)

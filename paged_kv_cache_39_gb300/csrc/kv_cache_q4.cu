@@ -39,8 +39,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Correctly rounded max / 7: a product and one step of its own remainder.  (The remainder of
-// a tiny value would leave the normal range: divided.)
+// max / 7 as the fp32 quotient: a product with the rounded reciprocal, then its remainder, exact in
+// an fma, once more times the reciprocal (Markstein's correction, IBM J. Res. Dev. 34, 1990).  The
+// remainder of a tiny value would leave the normal range: divided.
 __device__ __forceinline__ float over_seven(float x) {
   if (x < 1e-18f) return __fdiv_rn(x, 7.0f);
   const float c = 1.0f / 7.0f, q = x * c;

@@ -609,7 +609,7 @@ int kv_cache_gather_q4(const void* k_cache, const void* v_cache, int32_t layer,
  *   block_table    int32 [num_reqs, table_stride].
  *   span_start, span_end  int32 [num_reqs]: request r attends its positions
  *                  [start, end) (a sliding window starts late).
- *   out            bf16 [num_reqs, num_q_heads, head_dim], dense, apart from query.
+ *   out            bf16 [num_reqs, num_q_heads, head_dim], dense, apart from the inputs.
  *   workspace      device memory, 16-byte aligned, of at least
  *                  kv_attention_q4_workspace() bytes on the same device; it
  *                  holds no state between calls, and two calls that may run at
@@ -627,7 +627,7 @@ int kv_cache_gather_q4(const void* k_cache, const void* v_cache, int32_t layer,
  * Queries of 2^100 and more and value scales above 2^100 may give infinities or
  * NaN.  The same call gives the same bits every time.
  * Errors: as kv_attention_prompt and the 4-bit cache; KV_EINVAL for a workspace
- * that is missing, misaligned or too small; KV_EUNSUPPORTED for a layer of more
+ * that is missing, misaligned, too small or shared with out or an input; KV_EUNSUPPORTED for a layer of more
  * than 2^36 bytes in one cache.
  */
 int kv_attention_q4(const void* query, int64_t query_stride, const void* k_cache,

@@ -1061,7 +1061,9 @@ int prompt(const void* query, int64_t query_stride, const void* key, int64_t key
   const int64_t out_bytes = num_q_tokens * q_row * 2, n1 = num_k_tokens - 1;
   if (overlap(out, out_bytes, query, ((num_q_tokens - 1) * query_stride + q_row) * 2) ||
       (num_k_tokens > 0 && (overlap(out, out_bytes, key, (n1 * key_stride + k_row) * 2) ||
-                            overlap(out, out_bytes, value, (n1 * value_stride + k_row) * 2))))
+                            overlap(out, out_bytes, value, (n1 * value_stride + k_row) * 2))) ||
+      overlap(out, out_bytes, q_start_loc, (int64_t)(num_reqs + 1) * 4) ||
+      overlap(out, out_bytes, k_start_loc, (int64_t)(num_reqs + 1) * 4))
     return KV_EINVAL;
   const int group = num_q_heads / num_kv_heads, tq = kTile / group;
   CUtensorMap q_map, k_map, v_map;

@@ -964,20 +964,29 @@ extern "C" int kv_attention_q4(const void* query, int64_t query_stride, const vo
       !aligned(span_start, 4) || !aligned(span_end, 4))
     return KV_EINVAL;
   if (table_stride > 0 && (block_table == nullptr || !aligned(block_table, 4))) return KV_EINVAL;
-  const int64_t row = (int64_t)num_q_heads * head_dim;
-  if (overlap(out, num_reqs * row * 2, query, ((num_reqs - 1) * query_stride + row) * 2))
-    return KV_EINVAL;
-  const int64_t need = kv_attention_q4_workspace(num_reqs, num_q_heads, num_kv_heads, head_dim);
-  if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
-    return KV_EINVAL;
-  const int group = num_q_heads / num_kv_heads;
-  const int passes = (group + columns(group, head_dim) - 1) / columns(group, head_dim);
-  const int gang = gang_size(num_kv_heads * passes);
   const Q4Layout at{0, num_blocks, block_size, num_kv_heads, head_dim};
   // the kernel addresses a layer in 16-byte pieces of 32 bits
   const int64_t block_bytes = at.record_bytes() * num_kv_heads;
   if (num_blocks > ((int64_t)1 << 36) / block_bytes) return KV_EUNSUPPORTED;
-  const int64_t layer_at = layer * num_blocks * block_bytes;
+  const int64_t row = (int64_t)num_q_heads * head_dim;
+  const int64_t need = kv_attention_q4_workspace(num_reqs, num_q_heads, num_kv_heads, head_dim);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need))
+    return KV_EINVAL;
+  const int64_t spans = (int64_t)num_reqs * 4, cache = block_bytes * num_blocks;
+  const auto over_input = [&](const void* p, int64_t bytes) {
+    return overlap(p, bytes, query, ((num_reqs - 1) * query_stride + row) * 2) ||
+           overlap(p, bytes, block_table, spans * table_stride) || overlap(p, bytes, span_start, spans) ||
+           overlap(p, bytes, span_end, spans) ||
+           overlap(p, bytes, static_cast<const char*>(k_cache) + layer * cache, cache) ||
+           overlap(p, bytes, static_cast<const char*>(v_cache) + layer * cache, cache);
+  };
+  if (over_input(out, num_reqs * row * 2) || over_input(workspace, need) ||
+      overlap(out, num_reqs * row * 2, workspace, need))
+    return KV_EINVAL;
+  const int group = num_q_heads / num_kv_heads;
+  const int passes = (group + columns(group, head_dim) - 1) / columns(group, head_dim);
+  const int gang = gang_size(num_kv_heads * passes);
+  const int64_t layer_at = layer * cache;
   AttnArgs a{static_cast<const __nv_bfloat16*>(query), query_stride,
              static_cast<const uint8_t*>(k_cache) + layer_at,
              static_cast<const uint8_t*>(v_cache) + layer_at, at,

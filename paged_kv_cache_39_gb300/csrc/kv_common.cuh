@@ -299,10 +299,11 @@ inline bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
-// Whether the byte ranges [p, p + n) and [q, q + m) share a byte (a null range never does).
+// Whether the byte ranges [p, p + n) and [q, q + m) share a byte (a null or empty range never does).
 inline bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p != nullptr && q != nullptr && a < b + (uintptr_t)m && b < a + (uintptr_t)n;
+  return p != nullptr && q != nullptr && n > 0 && m > 0 && a < b + (uintptr_t)m &&
+         b < a + (uintptr_t)n;
 }
 
 inline int launch_status() {

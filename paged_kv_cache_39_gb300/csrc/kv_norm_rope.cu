@@ -309,6 +309,14 @@ extern "C" int kv_qk_norm_rope_write(
       overlap(q_out, qo, k_out, ko) ||
       (cached && (overlap(q_out, qo, value, v_bytes) || overlap(k_out, ko, value, v_bytes))))
     return KV_EINVAL;
+  const auto over_either = [&](const void* p, int64_t bytes) {
+    return overlap(q_out, qo, p, bytes) || overlap(k_out, ko, p, bytes);
+  };
+  if (over_either(q_weight, (int64_t)head_dim * 2) || over_either(k_weight, (int64_t)head_dim * 2) ||
+      over_either(positions, (int64_t)num_tokens * 8) ||
+      over_either(cos_sin, max_position * rotary_dim * 4) ||
+      (cached && over_either(slot_mapping, (int64_t)num_tokens * 8)))
+    return KV_EINVAL;
   NormRopeArgs a{static_cast<const __nv_bfloat16*>(query),
                  static_cast<const __nv_bfloat16*>(key),
                  static_cast<const __nv_bfloat16*>(value),

@@ -50,6 +50,7 @@
 // and its S, softmax and O follow one another with the barriers' times between them.
 #include <cuda_bf16.h>
 
+#include <cfloat>
 #include <mutex>
 #include <type_traits>
 
@@ -1087,7 +1088,7 @@ int prompt(const void* query, int64_t query_stride, const void* key, int64_t key
   const bool by_head = num_reqs == 1 && num_k_tokens * k_row * 4 > (int64_t)kL2Share;
   PromptArgs a{q_start_loc, k_start_loc, num_reqs, num_q_tokens, num_k_tokens, num_q_heads,
                num_kv_heads, head_dim, group, tq, (int32_t)items, 1, by_head,
-               scale * 1.44269504088896340736f, static_cast<__nv_bfloat16*>(out), d_err,
+               fminf(scale * 1.44269504088896340736f, FLT_MAX), static_cast<__nv_bfloat16*>(out), d_err,
                stall_role, stall_item, stall_ns};
   if constexpr (kStall) return launch<128, true>(a, q_map, k_map, v_map, stream);
   return head_dim <= 64 ? launch<64>(a, q_map, k_map, v_map, stream)

@@ -42,6 +42,7 @@
 // are xor-ed with the token, which makes every shared-memory read free of bank conflicts.
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "kv_q4.cuh"
@@ -511,7 +512,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) attention_q4_kernel(AttnArgs 
         // column 2 t + k is the query head of lanes 4 (2 t + k) ..
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          qc[n][k] = __shfl_sync(kFull, up, 4 * (2 * t + k)) * (a.scale_log2 * kCode);
+          // in the order that neither overflows nor loses bits early, and inside the normal range: a
+          // factor of zero or infinity would make NaN of hidden (infinite) or zero products
+          const float u = __shfl_sync(kFull, up, 4 * (2 * t + k)), c = a.scale_log2;
+          qc[n][k] = fminf(fmaxf(c > 1.f ? u * c * kCode : u * (c * kCode), FLT_MIN), FLT_MAX);
           ref[n][k] = kRefStart;
           sum[n][k] = 0.f;
         }
@@ -992,7 +996,8 @@ extern "C" int kv_attention_q4(const void* query, int64_t query_stride, const vo
              static_cast<const uint8_t*>(v_cache) + layer_at, at,
              (int32_t)(num_blocks < INT32_MAX ? num_blocks : INT32_MAX),
              BlockDiv::make(block_size), block_table, table_stride, span_start, span_end, num_reqs,
-             num_q_heads, group, passes, gang, worker_count() / gang, scale * 1.44269504088896340736f,
+             num_q_heads, group, passes, gang, worker_count() / gang,
+             fminf(scale * 1.44269504088896340736f, FLT_MAX),
              static_cast<__nv_bfloat16*>(out), static_cast<int64_t*>(workspace),
              reinterpret_cast<float*>(static_cast<char*>(workspace) + offsets_bytes(num_reqs)),
              d_err};

@@ -503,7 +503,10 @@ int kv_copy_blocks_bulk(void* k_cache, void* v_cache, int32_t num_layers, int64_
  * Errors: KV_EINVAL for null or misaligned pointers (16 bytes; positions and
  * slots 8), sizes out of range, a stride below the row, rotary_dim outside
  * (0, head_dim], an overlap as above; KV_EUNSUPPORTED for head_dim above 256,
- * head_dim or rotary_dim not a multiple of 8, a stride not a multiple of 8.
+ * head_dim or rotary_dim not a multiple of 8, a stride not a multiple of 8, more than
+ * 65535 query or KV heads, and more heads of all tokens together than a grid of
+ * 2^31 - 1 CTAs holds (a CTA takes 4 warps, a warp 16 heads of up to 64 channels, 8 of
+ * up to 128 or 4 of one token and kind).
  */
 int kv_qk_norm_rope_write(const void* query, int64_t query_stride, const void* key,
                           int64_t key_stride, const void* value, int64_t value_stride,
@@ -532,7 +535,7 @@ int kv_qk_norm_rope_write(const void* query, int64_t query_stride, const void* k
  *
  * With m query and n key rows, query i sees the keys j <= i + n - m:
  *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j.
- * A query that sees no key gets zeros.  Keys a query does not see contribute
+ * A query that sees no key gets zeros, as does one whose logits are all -infinity.  Keys a query does not see contribute
  * nothing to it, whatever they hold.  A NaN or an infinity in a value row makes
  * that channel NaN or infinite for the queries that see the row.  Query rows of
  * no request are left as they were.  A request whose rows are out of order or
@@ -547,7 +550,9 @@ int kv_qk_norm_rope_write(const void* query, int64_t query_stride, const void* k
  * not positive and finite, out overlapping an input; KV_EUNSUPPORTED for head_dim
  * above 128 or not a multiple of 8, a stride not a multiple of 8, more than 128
  * query heads per KV head, num_q_heads > 4096, num_reqs > KV_MAX_GATHER_REQS, more
- * than KV_MAX_TOKENS query or key rows.
+ * than KV_MAX_TOKENS query or key rows, and where the sequences' tile pairs (of 256 / group
+ * tokens, group being the query heads per KV head, rounded down) times num_kv_heads may be more
+ * than 2^31 - 1.
  */
 int kv_attention_prompt(const void* query, int64_t query_stride, const void* key,
                         int64_t key_stride, const void* value, int64_t value_stride,
@@ -577,7 +582,8 @@ int kv_attention_prompt(const void* query, int64_t query_stride, const void* key
  * Per group of 32 channels x: scale = bf16(max|x| / 7), code = round(x / scale)
  * + 8, nearest with ties to even.  A scale below 2^-126 makes the group zeros; a
  * group with a NaN or an infinity gets a NaN scale and reads as NaN.  Two tokens
- * with the same slot race: the row is then undefined.
+ * with the same slot race: the row is then undefined.  KV_EUNSUPPORTED also where
+ * num_tokens * num_kv_heads passes 16 * (2^31 - 1).
  */
 int kv_cache_write_q4(const void* key, int64_t key_stride, const void* value,
                       int64_t value_stride, void* k_cache, void* v_cache,
@@ -691,7 +697,7 @@ int kv_diag_attention_prompt_stall(const void* query, int64_t query_stride, cons
 /* Human-readable name of a kv_status value (static string). */
 const char* kv_status_string(int status);
 
-/* ABI version of this header (bumped on any signature change). */
+/* ABI version of this header (bumped on any signature change; a call that is added leaves it). */
 int kv_abi_version(void);
 
 #ifdef __cplusplus

@@ -44,3 +44,16 @@ def test_attention_prompt(scale, m, n):
         got = kv.kv_attention_prompt(q.to(BF16), k, v, i32([0, m]), i32([0, n]), scale=scale)
         for i in range(m):
             mean_check(got[i], v[:n - m + i + 1].expand(-1, 4, -1), f"scale {scale} row {i}")
+
+
+@pytest.mark.parametrize("m,n", [(5, 77), (5, 3000), (300, 300)])
+def test_prompt_rows_whose_logits_are_all_minus_infinity(m, n):
+    """They get zeros, as rows that see no key; a finite logit makes an ordinary row."""
+    q = torch.ones((m, 4, 64), dtype=BF16, device=dev())
+    k, v = normal((n, 1, 64), 1), normal((n, 1, 64), 2)
+    k[:, 0, 7] = -float("inf")
+    assert not kv.kv_attention_prompt(q, k, v, i32([0, m]), i32([0, n])).any()
+    at = n - m + 3
+    k[at, 0, 7] = 0
+    got = kv.kv_attention_prompt(q, k, v, i32([0, m]), i32([0, n]))
+    assert not got[:3].any() and torch.equal(got[3:], v[at].expand_as(got[3:]))

@@ -41,13 +41,15 @@
 //
 // Many pairs.  A CTA that runs takes over the pairs of CTAs that wait (see kv_tc.cuh), so that
 // the start of the next pair (search, loads, first scores) overlaps the end of this one: 64 prompts
-// of 128 tokens 74 -> 41 us, 256 of 64 207 -> 72.
+// of 128 tokens 74 -> 40 us, 256 of 64 207 -> 72.
 //
 // Measured (32 query heads, 8 KV heads of 128 channels): one prompt of 32768 tokens 5.3 to 5.4 ms
 // (1630 to 1660 TFLOP/s, near the card's power limit, 1.92 GHz), 16 chunks of 9 to 1855 tokens behind
-// up to 7685 367 us (1370 TFLOP/s), 77 tokens 7.6 us.  Per 128 keys a CTA's two tiles take 2900
+// up to 7685 366 us (1370 TFLOP/s), 77 tokens 7.7 us.  Per 128 keys a CTA's two tiles take 2900
 // cycles: 2048 of matrix instructions; a tile's softmax is 1140, beside the other tile's products,
-// and its S, softmax and O follow one another with the barriers' times between them.
+// and its S, softmax and O follow one another with the barriers' times between them.  The mixed
+// chunks' 32840 such steps are 311 us of it at 2.07 GHz (335 at 1.92), in this order on 152 SMs; the
+// rest is 4 to 8 us for each of a CTA's seven pairs: edge tiles, hand-over, output.
 #include <cuda_bf16.h>
 
 #include <cfloat>

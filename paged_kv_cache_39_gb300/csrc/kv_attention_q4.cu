@@ -16,8 +16,8 @@
 // at most 2^-32 of its own group's largest is lost then: groups and tokens of very different scales
 // do not cost each other bits.  f_j is taken off when a segment ends; sums are held in 32 bits.
 //
-// GPU shape.  The bytes of the cache bound this: 16 query rows at most read each of
-// them, far under a matrix unit tile of 128 rows, so the products go through the warp's
+// GPU shape.  The bytes of the cache bound this: a group's query rows, 4, 8 or 16 at a time, read
+// each of them, far under a matrix unit tile of 128 rows, so the products go through the warp's
 // own m16n8k16 instruction with tokens (of K) or channels (of V) as its 16 rows and the
 // group's query heads as its 8 columns.  The positions of all requests are cut into units of
 // 32, and the warps into gangs of one warp per KV head (at most 16): gang i takes the units
@@ -29,11 +29,11 @@
 // ahead, and nothing but the warp itself waits for them.  A warp whose range ends inside a
 // (request, head) leaves its sums in the workspace; a second kernel joins those.
 //
-// Measured (32 query heads, 8 KV heads of 128 channels): 8 contexts of 131072 tokens 222 us
-// (1.21 GB, 5.4 TB/s), 256 contexts of 512 to 4096 tokens 132 us (0.64 GB, 4.9 TB/s), one of 1009
-// 8.7 us, of which the second kernel is 2.5, one of 16384 13.6.  A unit of 32 tokens of one head is 4608 bytes and about
-// 600 instructions of a warp, half of them on the logic pipe (taking the codes apart); with 12
-// warps an SM issues 2.3 of 4 a cycle.  16 warps of 128 registers spill (253 us), 14 leave two
+// Measured (32 query heads, 8 KV heads of 128 channels): 8 contexts of 131072 tokens 229 us
+// (1.21 GB, 5.3 TB/s), 256 contexts of 512 to 4096 tokens 136 us (0.64 GB, 4.7 TB/s), one of 1009
+// 9.1 us, of which the second kernel is 2.5, one of 16384 13.9.  A unit of 32 tokens of one head is
+// 4608 bytes and about 650 instructions of a warp, half of them on the logic pipe (taking the codes
+// apart); with 12 warps an SM issues 2.35 of 4 a cycle.  The groups' powers of two are 2 % of it.  16 warps of 128 registers spill (253 us), 14 leave two
 // of the four schedulers one warp short (312 us).
 //
 // Layout of a unit in shared memory.  Row rho of the K product's 16 is token pi(rho) =
@@ -887,8 +887,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kJoinRows : 32 * W) join_q4_kern
 
 // Query heads a warp takes at once: 4, 8, or 16 (the cache is read once for all of them).  16 heads
 // of 128 channels do not fit in its registers: two passes of 8 instead, whose second reads come from
-// the L2 (64 contexts of 4096 tokens, 4 KV heads: 70 us against 88 with 16 and spills; of 64
-// channels, 36 with 16).
+// the L2 (64 contexts of 4096 tokens, 4 KV heads: 72 us against 88 with 16 and spills; of 64
+// channels, 38 with 16).
 int columns(int group, int head_dim) {
   return group > 8 && head_dim == 64 ? 16 : group > 4 ? 8 : 4;
 }

@@ -19,7 +19,7 @@
 // (query, key or value) of ONE token: position, slot and angles are read once for all of them
 // and every head's load is issued before the first is used.  fp32 in pairs (one instruction for
 // two).  Measured (32 query and 8 KV heads of 128 channels): 8432 tokens 40 us (229 MB, 5.7 TB/s),
-// 256 tokens 4.4 us.  9 CTAs an SM (56 registers; a few spilled
+// 256 tokens 4.0 us a call.  9 CTAs an SM (56 registers; a few spilled
 // words in some forms): with 8 (none) 42.8 us, with 10 (up to 23 words) 40.9; 2, 3 or 8 steps
 // instead of 4: 47.8, 47.8, 50.0.
 #include <cuda_bf16.h>

@@ -629,7 +629,8 @@ int kv_cache_gather_q4(const void* k_cache, const void* v_cache, int32_t layer,
  * zeros.
  * Products and sums are held in 32 bits; a weight times a value scale is rounded to
  * fp16 for its product with the codes: by 2^-11 of it at most, or, where it lies more
- * than 2^21 below the largest of its query and channel group, by 2^-32 of that one.
+ * than 2^21 below the largest of its query and channel group, by 2^-32 of that one
+ * (or by 2^-133, where those are near the end of the 32-bit range).
  * Queries of 2^100 and more and value scales above 2^100 may give infinities or
  * NaN.  The same call gives the same bits every time.
  * Errors: as kv_attention_prompt and the 4-bit cache; KV_EINVAL for a workspace

@@ -92,7 +92,7 @@ struct PromptArgs {
   int32_t stall_role, stall_item;
   int64_t stall_ns;
 };
-enum Role { kLoader, kIssuer, kChecker, kSoftmax };  // kSoftmax + tile
+enum Role { kLoader, kIssuer, kValueCheck, kSoftmax };  // kSoftmax + tile
 
 // One step of a transposition over lanes: with the lane `mask` away, a for its b (the lower of the
 // two lanes keeps its a, the higher its b).
@@ -630,7 +630,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__
       bool both = false;  // the item before had two tiles
       Work w = read(0);
       for (int item = 0; w.m > 0; ++item) {
-        if (stalled(kChecker, item)) break;
+        if (stalled(kValueCheck, item)) break;
         const Item x(w, a, split, rank_in);
         if (x.end > x.first) {
           bool ok = true;

@@ -13,7 +13,7 @@
 // above its largest logit when last raised, and for each of its channel groups a power of two f_j:
 // the product's operand is w b f_j, the largest one of a group is 2^7 at least, and reference and f
 // are set anew when a weight or an operand passes 2^15.  An operand below 2^-14 keeps fewer bits,
-// at most 2^-32 of its own group's largest is lost then: groups and tokens of very different scales
+// at most 2^-32 of its own group's largest (or 2^-137 outright) is lost then: groups and tokens of very different scales
 // do not cost each other bits.  f_j is taken off when a segment ends; sums are held in 32 bits.
 //
 // GPU shape.  The bytes of the cache bound this: a group's query rows, 4, 8 or 16 at a time, read

@@ -253,7 +253,7 @@ class Model:
         yield from self.settle(self.drain, 0)
         yield from self.meet()
 
-    def checker(self):
+    def value_check(self):
         slot = done = edge_at = written_at = item = cur = 0
         both = False
         while cur is not None:
@@ -331,7 +331,7 @@ class Model:
 
     def run(self):
         rng = self.rng
-        roles = [self.loader(), self.issuer(), self.checker(), self.softmax(0), self.softmax(1)]
+        roles = [self.loader(), self.issuer(), self.value_check(), self.softmax(0), self.softmax(1)]
         pace = [rng.choice([1, 1, 3, 10]) for _ in roles] + [rng.choice([0.05, 1, 9, 30]) for _ in range(2)]
         steps = 0
         alive = list(range(5))

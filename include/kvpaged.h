@@ -1,8 +1,9 @@
 /*
  * kvpaged.h -- C ABI of the GB300 paged KV-cache hot path (libkvpaged.so).
  *
- * Eighteen calls, each one kernel launch on the caller's stream (the attention
- * over the 4-bit cache adds a second one that joins the parts of its split):
+ * Twenty-two calls, each one kernel launch on the caller's stream (the attentions
+ * over the 4-bit cache and of drafted trees add a second one that joins the parts of
+ * their split):
  *   kv_slot_mapping_paged    token -> cache slot through a block table
  *   kv_slot_mapping_paged_cp the same, for one rank of context parallelism
  *   kv_slot_mapping_range    token -> cache slot through contiguous ranges
@@ -21,6 +22,10 @@
  *   kv_cache_write_q4        quantise new K/V rows into the 4-bit paged caches
  *   kv_cache_gather_q4       gather spans of the 4-bit caches as bf16 rows
  *   kv_attention_q4          one query token per request over the 4-bit caches
+ *   kv_tree_layout           masks and positions of drafted trees from their parents
+ *   kv_attention_tree        a step's rows (drafted trees, or one token) over the caches
+ *   kv_verify_drafts         drafted tokens kept or refused, and one more token
+ *   kv_cache_keep_path       the kept rows' K/V to consecutive positions, every layer
  *
  * Sources (page title, section):
  *   [BT]  "Blocktabelle" (vLLM v0.25.1 walkthrough)
@@ -87,8 +92,11 @@ enum kv_error_bits {
     KV_ERR_NULL_WRITE = 16,   /* write slot inside the null block 0 */
     KV_ERR_BAD_QSL = 32,      /* query_start_loc decreasing, negative, or past num_tokens */
     KV_ERR_OUT_OF_SPACE = 64, /* gather rows exceed out_rows, or ranges exceed a table row */
-    KV_ERR_TIMEOUT = 128      /* an asynchronous bulk copy did not complete within the bounded
+    KV_ERR_TIMEOUT = 128,     /* an asynchronous bulk copy did not complete within the bounded
                                  wait (see "Bounded waits" below) */
+    KV_ERR_BAD_TREE = 256,    /* a row's parent is no row before it, or a path does not go up */
+    KV_ERR_BAD_TOKEN = 512,   /* drafted token outside [0, vocab) */
+    KV_ERR_BAD_PROBS = 1024   /* no token has a probability above 0 */
 };
 
 /*
@@ -112,6 +120,7 @@ enum kv_error_bits {
 #define KV_NULL_BLOCK_ID 0
 #define KV_MAX_RANGES_PER_REQ 256   /* [RNG] The Fork Implementation: capped at 256 ranges */
 #define KV_MAX_GATHER_REQS 4096     /* requests per kv_cache_gather(_range) call */
+#define KV_MAX_TREE_ROWS 64         /* rows of a request's step: its last token and the drafted ones */
 /* Largest max_num_tokens of one slot-mapping call (paged, range,
  * context-parallel, fused with the write): 2^31 - 65536, so that token indices
  * of a whole last tile stay in int32.  Larger values: KV_EINVAL. */
@@ -649,6 +658,156 @@ int kv_attention_q4(const void* query, int64_t query_stride, const void* k_cache
  * KV_EINVAL for sizes out of range. */
 int64_t kv_attention_q4_workspace(int32_t num_reqs, int32_t num_q_heads, int32_t num_kv_heads,
                                   int32_t head_dim);
+
+/*
+ * Drafted trees.  A step of a request has m rows (1 .. KV_MAX_TREE_ROWS): row 0 is its last
+ * token, whose K and V are not cached yet, every other row a drafted token that follows its
+ * parent, a row before it.  Rows of all requests are packed: request r owns rows
+ * [q_start_loc[r], q_start_loc[r+1]) of num_rows.  With n = context_len[r] tokens cached, row
+ * i's K and V go to cache position n + i, whatever its place in the tree; its rotation is by
+ * position n + depth.  A step: kv_tree_layout; in every layer kv_qk_norm_rope_write (slots
+ * by kv_slot_mapping_paged of the cache positions) and kv_attention_tree; kv_verify_drafts;
+ * kv_cache_keep_path.  A request whose rows are out of order, out of range or too many
+ * sets KV_ERR_BAD_QSL and is skipped: its rows of the outputs are left as they were, as
+ * are rows of no request (rows that two requests claim, with such a one between them, hold
+ * either's).  All four calls: at most KV_MAX_GATHER_REQS requests and
+ * KV_MAX_TREE_ROWS * KV_MAX_GATHER_REQS rows (else KV_EUNSUPPORTED).
+ *
+ * kv_tree_layout -- what each row sees and where it stands.
+ *
+ *   parents          int32 [num_rows]: the index, in its request, of each row's parent
+ *                    (row 0's is not read); NULL: chains, the parent is the row before.
+ *   q_start_loc      int32 [num_reqs + 1]; context_len int32 [num_reqs].
+ *   tree_mask        int64 [num_rows]: bit j of row i: row j is row i or above it.
+ *   positions        int64 [num_rows]: context_len + depth (0 for row 0).
+ *   cache_positions  int64 [num_rows]: context_len + i.
+ *
+ * A row whose parent is not a row before it sets KV_ERR_BAD_TREE and stands like row 0: it
+ * sees itself, at depth 0.  A negative context_len sets KV_ERR_BAD_POSITION; both positions
+ * of its rows are -1.
+ * Errors: KV_EINVAL for negative counts, null or misaligned pointers (tree_mask and
+ * positions 8 bytes, others 4), an output that shares bytes with an input or another output.
+ */
+int kv_tree_layout(const int32_t* parents, const int32_t* q_start_loc, const int32_t* context_len,
+                   int32_t num_reqs, int32_t num_rows, int64_t* tree_mask, int64_t* positions,
+                   int64_t* cache_positions, int32_t* d_err, kv_stream_t stream);
+
+/*
+ * kv_attention_tree -- attention of a step's rows over the bf16 paged caches; with one row
+ * a request, a decode step.
+ *
+ *   query          bf16 [num_rows, num_q_heads, head_dim], rows query_stride elements
+ *                  apart; query head h reads KV head h / (num_q_heads / num_kv_heads).
+ *   k_cache, v_cache, layer, ..  as kv_cache_write; `layer` is read.
+ *   block_table    int32 [num_reqs, table_stride].
+ *   q_start_loc    int32 [num_reqs + 1].
+ *   span_start     int32 [num_reqs]: first visible position of the context (a sliding
+ *                  window starts late); NULL: 0.
+ *   context_len    int32 [num_reqs].
+ *   tree_mask      int64 [num_rows]: row i sees row j of its request (position
+ *                  context_len + j) where bit j is set, itself included; bits at and past
+ *                  the request's rows mean nothing.  NULL: row i sees the rows j <= i.
+ *   max_rows       1 .. KV_MAX_TREE_ROWS: no request has more rows (KV_ERR_BAD_QSL).
+ *   out            bf16 [num_rows, num_q_heads, head_dim], dense, apart from the inputs.
+ *   workspace      as kv_attention_q4, of kv_attention_tree_workspace() bytes.
+ *
+ *   out_i = sum_p softmax_p(scale * q_i . k_p) v_p
+ * over the positions [span_start, context_len) and the rows row i sees, as far as their table
+ * entry is a block of the pool.  Of the positions [span_start, context_len + rows), null entries
+ * are left out, entries outside [0, num_blocks) are left out with KV_ERR_BAD_BLOCK, positions past
+ * the table row with KV_ERR_BAD_POSITION.  A row with no position left, or whose logits are all -infinity, gets
+ * zeros; so do the rows of a request with span_start < 0 or context_len < span_start
+ * (KV_ERR_BAD_POSITION).  Positions a row does not see contribute nothing to it, whatever they hold.
+ * A NaN or an infinity in a value row makes that channel NaN or infinite for the rows that
+ * see it.  Products and sums are held in 32 bits; the weights are rounded to bf16 for
+ * their product with V.  The same call gives the same bits every time.
+ * Errors: KV_EINVAL for null or misaligned pointers, sizes out of range, a stride below the
+ * row, num_q_heads not a multiple of num_kv_heads, a scale that is not positive and finite, a
+ * workspace that is missing, misaligned or too small, out or workspace sharing bytes with
+ * each other or an input; KV_EUNSUPPORTED for head_dim above 128 or not a multiple of 8, a
+ * stride not a multiple of 8, more than 64 query heads per KV head, num_q_heads > 4096.
+ */
+int kv_attention_tree(const void* query, int64_t query_stride, const void* k_cache,
+                      const void* v_cache, int32_t layer, int32_t num_layers, int64_t num_blocks,
+                      int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                      int32_t head_dim, const int32_t* block_table, int32_t table_stride,
+                      const int32_t* q_start_loc, const int32_t* span_start,
+                      const int32_t* context_len, const int64_t* tree_mask, int32_t num_reqs,
+                      int32_t num_rows, int32_t max_rows, float scale, void* out, void* workspace,
+                      int64_t workspace_bytes, int32_t* d_err, kv_stream_t stream);
+
+/* Workspace bytes of a kv_attention_tree call on the current device (0 for none), or
+ * KV_EINVAL / KV_EUNSUPPORTED for sizes out of range. */
+int64_t kv_attention_tree_workspace(int32_t num_reqs, int32_t max_rows, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * kv_verify_drafts -- which drafted tokens are kept, and the token behind them.
+ *
+ *   target_probs  [num_rows, vocab], rows target_stride elements apart: the target's
+ *                 probabilities of the token that follows each row.
+ *   draft_probs   the same, rows draft_stride apart: the probabilities each row's children
+ *                 were drawn from, independently; rows without children are not read.  NULL:
+ *                 the drafted tokens were not drawn (the likeliest ones, a lookup).
+ *   prob_type     KV_F32 or KV_BF16, of both.
+ *   tokens        int32 [num_rows]: each row's token (row 0's is not read).
+ *   parents       as kv_tree_layout.
+ *   uniform       fp32 [num_rows], in [0, 1): row i's number decides on its token, row 0's draws
+ *                 the last token.
+ *   out_tokens    int32 [num_rows]: the kept tokens, then the last one, then -1.
+ *   path          int32 [num_rows]: the kept rows from row 0 on, then -1.
+ *   num_kept      int32 [num_reqs]: kept drafted tokens; num_kept + 1 entries of the other
+ *                 two are not -1 (0 for a request that is skipped or has no rows).
+ *
+ * At row i (from row 0 on), with p and q its rows of the two, s_0 = p and Z_0 = 1, its
+ * children are tried in order: child c with token x and number u is kept when
+ *   u q(x) Z_j < s_j(x),   else   s_(j+1) = max(s_j - Z_j q, 0),  Z_(j+1) = sum s_(j+1).
+ * Without draft_probs q is 1 at x and 0 elsewhere, and Z_(j+1) = Z_j - s_j(x).  A kept child is the next
+ * row.  With no child left, the last token is the smallest t with sum_(k <= t) s(k) > u_0 sum_k
+ * s(k); where s is 0 everywhere, s = p.  So the tokens are distributed as the target's.
+ * Sums are held in integers of 2^-46 and 64 bits, whose order does not matter; a weight is
+ * rounded to a multiple of 2^-46.  The same call gives the same bits every time.  (Rows that sum to
+ * 2^17 and more are no probabilities: the last token is then any, or -1.)
+ * Probabilities below 0 and NaN count as 0, above 1 as 1; numbers below 0 and NaN count as 0, of 1 and
+ * above as the largest below 1.  A token outside [0, vocab) is passed over with
+ * KV_ERR_BAD_TOKEN; so is a row whose parent is not a row before it (KV_ERR_BAD_TREE) and
+ * those below it.  Where p is 0 everywhere the last token is -1 (KV_ERR_BAD_PROBS).
+ * Errors: KV_EINVAL for negative counts, vocab < 1, a prob_type that is neither, a stride below
+ * vocab, null pointers or pointers not aligned to their elements, an output that shares bytes with
+ * an input or another output; KV_EUNSUPPORTED for vocab > 2^20.
+ */
+enum kv_prob_type { KV_F32 = 0, KV_BF16 = 1 };
+int kv_verify_drafts(const void* target_probs, int64_t target_stride, const void* draft_probs,
+                     int64_t draft_stride, int32_t prob_type, int32_t vocab, const int32_t* tokens,
+                     const int32_t* parents, const int32_t* q_start_loc, const float* uniform,
+                     int32_t num_reqs, int32_t num_rows, int32_t* out_tokens, int32_t* path,
+                     int32_t* num_kept, int32_t* d_err, kv_stream_t stream);
+
+/*
+ * kv_cache_keep_path -- the kept rows' K and V to consecutive positions, in every layer of
+ * the bf16 caches, in place: of request r, for i = 1 .. num_kept[r], the rows of cache
+ * position context_len + path[i] go to position context_len + i.
+ *
+ *   k_cache, v_cache, ..  as kv_cache_write.
+ *   block_table, context_len, q_start_loc  as kv_attention_tree.
+ *   path, num_kept        as kv_verify_drafts: path goes up from 0.
+ *
+ * The rows behind the last kept one stay as they were, for the next step to overwrite.  Blocks that
+ * requests share must not hold a moved position.  A request is left as it was where num_kept
+ * is negative or not below its rows, or path does not start at 0 and go up inside them
+ * (KV_ERR_BAD_TREE), context_len is negative or a position past the table row
+ * (KV_ERR_BAD_POSITION), or a moved row's block, old or new, is the null block
+ * (KV_ERR_NULL_WRITE) or outside the pool (KV_ERR_BAD_BLOCK).
+ * Errors: KV_EINVAL for sizes out of range, null or misaligned pointers (caches 16 bytes), caches that
+ * share bytes with each other or with another argument; KV_EUNSUPPORTED for a row
+ * (num_kv_heads * head_dim) that is no multiple of 8.
+ */
+int kv_cache_keep_path(void* k_cache, void* v_cache, int32_t num_layers, int64_t num_blocks,
+                       int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                       const int32_t* block_table, int32_t table_stride,
+                       const int32_t* q_start_loc, const int32_t* context_len, const int32_t* path,
+                       const int32_t* num_kept, int32_t num_reqs, int32_t num_rows, int32_t* d_err,
+                       kv_stream_t stream);
 
 /*
  * kv_diag_bounded_wait -- self-test of the bounded wait the bulk-copy gather

@@ -23,11 +23,16 @@ ERR_BITS = {
     "BAD_QSL": 32,
     "OUT_OF_SPACE": 64,
     "TIMEOUT": 128,
+    "BAD_TREE": 256,
+    "BAD_TOKEN": 512,
+    "BAD_PROBS": 1024,
 }
 PAD_SLOT_ID = -1
 NULL_BLOCK_ID = 0
 MAX_RANGES_PER_REQ = 256
 MAX_GATHER_REQS = 4096
+MAX_TREE_ROWS = 64
+PROB_TYPES = ("float32", "bfloat16")  # kv_prob_type, by value
 MAX_TOKENS = 2147418112  # largest max_num_tokens of one slot-mapping call (2^31 - 65536)
 
 # Every entry point the header declares, with its argument and result types.
@@ -71,6 +76,14 @@ SIGNATURES = {
     "kv_attention_q4_workspace": ([_I32, _I32, _I32, _I32], ctypes.c_int64),
     "kv_attention_q4": ([_P, _I64, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _P, _I32, _P,
                          _P, _I32, _F32, _P, _P, _I64, _P, _P], ctypes.c_int),
+    "kv_tree_layout": ([_P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P], ctypes.c_int),
+    "kv_attention_tree_workspace": ([_I32, _I32, _I32, _I32, _I32], ctypes.c_int64),
+    "kv_attention_tree": ([_P, _I64, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _P, _I32, _P,
+                           _P, _P, _P, _I32, _I32, _I32, _F32, _P, _P, _I64, _P, _P], ctypes.c_int),
+    "kv_verify_drafts": ([_P, _I64, _P, _I64, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _P, _P, _P, _P,
+                          _P], ctypes.c_int),
+    "kv_cache_keep_path": ([_P, _P, _I32, _I64, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _I32,
+                            _I32, _P, _P], ctypes.c_int),
     "kv_diag_bounded_wait": ([_I32, _P, _P], ctypes.c_int),
     "kv_diag_attention_prompt_stall": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _I32, _I32,
                                         _I32, _I32, _I32, _F32, _P, _P, _I32, _I32, _I64, _P],

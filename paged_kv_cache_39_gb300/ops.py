@@ -22,7 +22,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import KV_OK, check, load
+from ._lib import KV_OK, PROB_TYPES, check, load
 
 try:  # the current stream's handle, without a Stream object around it (about 1 us less)
     from torch._C import _cuda_getCurrentRawStream as _raw_stream
@@ -52,6 +52,10 @@ __all__ = [
     "kv_cache_write_q4",
     "kv_cache_gather_q4",
     "kv_attention_q4",
+    "kv_tree_layout",
+    "kv_attention_tree",
+    "kv_verify_drafts",
+    "kv_cache_keep_path",
     "new_error_word",
     "new_q4_cache",
 ]
@@ -723,3 +727,174 @@ def kv_attention_q4(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     return _run("kv_attention_q4", args, dev,
                 (query, k_cache, v_cache, block_table, span_start, span_end, out, workspace, err),
                 out, prepare)
+
+
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device: int) -> None:
+    _need(t, name, dtype, device)
+    if t.numel() < n:
+        raise ValueError(f"{name} needs {n} elements, got {t.numel()}")
+
+
+def _result(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int,
+            like: torch.Tensor, device: int) -> torch.Tensor:
+    if t is None:
+        return torch.empty(n, dtype=dtype, device=like.device)
+    _vector(t, name, dtype, n, device)
+    return t
+
+
+def kv_tree_layout(parents: Optional[torch.Tensor], q_start_loc: torch.Tensor,
+                   context_len: torch.Tensor, num_rows: Optional[int] = None,
+                   tree_mask: Optional[torch.Tensor] = None,
+                   positions: Optional[torch.Tensor] = None,
+                   cache_positions: Optional[torch.Tensor] = None,
+                   err: Optional[torch.Tensor] = None, prepare: bool = False):
+    """What each row of a step sees and where it stands (see "Drafted trees" in the header).
+
+    parents int32 [N] (None: chains, then give ``num_rows``), q_start_loc int32 [R + 1],
+    context_len int32 [R].  Returns (tree_mask, positions, cache_positions), int64 [N]: bit j of
+    a row's mask: row j of its request is the row or above it; context + depth, for the rotation;
+    context + index, for the slot mapping.  Rows of no request are left as they were
+    (undefined in outputs made here)."""
+    dev = _device_of(q_start_loc, "q_start_loc")
+    _need(q_start_loc, "q_start_loc", torch.int32, dev)
+    R = max(q_start_loc.numel() - 1, 0)
+    _vector(context_len, "context_len", torch.int32, R, dev)
+    if parents is None and num_rows is None:
+        raise ValueError("give num_rows (or parents)")
+    n = parents.numel() if num_rows is None else int(num_rows)
+    if parents is not None:
+        _vector(parents, "parents", torch.int32, n, dev)
+    out = tuple(_result(t, name, torch.int64, n, q_start_loc, dev) for t, name in
+                ((tree_mask, "tree_mask"), (positions, "positions"),
+                 (cache_positions, "cache_positions")))
+    args = (_ptr(parents), _ptr(q_start_loc), _ptr(context_len), R, n, *map(_ptr, out),
+            _err_ptr(err, dev))
+    return _run("kv_tree_layout", args, dev, (parents, q_start_loc, context_len, *out, err), out,
+                prepare)
+
+
+def kv_attention_tree(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      block_table: torch.Tensor, q_start_loc: torch.Tensor,
+                      context_len: torch.Tensor, max_rows: int,
+                      tree_mask: Optional[torch.Tensor] = None,
+                      span_start: Optional[torch.Tensor] = None, layer: int = 0,
+                      scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      err: Optional[torch.Tensor] = None, prepare: bool = False):
+    """Attention of a step's rows (drafted trees; with one row a request, a decode step) over
+    the bf16 paged caches.
+
+    query [N, q_heads, D] bf16, any row stride; request r owns rows [q_start_loc[r],
+    q_start_loc[r+1]), at most ``max_rows`` <= 64 of them, and attends positions
+    [span_start_r, context_len_r) of its cache (``span_start`` None: all of them) and, at
+    context_len_r + j, the rows j whose bits are set in the row's ``tree_mask`` (int64 [N];
+    None: the row itself and those before it).  The rows' own K and V are in the caches
+    already.  ``scale`` defaults to D ** -0.5.  The workspace is allocated here, as in
+    kv_attention_q4: give each stream (or graph) that runs beside another its own prepared call.
+    Returns out [N, q_heads, D]; a row that sees nothing gets zeros."""
+    dev = _device_of(query, "query")
+    N, Hq, D, qs = _rows_of(query, "query", dev)
+    L, B, T, H, Dc = _cache_dims(k_cache, v_cache, dev)
+    if Dc != D:
+        raise ValueError("query and the caches differ in head_dim")
+    _need(block_table, "block_table", torch.int32, dev)
+    _need(q_start_loc, "q_start_loc", torch.int32, dev)
+    R = max(q_start_loc.numel() - 1, 0)
+    if block_table.dim() != 2 or block_table.shape[0] < R:
+        raise ValueError("block_table must be [num_reqs, table_stride]")
+    _vector(context_len, "context_len", torch.int32, R, dev)
+    if span_start is not None:
+        _vector(span_start, "span_start", torch.int32, R, dev)
+    if tree_mask is not None:
+        _vector(tree_mask, "tree_mask", torch.int64, N, dev)
+    out = _output(out, "out", (N, Hq, D), query, dev)
+    with torch.cuda.device(dev):
+        need = load().kv_attention_tree_workspace(R, int(max_rows), Hq, H, D)
+    workspace = torch.empty(max(int(need), 0), dtype=torch.uint8, device=query.device)
+    args = (_ptr(query), qs, _ptr(k_cache), _ptr(v_cache), int(layer), L, B, T, Hq, H, D,
+            _ptr(block_table), block_table.shape[1], _ptr(q_start_loc), _ptr(span_start),
+            _ptr(context_len), _ptr(tree_mask), R, N, int(max_rows),
+            D ** -0.5 if scale is None else float(scale), _ptr(out), _ptr(workspace),
+            workspace.numel(), _err_ptr(err, dev))
+    return _run("kv_attention_tree", args, dev,
+                (query, k_cache, v_cache, block_table, q_start_loc, span_start, context_len,
+                 tree_mask, out, workspace, err), out, prepare)
+
+
+def _probs_of(t: torch.Tensor, name: str, device: int) -> Tuple[int, int, int]:
+    """(rows, vocab, elements between rows) of probabilities with dense rows."""
+    _cuda_check(t, name)
+    if str(t.dtype)[6:] not in PROB_TYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must live on cuda:{device}, got {t.device}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, vocab] with contiguous rows")
+    n, v = (int(x) for x in t.shape)
+    return n, v, (int(t.stride(0)) if n > 1 else v)
+
+
+def kv_verify_drafts(target_probs: torch.Tensor, tokens: torch.Tensor, q_start_loc: torch.Tensor,
+                     uniform: torch.Tensor, draft_probs: Optional[torch.Tensor] = None,
+                     parents: Optional[torch.Tensor] = None,
+                     out_tokens: Optional[torch.Tensor] = None,
+                     path: Optional[torch.Tensor] = None,
+                     num_kept: Optional[torch.Tensor] = None,
+                     err: Optional[torch.Tensor] = None, prepare: bool = False):
+    """Which drafted tokens of a step are kept, and the token behind them, so that the tokens
+    are distributed as the target's (the rule is in the header).
+
+    target_probs [N, vocab] fp32 or bf16, any row stride: the target's probabilities behind
+    each row; draft_probs, the same type: those the row's children were drawn from, independently
+    (None: they were not drawn, but chosen).  tokens int32 [N], parents int32 [N] (None: chains),
+    uniform fp32 [N] in [0, 1).  Returns (out_tokens [N], path [N], num_kept [R]), int32: the kept
+    tokens and the last one, then -1; the kept rows from row 0 on, then -1."""
+    dev = _device_of(target_probs, "target_probs")
+    N, V, ts = _probs_of(target_probs, "target_probs", dev)
+    ds = V
+    if draft_probs is not None:
+        Nd, Vd, ds = _probs_of(draft_probs, "draft_probs", dev)
+        if (Nd, Vd) != (N, V) or draft_probs.dtype != target_probs.dtype:
+            raise ValueError("target_probs and draft_probs differ in shape or type")
+    _need(q_start_loc, "q_start_loc", torch.int32, dev)
+    R = max(q_start_loc.numel() - 1, 0)
+    _vector(tokens, "tokens", torch.int32, N, dev)
+    _vector(uniform, "uniform", torch.float32, N, dev)
+    if parents is not None:
+        _vector(parents, "parents", torch.int32, N, dev)
+    out = (_result(out_tokens, "out_tokens", torch.int32, N, tokens, dev),
+           _result(path, "path", torch.int32, N, tokens, dev),
+           _result(num_kept, "num_kept", torch.int32, R, tokens, dev))
+    args = (_ptr(target_probs), ts, _ptr(draft_probs), ds,
+            PROB_TYPES.index(str(target_probs.dtype)[6:]), V, _ptr(tokens), _ptr(parents),
+            _ptr(q_start_loc), _ptr(uniform), R, N, *map(_ptr, out), _err_ptr(err, dev))
+    return _run("kv_verify_drafts", args, dev,
+                (target_probs, draft_probs, tokens, parents, q_start_loc, uniform, *out, err), out,
+                prepare)
+
+
+def kv_cache_keep_path(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                       q_start_loc: torch.Tensor, context_len: torch.Tensor, path: torch.Tensor,
+                       num_kept: torch.Tensor, err: Optional[torch.Tensor] = None,
+                       prepare: bool = False):
+    """The kept rows' K and V to consecutive positions behind the context, in every layer, in
+    place: position context_len_r + path[i] to context_len_r + i for i = 1 .. num_kept_r.
+
+    path int32 [N] and num_kept int32 [R] as kv_verify_drafts gives them.  Returns None (or the
+    ``Prepared`` call)."""
+    dev = _device_of(k_cache, "k_cache")
+    L, B, T, H, D = _cache_dims(k_cache, v_cache, dev)
+    _need(block_table, "block_table", torch.int32, dev)
+    _need(q_start_loc, "q_start_loc", torch.int32, dev)
+    _need(path, "path", torch.int32, dev)
+    R = max(q_start_loc.numel() - 1, 0)
+    if block_table.dim() != 2 or block_table.shape[0] < R:
+        raise ValueError("block_table must be [num_reqs, table_stride]")
+    _vector(context_len, "context_len", torch.int32, R, dev)
+    _vector(num_kept, "num_kept", torch.int32, R, dev)
+    args = (_ptr(k_cache), _ptr(v_cache), L, B, T, H, D, _ptr(block_table), block_table.shape[1],
+            _ptr(q_start_loc), _ptr(context_len), _ptr(path), _ptr(num_kept), R, path.numel(),
+            _err_ptr(err, dev))
+    return _run("kv_cache_keep_path", args, dev,
+                (k_cache, v_cache, block_table, q_start_loc, context_len, path, num_kept, err),
+                None, prepare)

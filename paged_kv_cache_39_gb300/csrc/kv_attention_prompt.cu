@@ -94,20 +94,6 @@ struct PromptArgs {
 };
 enum Role { kLoader, kIssuer, kValueCheck, kSoftmax };  // kSoftmax + tile
 
-// One step of a transposition over lanes: with the lane `mask` away, a for its b (the lower of the
-// two lanes keeps its a, the higher its b).
-__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b, bool high, int mask) {
-  const uint32_t got = __shfl_xor_sync(kFull, high ? a : b, mask);
-  a = high ? got : a;
-  b = high ? b : got;
-}
-__device__ __forceinline__ void exchange(uint4& a, uint4& b, bool high, int mask) {
-  exchange(a.x, b.x, high, mask);
-  exchange(a.y, b.y, high, mask);
-  exchange(a.z, b.z, high, mask);
-  exchange(a.w, b.w, high, mask);
-}
-
 template <int DP>
 struct Smem {
   static constexpr int kTileBytes = kTile * DP * 2;
@@ -158,17 +144,6 @@ struct Item : Work {
     two = t0 + a.tq < m;
   }
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // Behind a role's last wait, read and issue: all roles of the CTA have come so far.
 __device__ __forceinline__ void roles_met() {

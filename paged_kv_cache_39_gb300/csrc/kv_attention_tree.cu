@@ -1,21 +1,56 @@
 // kv_attention_tree.cu -- attention of a step's rows (drafted trees, or one token) over the
-// bf16 paged caches.
+// bf16 paged caches, on the matrix unit.
 //
 // Mathematics.  Row i of request r sees the positions [start, context) and context + j for the
 // bits j of its mask, as far as the block table maps them to a block of the pool:
-//   o_i = sum_p w_p v_p / sum_p w_p,  w_p = 2^(c q_i . k_p - ref),  c = scale * log2(e),
-// in one pass with a running maximum ref.
+//   o_i = sum_p w_ip v_p / sum_p w_ip,  w_ip = 2^(c q_i . k_p - ref_i),  c = scale * log2(e),
+// in one pass with a running reference, raised (and the sums rescaled) only when a logit passes it by
+// more than 8.  Logits, weights, sums and outputs are held in 32 bits; a weight is rounded
+// to bf16 for its product with V (the matrix unit takes both operands in one type), at most
+// 2^-8 of it; the sum takes it before that.
+//
+// GPU shape.  All query heads of a group and all rows of a request read the same keys, so
+// its rows are packed (row = token * group + head) into tiles of 128, one (kRows = 1) or two at a time.
+// With up to 128 rows the cache's bytes bound this: 128 keys of a head of 128 channels are
+// 64 KB, 2850 cycles of an SM's share of the memory, and 1024 of the matrix unit however few of
+// the tile's rows there are.  Positions are cut into units of 128, and CTAs (one per SM) into gangs
+// of one CTA per KV head or so: gang i takes the units [i C, (i+1) C) whatever requests
+// they belong to, so every CTA reads the same number of keys however long the contexts are, and
+// the heads of a block, which lie side by side in memory, are read at about the same time.  A CTA
+// whose range ends inside a (request, head) leaves its sums in the workspace, and a second
+// kernel joins those.
+//
+// Roles by warp:
+//   softmax   one row per thread; also the rescale and the output of its tile
+//   issuer    the matrix instructions: S = Q K^T, then O += P V with P in tensor memory
+//   4 copiers look up blocks and copy K and V rows (cp.async: any block size, and rows that are
+//             no position of the request are filled with zeros) into a ring of 128-row tiles
+//             in the 128-byte swizzle; they also find the next unit and describe it
+// Tensor memory: S twice and O twice.  One tile: units take turns with S, so the next scores are
+// computed during this softmax, and segments with O.  Two tiles: one S and O each.
+//
+// Hidden keys.  A hidden logit is replaced, so a NaN there is gone, but 0 * NaN in P V is NaN.
+// Hidden from all rows: filled with zeros, never read.  Hidden from some rows are only the step's
+// own rows: their values are checked when they arrive; what is not finite is set to 0 in
+// shared memory and its row noted, and the output of a row that sees it looks the value up again.
 #include <cuda_bf16.h>
 
 #include <cfloat>
 
+#include "kv_tc.cuh"
 #include "kv_tree.cuh"
 
 namespace kvp {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 128;             // keys of a unit, rows of a tile
+constexpr int kCopiers = 4;            // warps
+constexpr int kNotes = 8;              // units described ahead (a power of two: 2^3)
+constexpr int kBadRing = 16;           // segments whose values are noted
+constexpr float kLazy = 8.0f;          // log2 of the most a weight may pass the reference
+constexpr float kRefStart = -1e30f;    // of a row with no finite logit yet
+constexpr int kSmemMax = 232448 - 64;  // of a CTA, less static
+constexpr int kJoinThreads = 128;
 
 struct TreeArgs {
   const __nv_bfloat16* q;
@@ -35,88 +70,908 @@ struct TreeArgs {
   float scale_log2;
   __nv_bfloat16* out;
   int32_t* err;
+  int32_t passes;    // groups of kRows tiles of a request's rows
+  int32_t gang;      // CTAs that take the same positions of neighbouring (KV head, pass)
+  int32_t gangs;
+  int32_t part_rows; // rows of a part in the workspace
+  int32_t q_rows;    // rows of a tile's Q in shared memory (a multiple of 8)
+  int32_t q_bufs;    // Q of this segment and the next, where there is room
+  int32_t slots;     // of the ring
+  int32_t warps;     // softmax warps of a tile that can have rows
+  int4* joins;       // [CTAs]: the segment a CTA began and did not end: request, segment, last gang
+  float* parts;      // [CTAs][2][part_rows][DP], then (reference, sum) [CTAs][2][part_rows]
 };
 
-// A CTA per (row of a request, query head); a warp takes every fourth key, a lane 4 channels.
-__global__ void __launch_bounds__(kThreads) attention_tree_kernel(TreeArgs a) {
-  __shared__ float s_o[kWarps][128], s_l[kWarps], s_ref[kWarps];
+// A request's rows and the positions they may see; no unit: nothing to attend.
+struct Req {
+  int32_t first, count;   // rows
+  uint32_t lo, hi, ctx;   // positions [lo, hi); the step's rows begin at ctx
+  int32_t units;
+};
+__device__ __forceinline__ Req request(const TreeArgs& a, int r, uint32_t& err) {
+  const StepRows rows = step_rows(a.q_start, r, a.num_rows, a.max_rows);
+  const int32_t s0 = a.span_start != nullptr ? a.span_start[r] : 0, c = a.context_len[r];
+  Req q = {rows.first, rows.count, 0, 0, 0, 0};
+  if (rows.count < 0) err |= KV_ERR_BAD_QSL;
+  if (rows.count <= 0) return q;
+  if (s0 < 0 || c < s0) {
+    err |= KV_ERR_BAD_POSITION;
+    return q;
+  }
+  const int64_t reach = (int64_t)a.stride * a.div.size, end = (int64_t)c + rows.count;
+  if (end > reach) err |= KV_ERR_BAD_POSITION;
+  q.ctx = (uint32_t)c;
+  q.lo = (uint32_t)s0;
+  q.hi = (uint32_t)(end < reach ? end : reach);
+  q.units = q.hi > q.lo ? (int32_t)((q.hi - q.lo + kTile - 1) / kTile) : 0;
+  return q;
+}
+
+// What the copiers tell the others about a unit.
+struct __align__(16) Note {
+  uint32_t valid[4];       // keys that some row may see, a warp of copiers a word
+  int32_t r, seg;
+  int32_t step;            // the step's row 0 is key `step` of the unit
+  int32_t flags;
+  int32_t first, count;    // the request's rows
+  uint32_t ctx;
+  int32_t pad;
+};
+enum Flags { kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8 };  // of this CTA's share; of the segment
+
+constexpr int kNumBars = 2 * 12 + 2 * kNotes + 2 + 4 + 2 + 2 + 2 + 1;
+template <int DP>
+struct Smem {
+  static constexpr int kSlot = kTile * DP * 2;
+  static constexpr int kBars = 0;
+  static constexpr int kNote = (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kBad = kNote + kNotes * (int)sizeof(Note);
+  static constexpr int kMisc = kBad + kBadRing * 8;
+  static constexpr int kScan = kMisc + 16;                              // int64_t[17]: units by warp, all
+  static constexpr int kHead = (kScan + 17 * 8 + 1023) / 1024 * 1024;   // Q, then the ring
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+  const int n = real ? 16 : 0;  // 0: zeros, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Threads: kRows tiles of 4 softmax warps, the issuer and 3 others, 4 copiers.
+template <int kRows>
+constexpr int kThreadsOf = 128 * kRows + 256;
+
+template <int DP, int kRows>
+__global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(const __grid_constant__ TreeArgs a) {
+  using L = Smem<DP>;
+  constexpr int kThreads = kThreadsOf<kRows>;
+  constexpr int kIssuer = 4 * kRows, kCopy = kIssuer + 4;
+  // registers of the warpgroups: 384 threads x 168 at launch >= 128 x (224 + 104 + 168), 512 x 128 >= 128 x
+  // (184 + 184 + 56 + 80)
+  constexpr int kSoftmaxRegs = kRows == 1 ? 224 : 184, kIssueRegs = kRows == 1 ? 104 : 56, kCopyRegs = 80;
+  constexpr int kLag = DP == 128 ? 3 : 7;   // groups of copies in flight beside the newest
+  constexpr int kPieces = DP / 8;           // 16-byte pieces of a row
+  extern __shared__ __align__(1024) unsigned char smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* full = bars;
+  uint64_t* empty = full + 12;
+  uint64_t* note_full = empty + 12;
+  uint64_t* note_free = note_full + kNotes;
+  uint64_t* s_full = note_free + kNotes;    // one tile: by unit & 1; two: by tile
+  uint64_t* p_full = s_full + 2;            // the same, by half of the keys
+  uint64_t* o_full = p_full + 4;            // one tile: [0], every unit; two: by tile, at a segment's end
+  uint64_t* o_free = o_full + 2;            // one tile: by segment & 1; two: by tile
+  uint64_t* q_free = o_free + 2;            // by segment % q_bufs
+  uint64_t* drain = q_free + 2;
+  Note* notes = reinterpret_cast<Note*>(smem + L::kNote);
+  volatile uint64_t* bad = reinterpret_cast<uint64_t*>(smem + L::kBad);
+  int* misc = reinterpret_cast<int*>(smem + L::kMisc);
+  uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(misc);
+  volatile int* abort = misc + 1;
+  const int q_tile = a.q_rows * DP * 2;     // bytes of a tile's Q
+  const int q_odd = a.q_bufs - 1;           // 1: segments take turns with Q
+  unsigned char* const q_smem = smem + L::kHead;
+  unsigned char* const ring = q_smem + (a.q_bufs * kRows * q_tile + 1023) / 1024 * 1024;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform for the compiler, too
+
+  if (tid < kNumBars) {
+    const uint64_t* b = &bars[tid];
+    int count = 1;
+    if (b < empty) count = kCopiers;
+    if (b >= note_full && b < note_free) count = kCopiers;
+    if (b >= note_free && b < s_full) count = kRows * a.warps + 1;
+    if (b >= p_full && b < o_full) count = a.warps;
+    if (b >= o_free && b < q_free) count = a.warps;
+    mbar_init(&bars[tid], count);
+    mbar_fence_init();
+  }
+  if (tid < kBadRing) bad[tid] = 0;
+  if (tid == 0) *abort = 0;
   pdl_allow_next();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.y / a.max_rows, i = blockIdx.y - r * a.max_rows, qh = blockIdx.x;
-  const StepRows rows = step_rows(a.q_start, r, a.num_rows, a.max_rows);
-  uint32_t err = rows.count < 0 ? KV_ERR_BAD_QSL : 0;
-  if (i >= rows.count) {
-    if (i == 0 && qh == 0 && threadIdx.x == 0) report(a.err, err);
-    return;
+  if (warp == kIssuer) tmem_alloc(tmem_ptr, 512);
+
+  // ---- where the requests' units begin (by thread, in the ring's place)
+  const int segs = a.kv_heads * a.passes, rounds = segs / a.gang;
+  const int per = (a.num_reqs + kThreads - 1) / kThreads;
+  int64_t* s_before = reinterpret_cast<int64_t*>(ring);   // [kThreads] units before each thread's requests
+  int64_t* s_warp = reinterpret_cast<int64_t*>(smem + L::kScan);
+  {
+    const int r_lo = min(a.num_reqs, tid * per), r_hi = min(a.num_reqs, r_lo + per);
+    uint32_t err = 0;
+    int64_t mine = 0;
+    for (int r = r_lo; r < r_hi; ++r) mine += (int64_t)request(a, r, err).units * rounds;
+    if (blockIdx.x == 0) report(a.err, err);
+    const int64_t incl = warp_inclusive_scan<int64_t>(mine);
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    s_before[tid] = before;
+    if (tid == kThreads - 1) s_warp[kThreads / 32] = before + mine;
   }
-  const int64_t start = a.span_start != nullptr ? a.span_start[r] : 0, ctx = a.context_len[r];
-  const int64_t reach = (int64_t)a.stride * a.div.size;
-  int64_t end = ctx + rows.count, lo = start;
-  if (start < 0 || ctx < start) {
-    err |= KV_ERR_BAD_POSITION;
-    end = lo = 0;
-  }
-  if (end > reach && end > lo) {
-    err |= KV_ERR_BAD_POSITION;
-    end = reach;
-  }
-  const int64_t row = (int64_t)rows.first + i;
-  const uint64_t mask = a.tree_mask != nullptr ? (uint64_t)a.tree_mask[row] : ~0ull >> (63 - i);
-  const int h = qh / a.group, D = a.head_dim;
-  const bool mine = 4 * lane < D;
-  float q[4] = {};
-  auto load4 = [&](const __nv_bfloat16* p, float (&x)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * lane);
-    x[0] = __uint_as_float(v.x << 16);
-    x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16);
-    x[3] = __uint_as_float(v.y & 0xffff0000u);
-  };
-  if (mine) load4(a.q + row * a.q_stride + (int64_t)qh * D, q);
-  float o[4] = {}, l = 0.f, ref = -INFINITY;
-  for (int64_t p = lo + warp; p < end; p += kWarps) {
-    int64_t lb, off;
-    a.div.divmod(p, lb, off);
-    const int32_t b = a.table[(int64_t)r * a.stride + lb];
-    if (b == kNull) continue;
-    if (b < 0 || b >= a.num_blocks) {
-      err |= KV_ERR_BAD_BLOCK;
-      continue;
-    }
-    if (p >= ctx && !((mask >> (p - ctx)) & 1)) continue;
-    const int64_t at = (((int64_t)b * a.div.size + off) * a.kv_heads + h) * D;
-    float k[4] = {}, v[4] = {};
-    if (mine) {
-      load4(a.k_cache + at, k);
-      load4(a.v_cache + at, v);
-    }
-    float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-    s *= a.scale_log2;
-    if (s == -INFINITY) continue;
-    const float up = fmaxf(ref, s), f = exp2f(ref - up), w = exp2f(s - up);
-    ref = up;
-    l = l * f + w;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = o[c] * f + w * v[c];
-  }
-  report(a.err, err);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) s_o[warp][4 * lane + c] = o[c];
-  if (lane == 0) s_l[warp] = l, s_ref[warp] = ref;
+  tc_fence_before();
   __syncthreads();
-  if ((int)threadIdx.x >= D) return;
-  float top = -INFINITY, sum = 0.f, y = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ref[w]);
-  if (top > -INFINITY)
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(s_ref[w] - top);
-      sum += f * s_l[w];
-      y += f * s_o[w][threadIdx.x];
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(kFull, *tmem_ptr, 0);
+  const int64_t total = s_warp[kThreads / 32];
+  const int64_t share = (total + a.gangs - 1) / a.gangs;
+  const int my_gang = blockIdx.x / a.gang, member = blockIdx.x - my_gang * a.gang;
+  const int64_t begin = my_gang * share;
+  const int64_t count = my_gang < a.gangs && begin < total ? min(share, total - begin) : 0;
+
+  auto all = [](bool ok) { return __all_sync(kFull, ok) != 0; };
+  auto wait = [&](uint64_t* b, uint32_t parity) { return all(mbar_wait_role(b, parity & 1, abort)); };
+  // a reader's next note; its lanes have all of it
+  auto read_note = [&](int64_t u, Note& n) {
+    if (!wait(&note_full[u & (kNotes - 1)], (uint32_t)(u >> 3))) return false;
+    n = notes[u & (kNotes - 1)];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&note_free[u & (kNotes - 1)]);
+    return true;
+  };
+
+  if (warp >= kCopy) {
+    // ---------------------------------------------------------------- copies
+    if (kRows == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+    const int w = warp - kCopy;
+    uint32_t err = 0;
+    if (w == 0 && lane == 0) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);  // until it is known better
+    // the first unit: the request whose units hold `begin`
+    int r = 0, seg = 0, tile = 0;
+    if (count > 0) {
+      int lo = 0, hi = kThreads;  // last thread whose requests begin at or before it
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_before[mid] <= begin) lo = mid; else hi = mid;
+      }
+      r = lo * per;
+      int64_t at = s_before[lo];
+      uint32_t ignore = 0;
+      int units = request(a, r, ignore).units;
+      while (at + (int64_t)units * rounds <= begin) {
+        at += (int64_t)units * rounds;
+        units = request(a, ++r, ignore).units;
+      }
+      const int64_t rest = begin - at;
+      seg = (int)(rest / units) * a.gang + member;
+      tile = (int)(rest % units);
     }
-  a.out[(row * a.q_heads + qh) * D + threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : y / sum);
+    asm volatile("bar.sync 2, 128;" ::: "memory");  // before the ring is written
+    // 32 requests at a time, one a lane
+    int base = r;
+    Req mine = {};
+    auto look = [&]() {
+      uint32_t ignore = 0;
+      mine = Req{0, 0, 0, 0, 0, 0};
+      if (base + lane < a.num_reqs) mine = request(a, base + lane, ignore);
+    };
+    Req now;
+    auto take = [&]() {
+      now.first = __shfl_sync(kFull, mine.first, r - base);
+      now.count = __shfl_sync(kFull, mine.count, r - base);
+      now.lo = __shfl_sync(kFull, mine.lo, r - base);
+      now.hi = __shfl_sync(kFull, mine.hi, r - base);
+      now.ctx = __shfl_sync(kFull, mine.ctx, r - base);
+      now.units = __shfl_sync(kFull, mine.units, r - base);
+    };
+    // this lane's row of the unit: its place in the cache in rows of all heads; < 0: none
+    auto place = [&]() {
+      const uint32_t p = now.lo + (uint32_t)tile * kTile + w * 32 + lane;
+      if (p >= now.hi) return (int64_t)-1;
+      int64_t lb, off;
+      a.div.divmod((int64_t)p, lb, off);
+      const int32_t b = a.table[(int64_t)r * a.stride + lb];
+      if (b == kNull) return (int64_t)-1;
+      if (b < 0 || b >= a.num_blocks) {
+        err |= KV_ERR_BAD_BLOCK;
+        return (int64_t)-1;
+      }
+      return (int64_t)b * a.div.size + off;
+    };
+    int64_t at = -1;
+    if (count > 0) {
+      look();
+      take();
+      at = place();
+    }
+    const int sub = lane / kPieces, piece = lane % kPieces;
+    constexpr int kPer = 32 / kPieces;      // rows of a copy instruction
+    const bool piece_real = piece * 8 < a.head_dim;
+    // rows w * 32 + i * kPer + sub: their 8-row groups are 1024 bytes, column blocks of 64 channels apart
+    const uint32_t dst_lane = (uint32_t)((w * 32 + sub) * 128 + (piece >> 3) * (kTile * 128));
+    const uint32_t col_lane = (uint32_t)(((piece & 7) ^ sub) << 4);
+    const uint32_t ring_at = smem_addr(ring);
+
+    int64_t group = 0;        // groups of copies issued: 2 a unit
+    int slot = 0;
+    uint32_t turn = 0;
+    int done_slot = 0;        // the next slot to be told about
+    int64_t done = 0;
+    int64_t segment = -1;     // of this CTA, counted
+    int hist_step[5] = {kTile, kTile, kTile, kTile, kTile};  // of the last units: where the step's rows begin
+    int hist_seg[5] = {};
+    bool ok = true;
+    // Values of the step's rows that are not finite: 0, and their rows noted.
+    auto check_values = [&](int step, int seg_no, int s) {
+      const int y = w * 32 + lane;
+      if (y < step) return;
+      unsigned char* row = ring + s * L::kSlot + y * 128;
+      bool any = false;
+#pragma unroll 4
+      for (int c = 0; c < kPieces; ++c) {
+        uint4* p = reinterpret_cast<uint4*>(row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (y & 7)) << 4));
+        uint4 v = *p;
+        uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+        bool hit = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
+          if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0xffffu, hit = true;
+        }
+        if (hit) *p = v;
+        any |= hit;
+      }
+      if (any)
+        atomicOr(reinterpret_cast<unsigned long long*>(smem + L::kBad) + seg_no, 1ull << (y - step));
+    };
+    // Group `done` has arrived: the issuer may use it.  `back`: units since its own.
+    auto tell = [&](int back) {
+      if (done & 1) {
+        int step = kTile, seg_no = 0;
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+          if (i == back) step = hist_step[i], seg_no = hist_seg[i];
+        if (step < kTile) {
+          __syncwarp();
+          check_values(step, seg_no, done_slot);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[done_slot]);
+      ++done;
+      if (++done_slot == a.slots) done_slot = 0;
+    };
+    auto advance_slot = [&]() {
+      copy_commit();
+      ++group;
+      if (++slot == a.slots) {
+        slot = 0;
+        ++turn;
+      }
+    };
+    // The issuer needs what is in flight to get to the end of a wait of this role: the oldest groups
+    // are told about until it is over.
+    auto wait_telling = [&](uint64_t* b, uint32_t parity) {
+      while (done < group && !__any_sync(kFull, mbar_try_wait(b, parity & 1))) {
+        switch ((int)(group - done)) {
+          case 1: copy_wait<0>(); break;
+          case 2: copy_wait<1>(); break;
+          case 3: copy_wait<2>(); break;
+          case 4: copy_wait<3>(); break;
+          case 5: copy_wait<4>(); break;
+          case 6: copy_wait<5>(); break;
+          default: copy_wait<6>(); break;
+        }
+        tell((int)((group - 1) / 2 - done / 2));
+      }
+      return wait(b, parity);
+    };
+    bool first_run = true;
+    for (int64_t u = 0; ok && u < count; ++u) {
+      // this unit, then the next one's place (its table entries arrive meanwhile)
+      const int64_t here = at;
+      const Req req = now;
+      const int here_r = r, here_seg = seg, here_tile = tile;
+      const bool first = first_run || tile == 0;
+      first_run = false;
+      const bool to_end = tile + 1 == now.units, last = to_end || u + 1 == count;
+      if (u + 1 < count) {
+        if (++tile == now.units) {
+          tile = 0;
+          seg += a.gang;
+          if (seg >= segs) {
+            seg = member;
+            do {
+              if (++r >= base + 32) {
+                base = r;
+                look();
+              }
+            } while (__shfl_sync(kFull, mine.units, r - base) == 0);
+            take();
+          }
+        }
+        at = place();
+      }
+      if (first) {
+        ++segment;
+        if (w == 0 && lane == 0) bad[(segment + 7) & (kBadRing - 1)] = 0;  // all have read that one, none written
+      }
+      const int64_t tile_at = (int64_t)req.lo + (int64_t)here_tile * kTile;
+      const int step = (int)max((int64_t)-kTile, min((int64_t)kTile, (int64_t)req.ctx - tile_at));
+#pragma unroll
+      for (int i = 4; i > 0; --i) hist_step[i] = hist_step[i - 1], hist_seg[i] = hist_seg[i - 1];
+      hist_step[0] = step;
+      hist_seg[0] = (int)(segment & (kBadRing - 1));
+      // describe it
+      if (u >= kNotes) ok = wait(&note_free[u & (kNotes - 1)], (uint32_t)(u >> 3) - 1);
+      if (!ok) break;
+      const uint32_t valid = __ballot_sync(kFull, here >= 0);
+      if (lane == 0) {
+        Note* n = &notes[u & (kNotes - 1)];
+        n->valid[w] = valid;
+        if (w == 0) {
+          n->r = here_r;
+          n->seg = here_seg;
+          n->step = step;
+          n->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (to_end ? kToEnd : 0);
+          n->first = req.first;
+          n->count = req.count;
+          n->ctx = req.ctx;
+          // a segment that begins here and ends with another CTA: how far the join reaches
+          if (first && here_tile == 0) n->flags |= kFromStart;
+          const int64_t from = begin + u - here_tile;  // the segment's first unit
+          if (u + 1 == count && !to_end && from >= begin)
+            a.joins[blockIdx.x] = make_int4(here_r, here_seg, (int)((from + req.units - 1) / share), req.count);
+        }
+        mbar_arrive(&note_full[u & (kNotes - 1)]);
+      }
+      const int head = here_seg / a.passes;
+      // Q with the segment's first K
+      if (turn > 0) ok = wait(&empty[slot], turn - 1);
+      if (ok && first && segment >= a.q_bufs)
+        ok = wait_telling(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1);
+      if (!ok) break;
+      if (first) {
+        const int pass = here_seg - head * a.passes;
+        for (int t = 0; t < kRows; ++t) {
+          const int row0 = (pass * kRows + t) * kTile, left = req.count * a.group - row0;  // rows of this tile
+          const uint32_t q_at = smem_addr(q_smem) + ((int)(segment & q_odd) * kRows + t) * q_tile;
+          for (int y = w * kPer + sub; y < min(left, kTile); y += kCopiers * kPer) {
+            const int tok = (row0 + y) / a.group, g = row0 + y - tok * a.group;
+            const __nv_bfloat16* src = a.q + (int64_t)(req.first + tok) * a.q_stride +
+                                       (int64_t)(head * a.group + g) * a.head_dim + piece * 8;
+            copy16(q_at + (piece >> 3) * (a.q_rows * 128) + y * 128 + (((piece & 7) ^ (y & 7)) << 4),
+                   piece_real ? src : a.q, piece_real);
+          }
+        }
+      }
+      const int64_t off = (here * a.kv_heads + head) * a.head_dim;   // of this lane's row
+      auto rows = [&](const __nv_bfloat16* cache) {
+        const uint32_t to = ring_at + slot * L::kSlot + dst_lane;
+#pragma unroll
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const int64_t o = __shfl_sync(kFull, here >= 0 ? off : (int64_t)-1, i * kPer + sub);
+          const bool real = o >= 0 && piece_real;
+          copy16(to + i * kPer * 128 + (col_lane ^ (((i * kPer) & 7) << 4)),
+                 cache + (real ? o + piece * 8 : 0), real);
+        }
+      };
+      rows(a.k_cache);
+      advance_slot();
+      if (group - done > kLag) {
+        copy_wait<kLag>();
+        tell((int)((group - 1) / 2 - done / 2));
+      }
+      if (turn > 0) ok = wait(&empty[slot], turn - 1);
+      if (!ok) break;
+      rows(a.v_cache);
+      advance_slot();
+      if (group - done > kLag) {
+        copy_wait<kLag>();
+        tell((int)((group - 1) / 2 - done / 2));
+      }
+    }
+    copy_wait<0>();
+    while (ok && done < group) tell((int)((group - 1) / 2 - done / 2));
+    report(a.err, err);
+  } else if (warp >= kIssuer) {
+    // ---------------------------------------------------------------- matrix instructions
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));  // the whole warpgroup
+    if (warp == kIssuer) {
+      constexpr uint32_t s_desc = mma_desc(128, kTile, false), o_desc = mma_desc(128, DP, true);
+      const uint32_t ring_at = smem_addr(ring), q_base = smem_addr(q_smem);
+      const bool leader = elect_one();
+      const uint32_t q_cols = (uint32_t)(a.q_rows * 128) >> 4;  // from a 64-channel block of Q to the next
+      auto scores = [&](uint32_t d, uint32_t q_at, int slot) {
+        const uint64_t qd = smem_desc(q_at, 16), kd = smem_desc(ring_at + slot * L::kSlot, 16);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k)
+            mma_ss(d, qd + (k / 4) * q_cols + (k % 4) * 2, kd + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
+                   s_desc, k > 0);
+        }
+      };
+      auto values = [&](uint32_t d, uint32_t p, int slot, bool add, int half) {
+        const uint64_t vd = smem_desc(ring_at + slot * L::kSlot, kTile * 128) + half * ((kTile / 2 * 128) >> 4);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_ts(d, p + half * (kTile / 4) + k * 8, vd + k * (2048 >> 4), o_desc, add || k > 0);
+        }
+      };
+      auto commit = [&](uint64_t* b) {
+        if (leader) mma_commit(b);
+      };
+      bool ok = true;
+      int slot = 0;
+      uint32_t turn = 0;
+      auto step = [&]() {
+        if (++slot == a.slots) {
+          slot = 0;
+          ++turn;
+        }
+      };
+      int64_t segment = -1;
+      if constexpr (kRows == 1) {
+        // unit u's scores, then unit u - 1's products with V
+        int v_slot = 0;
+        uint32_t v_turn = 0;
+        int64_t v_segment = 0;
+        bool v_first = false;
+        auto products = [&](int64_t u) {
+          const uint32_t d = tmem + 2 * kTile + (uint32_t)(v_segment & 1) * DP, p = tmem + (uint32_t)(u & 1) * kTile;
+          if (v_first && v_segment >= 2 && !wait(&o_free[v_segment & 1], (uint32_t)(v_segment / 2 - 1))) return false;
+          if (!wait(&full[v_slot], v_turn)) return false;
+          if (!wait(&p_full[2 * (u & 1)], (uint32_t)(u >> 1))) return false;
+          tc_fence_after();
+          values(d, p, v_slot, !v_first, 0);
+          if (!wait(&p_full[2 * (u & 1) + 1], (uint32_t)(u >> 1))) return false;
+          tc_fence_after();
+          values(d, p, v_slot, true, 1);
+          commit(&empty[v_slot]);
+          commit(&o_full[0]);
+          return true;
+        };
+        for (int64_t u = 0; ok && u < count; ++u) {
+          Note n;
+          ok = read_note(u, n);
+          if (!ok) break;
+          if (n.flags & kFirst) ++segment;
+          ok = wait(&full[slot], turn);
+          if (!ok) break;
+          tc_fence_after();
+          scores(tmem + (uint32_t)(u & 1) * kTile, q_base + (uint32_t)(segment & q_odd) * q_tile, slot);
+          commit(&s_full[u & 1]);
+          commit(&empty[slot]);
+          if (n.flags & kLast) commit(&q_free[segment & q_odd]);
+          step();
+          if (u > 0) ok = products(u - 1);
+          v_slot = slot;
+          v_turn = turn;
+          v_segment = segment;
+          v_first = n.flags & kFirst;
+          step();
+        }
+        if (ok && count > 0) ok = products(count - 1);
+      } else {
+        // the tiles take turns: P V of a tile, then its next scores behind it
+        Note n;
+        n.flags = 0;
+        n.count = 0;
+        bool two = false;
+        uint32_t p_at = 0;       // parities of the next p_full
+        uint32_t segs_of[2] = {0, 0};
+        auto rows_two = [&](const Note& x) {
+          const int pass = x.seg % a.passes;
+          return x.count * a.group > (pass * 2 + 1) * kTile;
+        };
+        auto first_scores = [&](int64_t u) {  // of a segment's first unit here
+          if (!read_note(u, n)) return false;
+          ++segment;
+          two = rows_two(n);
+          if (!wait(&full[slot], turn)) return false;
+          tc_fence_after();
+          const uint32_t q_at = q_base + (uint32_t)(segment & q_odd) * 2 * q_tile;
+          for (int t = 0; t < (two ? 2 : 1); ++t) {
+            scores(tmem + t * kTile, q_at + t * q_tile, slot);
+            commit(&s_full[t]);
+          }
+          commit(&empty[slot]);
+          if (n.flags & kLast) commit(&q_free[segment & q_odd]);
+          step();
+          return true;
+        };
+        if (count > 0) ok = first_scores(0);
+        for (int64_t u = 0; ok && u < count; ++u) {
+          // slot: V of this unit
+          const int v_slot = slot;
+          const uint32_t v_turn = turn;
+          const bool first = n.flags & kFirst, last = n.flags & kLast;
+          step();
+          ok = wait(&full[v_slot], v_turn);
+          if (!ok) break;
+          Note next = n;
+          if (!last) {
+            ok = read_note(u + 1, next) && wait(&full[slot], turn);
+            if (!ok) break;
+          }
+          const uint32_t q_at = q_base + (uint32_t)(segment & q_odd) * 2 * q_tile;
+          for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
+            const uint32_t d = tmem + 2 * kTile + t * DP, p = tmem + t * kTile;
+            if (first && segs_of[t] > 0) ok = wait(&o_free[t], segs_of[t] - 1);
+            if (ok) ok = wait(&p_full[2 * t], p_at >> t);
+            if (!ok) break;
+            tc_fence_after();
+            values(d, p, v_slot, !first, 0);
+            ok = wait(&p_full[2 * t + 1], p_at >> t);
+            if (!ok) break;
+            tc_fence_after();
+            values(d, p, v_slot, true, 1);
+            if (!last) {
+              scores(tmem + t * kTile, q_at + t * q_tile, slot);
+              commit(&s_full[t]);
+            } else {
+              commit(&o_full[t]);
+              ++segs_of[t];
+            }
+            p_at ^= 1u << t;
+          }
+          if (!ok) break;
+          commit(&empty[v_slot]);
+          if (!last) {
+            commit(&empty[slot]);
+            if (next.flags & kLast) commit(&q_free[segment & q_odd]);
+            step();
+            n = next;
+          } else if (u + 1 < count) {
+            ok = first_scores(u + 1);
+          }
+        }
+      }
+      // none of the matrix unit's arrivals may come after the shared memory has gone to another CTA
+      __syncwarp();
+      if (leader) mma_commit(drain);
+      mbar_wait_bounded(drain, 0);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // requests without a position: zeros
+    const int64_t vecs = (int64_t)a.q_heads * a.head_dim / 8;
+    for (int r = blockIdx.x; r < a.num_reqs; r += gridDim.x) {
+      uint32_t ignore = 0;
+      const Req q = request(a, r, ignore);
+      if (q.units > 0 || q.count <= 0) continue;
+      uint4* o = reinterpret_cast<uint4*>(a.out) + q.first * vecs;
+      for (int64_t i = tid; i < q.count * vecs; i += 128 * kRows) o[i] = make_uint4(0, 0, 0, 0);
+    }
+    const int t = warp >> 2;                 // the tile
+    if ((warp & 3) < a.warps) {
+      // -------------------------------------------------------------- softmax
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes, in bits 16..
+      const float c = a.scale_log2;
+      int64_t segment = -1, mine_u = 0;      // mine_u: units of this tile so far
+      uint32_t segments = 0;                 // of this tile
+      float ref = 0.f;
+      uint64_t part[2] = {0, 0};             // sums of weights, two by two
+      uint64_t mask = 0;
+      int tok = 0, g = 0;
+      bool mine = false, from_start = false;
+      bool ok = true;
+      for (int64_t u = 0; u < count; ++u) {
+        Note n;
+        if (!read_note(u, n)) break;
+        const int head = n.seg / a.passes, pass = n.seg - head * a.passes;
+        const int row = (pass * kRows + t) * kTile + (tid & 127);
+        if (n.flags & kFirst) {
+          ++segment;
+          tok = row / a.group;
+          g = row - tok * a.group;
+          mine = tok < n.count;
+          from_start = n.flags & kFromStart;
+          mask = 0;
+          if (mine) mask = a.tree_mask != nullptr ? (uint64_t)a.tree_mask[n.first + tok] : ~0ull >> (63 - tok);
+        }
+        if (kRows == 2 && t == 1 && n.count * a.group <= (pass * 2 + 1) * kTile) continue;
+        const int sb = kRows == 1 ? (int)(u & 1) : t;
+        const uint32_t s_at = tmem + lanes + sb * kTile;
+        const uint32_t o_at = tmem + lanes + 2 * kTile + (kRows == 1 ? (uint32_t)(segment & 1) : (uint32_t)t) * DP;
+        ok = wait(&s_full[sb], (uint32_t)(kRows == 1 ? u >> 1 : mine_u));
+        if (!ok) break;
+        ++mine_u;
+        tc_fence_after();
+        uint32_t s[kTile];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, s + 32 * b);
+        tmem_wait_ld();
+        if (n.step < kTile || (n.valid[0] & n.valid[1] & n.valid[2] & n.valid[3]) != kFull) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            // word b of what this row sees: the context before `step`, its mask from there on
+            const int from = n.step - 32 * b;
+            uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
+            if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
+            else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
+            see &= n.valid[b];
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!((see >> y) & 1u)) s[32 * b + y] = 0xff800000u;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int z = 0; z < kTile; z += 4)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[z + y]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        if (n.flags & kFirst) {
+          ref = top > -INFINITY ? top : kRefStart;
+          part[0] = part[1] = 0;
+        } else {
+          const bool raise = mine && top > ref + kLazy;
+          if (__any_sync(kFull, raise)) {
+            // one tile: the last unit's P V may still run (two: S of this unit came behind it)
+            if (kRows == 1) {
+              ok = wait(&o_full[0], (uint32_t)(u - 1));
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const float f = raise ? ex2(ref - top) : 1.f;
+            if (raise) ref = top;
+            part[0] = mul2(part[0], pair(f, f));
+            part[1] = mul2(part[1], pair(f, f));
+#pragma unroll 1
+            for (int b = 0; b < DP / 32; ++b) {
+              uint32_t o[32];
+              tmem_ld32(o_at + 32 * b, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st32(o_at + 32 * b, o);
+            }
+          }
+        }
+        const uint64_t c2 = pair(c, c), r2 = pair(-ref, -ref);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t p[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            float e0, e1;
+            unpair(fma2(pair(__uint_as_float(s[32 * b + 2 * y]), __uint_as_float(s[32 * b + 2 * y + 1])), c2, r2),
+                   e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            part[y & 1] = add2(part[y & 1], pair(e0, e1));
+            p[y] = pack_bf16(e0, e1);
+          }
+          tmem_st16(s_at + 16 * b, p);
+          if (b & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * sb + (b >> 1)]);
+          }
+        }
+        if (!(n.flags & kLast)) continue;
+        // ------------------------------------------------------------ output
+        float sum;
+        {
+          float a0, a1, b0, b1;
+          unpair(part[0], a0, a1);
+          unpair(part[1], b0, b1);
+          sum = (a0 + a1) + (b0 + b1);
+        }
+        // a wait sees the last phase only: those before it in turn (S of this unit came behind u - 2's)
+        if (kRows == 1) ok = (u == 0 || wait(&o_full[0], (uint32_t)u - 1)) && wait(&o_full[0], (uint32_t)u);
+        else ok = wait(&o_full[t], segments);
+        if (!ok) break;
+        ++segments;
+        tc_fence_after();
+        const bool whole = from_start && (n.flags & kToEnd);
+        uint64_t spoilt = bad[segment & (kBadRing - 1)];
+        spoilt &= mask;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int in_part = t * kTile + (tid & 127);
+        float* part_at = a.parts + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * a.part_rows * DP;
+        // 4 lanes hold 4 rows; they exchange 16-byte pieces, so that a store writes 64 bytes of
+        // each of 8 rows
+        const int64_t own = !mine ? -1
+                            : whole ? ((int64_t)(n.first + tok) * a.q_heads + head * a.group + g) * a.head_dim
+                                    : (int64_t)in_part * DP;
+        int64_t to[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) to[y] = __shfl_sync(kFull, own, (lane & 28) + y);
+#pragma unroll 1
+        for (int b = 0; b < DP / 32; ++b) {
+          uint32_t o[32];
+          tmem_ld32(o_at + 32 * b, o);
+          tmem_wait_ld();
+          // values that were set to 0, where this row sees them
+          for (uint64_t left = spoilt; left != 0; left &= left - 1) {
+            const int64_t p = (int64_t)n.ctx + __ffsll((long long)left) - 1;
+            int64_t lb, off;
+            a.div.divmod(p, lb, off);
+            const int64_t blk = a.table[(int64_t)n.r * a.stride + lb];
+            const __nv_bfloat16* v = a.v_cache + ((blk * a.div.size + off) * a.kv_heads + head) * a.head_dim;
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (32 * b + y < a.head_dim &&
+                  (__bfloat16_as_ushort(v[32 * b + y]) & 0x7f80u) == 0x7f80u)
+                o[y] = 0x7fc00000u;
+          }
+          if (whole) {
+            uint4 z[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t* e = o + 8 * y;
+              auto two = [&](int k) {
+                return pack_bf16(__uint_as_float(e[k]) * inv, __uint_as_float(e[k + 1]) * inv);
+              };
+              z[y] = make_uint4(two(0), two(2), two(4), two(6));
+            }
+            exchange(z[0], z[1], lane & 1, 1);
+            exchange(z[2], z[3], lane & 1, 1);
+            exchange(z[0], z[2], lane & 2, 2);
+            exchange(z[1], z[3], lane & 2, 2);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (to[y] >= 0 && 32 * b + 8 * (lane & 3) < a.head_dim)
+                *reinterpret_cast<uint4*>(a.out + to[y] + 32 * b + 8 * (lane & 3)) = z[y];
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint4 z[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                z[y] = make_uint4(o[16 * h + 4 * y], o[16 * h + 4 * y + 1], o[16 * h + 4 * y + 2], o[16 * h + 4 * y + 3]);
+              exchange(z[0], z[1], lane & 1, 1);
+              exchange(z[2], z[3], lane & 1, 1);
+              exchange(z[0], z[2], lane & 2, 2);
+              exchange(z[1], z[3], lane & 2, 2);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                if (to[y] >= 0)
+                  *reinterpret_cast<uint4*>(part_at + to[y] + 32 * b + 16 * h + 4 * (lane & 3)) = z[y];
+            }
+          }
+        }
+        if (!whole && mine)
+          reinterpret_cast<float2*>(a.parts + (int64_t)gridDim.x * 2 * a.part_rows * DP)[
+              ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * a.part_rows + in_part] = make_float2(ref, sum);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[kRows == 1 ? (int)(segment & 1) : t]);
+      }
+    }
+  }
+  // all roles have come so far: no copy, matrix instruction or arrival is left
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) {
+    tmem_dealloc(tmem, 512);
+    if (lane == 0 && *abort != 0 && a.err != nullptr) atomicOr(a.err, KV_ERR_TIMEOUT);
+  }
+}
+
+// Join: out = sum_i f_i o_i / sum_i f_i l_i, f_i = 2^(ref_i - max ref), over the parts of the
+// segment that CTA x began and did not end: its own second part, then the first parts of the
+// same member of the gangs behind it.  A warp per row, 4 channels a lane.
+template <int DP, int kRows>
+__global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const __grid_constant__ TreeArgs a) {
+  pdl_allow_next();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int x = blockIdx.x;
+  const int4 j = a.joins[x];
+  if (j.x < 0) return;
+  const int head = j.y / a.passes, pass = j.y - head * a.passes;
+  const int row0 = pass * kRows * kTile, rows = min(j.w * a.group - row0, kRows * kTile);
+  const int g0 = x / a.gang, member = x - g0 * a.gang;
+  const float2* stats = reinterpret_cast<const float2*>(a.parts + (int64_t)a.gangs * a.gang * 2 * a.part_rows * DP);
+  const int first = a.q_start[j.x];
+  for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rows;
+       row += gridDim.y * (kJoinThreads / 32)) {
+    float top = kRefStart, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 4;
+    for (int i = g0; i <= j.z; i += kBatch) {
+      float2 st[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int64_t part = ((int64_t)((i + b) * a.gang + member) * 2 + (i + b == g0 ? 1 : 0)) * a.part_rows + row;
+        st[b] = make_float2(kRefStart, 0.f);
+        v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + b <= j.z) {
+          st[b] = stats[part];
+          if (4 * lane < DP) v[b] = *reinterpret_cast<const float4*>(a.parts + part * DP + 4 * lane);
+        }
+      }
+      float up = top;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) up = fmaxf(up, st[b].x);
+      const float f = ex2(top - up);
+      top = up;
+      l *= f;
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float h = ex2(st[b].x - up);
+        l = fmaf(st[b].y, h, l);
+        o = make_float4(fmaf(v[b].x, h, o.x), fmaf(v[b].y, h, o.y), fmaf(v[b].z, h, o.z), fmaf(v[b].w, h, o.w));
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int tok = (row0 + row) / a.group, g = row0 + row - tok * a.group;
+    if (4 * lane < a.head_dim)
+      *reinterpret_cast<uint2*>(
+          a.out + ((int64_t)(first + tok) * a.q_heads + head * a.group + g) * a.head_dim + 4 * lane) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  }
+}
+
+// How a call's work is laid out.
+struct Plan {
+  int dp, rows, passes, gang, gangs, part_rows, q_rows, q_bufs, slots, warps;
+  int64_t joins_bytes() const { return ((int64_t)gangs * gang * 16 + 127) / 128 * 128; }
+  int64_t bytes() const { return joins_bytes() + (int64_t)gangs * gang * 2 * part_rows * (dp + 2) * 4; }
+};
+Plan plan_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  Plan p;
+  const int group = num_q_heads / num_kv_heads, rows = max_rows * group;
+  p.dp = head_dim <= 64 ? 64 : 128;
+  p.rows = rows > kTile ? 2 : 1;
+  p.passes = (rows + p.rows * kTile - 1) / (p.rows * kTile);
+  const int segs = num_kv_heads * p.passes;
+  // the largest divisor of the (KV head, pass) pairs up to 8
+  p.gang = segs < 8 ? segs : 8;
+  while (segs % p.gang != 0) --p.gang;
+  p.gangs = sm_count() / p.gang;
+  if (p.gangs < 1) p.gang = p.gangs = 1;
+  p.part_rows = rows < p.rows * kTile ? rows : p.rows * kTile;
+  const int tile_rows = rows < kTile ? rows : kTile;
+  p.q_rows = (tile_rows + 7) / 8 * 8;
+  p.warps = (tile_rows + 31) / 32;
+  const int head = p.dp == 64 ? Smem<64>::kHead : Smem<128>::kHead;
+  const int q_bytes = (p.q_rows * p.dp * 2 * p.rows + 1023) / 1024 * 1024, slot = kTile * p.dp * 2;
+  const int want = p.dp == 64 ? 10 : 5;
+  p.q_bufs = head + 2 * q_bytes + want * slot <= kSmemMax ? 2 : 1;
+  p.slots = (kSmemMax - head - p.q_bufs * q_bytes) / slot;
+  if (p.slots > 12) p.slots = 12;
+  return p;
+}
+
+template <int DP, int kRows>
+int launch(const TreeArgs& a, cudaStream_t stream) {
+  auto kernel = attention_tree_kernel<DP, kRows>;
+  const int q_bytes = (a.q_bufs * kRows * a.q_rows * DP * 2 + 1023) / 1024 * 1024;
+  // Q's matrix instructions read whole tiles of 128 rows: the ring lies behind it
+  const int smem = Smem<DP>::kHead + q_bytes + a.slots * Smem<DP>::kSlot;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return KV_ECUDA;
+  const unsigned ctas = (unsigned)(a.gangs * a.gang);
+  const int rc = launch_pdl(kernel, ctas, kThreadsOf<kRows>, smem, stream, a);
+  if (rc != KV_OK) return rc;
+  const unsigned chunks = (unsigned)(a.part_rows + 15) / 16;
+  return launch_pdl(join_tree_kernel<DP, kRows>, dim3(ctas, chunks), kJoinThreads, 0, stream, a);
 }
 
 int sizes(int32_t num_reqs, int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads,
@@ -139,7 +994,7 @@ extern "C" int64_t kv_attention_tree_workspace(int32_t num_reqs, int32_t max_row
                                                int32_t num_q_heads, int32_t num_kv_heads,
                                                int32_t head_dim) {
   const int rc = sizes(num_reqs, max_rows, num_q_heads, num_kv_heads, head_dim);
-  return rc != KV_OK ? rc : 0;
+  return rc != KV_OK ? rc : plan_of(max_rows, num_q_heads, num_kv_heads, head_dim).bytes();
 }
 
 extern "C" int kv_attention_tree(const void* query, int64_t query_stride, const void* k_cache,
@@ -190,6 +1045,7 @@ extern "C" int kv_attention_tree(const void* query, int64_t query_stride, const 
   if (over_input(out, out_bytes) || over_input(workspace, need) ||
       overlap(out, out_bytes, workspace, need))
     return KV_EINVAL;
+  const Plan p = plan_of(max_rows, num_q_heads, num_kv_heads, head_dim);
   const TreeArgs a{static_cast<const __nv_bfloat16*>(query), query_stride,
                    reinterpret_cast<const __nv_bfloat16*>(k_layer),
                    reinterpret_cast<const __nv_bfloat16*>(v_layer), num_blocks,
@@ -197,8 +1053,9 @@ extern "C" int kv_attention_tree(const void* query, int64_t query_stride, const 
                    num_q_heads / num_kv_heads, block_table, table_stride, q_start_loc, span_start,
                    context_len, tree_mask, num_reqs, num_rows, max_rows,
                    fminf(scale * 1.44269504088896340736f, FLT_MAX),
-                   static_cast<__nv_bfloat16*>(out), d_err};
-  if ((int64_t)num_reqs * max_rows > 65535) return KV_EUNSUPPORTED;
-  return launch_pdl(attention_tree_kernel, dim3((unsigned)num_q_heads, (unsigned)(num_reqs * max_rows)),
-                    kThreads, 0, stream, a);
+                   static_cast<__nv_bfloat16*>(out), d_err, p.passes, p.gang, p.gangs, p.part_rows,
+                   p.q_rows, p.q_bufs, p.slots, p.warps, static_cast<int4*>(workspace),
+                   reinterpret_cast<float*>(static_cast<char*>(workspace) + p.joins_bytes())};
+  if (p.dp == 64) return p.rows == 1 ? launch<64, 1>(a, stream) : launch<64, 2>(a, stream);
+  return p.rows == 1 ? launch<128, 1>(a, stream) : launch<128, 2>(a, stream);
 }

@@ -175,6 +175,34 @@ __device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------------------
+// Arithmetic of the softmax, and rows that change lanes
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// One step of a transposition over lanes: with the lane `mask` away, a for its b (the lower of the
+// two lanes keeps its a, the higher its b).
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b, bool high, int mask) {
+  const uint32_t got = __shfl_xor_sync(kFull, high ? a : b, mask);
+  a = high ? got : a;
+  b = high ? b : got;
+}
+__device__ __forceinline__ void exchange(uint4& a, uint4& b, bool high, int mask) {
+  exchange(a.x, b.x, high, mask);
+  exchange(a.y, b.y, high, mask);
+  exchange(a.z, b.z, high, mask);
+  exchange(a.w, b.w, high, mask);
+}
+
+// ---------------------------------------------------------------------------
 // Work stealing.  take_over() asks the hardware for a CTA of this grid that has not started (one
 // thread; 16 bytes of answer, counted by `bar`, 16-byte aligned); if it gives one, that CTA never
 // starts and its work is the asker's.  After a refusal no more is asked for.

@@ -725,7 +725,8 @@ int kv_tree_layout(const int32_t* parents, const int32_t* q_start_loc, const int
  * row, num_q_heads not a multiple of num_kv_heads, a scale that is not positive and finite, a
  * workspace that is missing, misaligned or too small, out or workspace sharing bytes with
  * each other or an input; KV_EUNSUPPORTED for head_dim above 128 or not a multiple of 8, a
- * stride not a multiple of 8, more than 64 query heads per KV head, num_q_heads > 4096.
+ * stride not a multiple of 8, more than 64 query heads per KV head, num_q_heads > 4096, a pool of
+ * more than 2^31 - 1 tokens (num_blocks * block_size).
  */
 int kv_attention_tree(const void* query, int64_t query_stride, const void* k_cache,
                       const void* v_cache, int32_t layer, int32_t num_layers, int64_t num_blocks,

@@ -135,6 +135,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real)
   const int n = real ? 16 : 0;  // 0: zeros, nothing is read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
   // registers of the warpgroups: 384 threads x 168 at launch >= 128 x (224 + 104 + 168), 512 x 128 >= 128 x
   // (184 + 184 + 56 + 80)
   constexpr int kSoftmaxRegs = kRows == 1 ? 224 : 184, kIssueRegs = kRows == 1 ? 104 : 56, kCopyRegs = 80;
-  constexpr int kLag = DP == 128 ? 3 : 7;   // groups of copies in flight beside the newest
+  constexpr int kLag = DP == 128 ? 1 : 3;   // units in flight beside the newest: 128 KB with it
   constexpr int kPieces = DP / 8;           // 16-byte pieces of a row
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -280,42 +283,55 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
       now.ctx = __shfl_sync(kFull, mine.ctx, r - base);
       now.units = __shfl_sync(kFull, mine.units, r - base);
     };
-    // this lane's row of the unit: its place in the cache in rows of all heads; < 0: none
-    auto place = [&]() {
+    // This lane's row of a unit, in two steps, so that its table entry arrives while the unit before
+    // it is copied: block and offset, then the token's number in the pool (kNowhere: none).
+    constexpr uint32_t kNowhere = ~0u;
+    int32_t next_block = kNull;
+    uint32_t next_off = 0;
+    auto look_up = [&]() {
       const uint32_t p = now.lo + (uint32_t)tile * kTile + w * 32 + lane;
-      if (p >= now.hi) return (int64_t)-1;
-      int64_t lb, off;
-      a.div.divmod((int64_t)p, lb, off);
-      const int32_t b = a.table[(int64_t)r * a.stride + lb];
-      if (b == kNull) return (int64_t)-1;
-      if (b < 0 || b >= a.num_blocks) {
-        err |= KV_ERR_BAD_BLOCK;
-        return (int64_t)-1;
+      next_block = kNull;
+      if (p < now.hi) {
+        int64_t lb, off;
+        a.div.divmod((int64_t)p, lb, off);
+        next_off = (uint32_t)off;
+        next_block = a.table[(int64_t)r * a.stride + lb];
       }
-      return (int64_t)b * a.div.size + off;
     };
-    int64_t at = -1;
+    auto token = [&]() {
+      if (next_block == kNull) return kNowhere;
+      if (next_block < 0 || next_block >= a.num_blocks) {
+        err |= KV_ERR_BAD_BLOCK;
+        return kNowhere;
+      }
+      return (uint32_t)next_block * (uint32_t)a.div.size + next_off;
+    };
     if (count > 0) {
       look();
       take();
-      at = place();
+      look_up();
     }
     const int sub = lane / kPieces, piece = lane % kPieces;
     constexpr int kPer = 32 / kPieces;      // rows of a copy instruction
-    const bool piece_real = piece * 8 < a.head_dim;
+    constexpr int kTurns = 8 / kPer;        // instructions after which the swizzle repeats
+    const bool piece_real = piece * 8 < a.head_dim, dense = a.head_dim == DP;
+    const uint32_t row_bytes = (uint32_t)(a.kv_heads * a.head_dim * 2);
+    const char* const k_lane = reinterpret_cast<const char*>(a.k_cache) + (piece_real ? piece * 16 : 0);
+    const int64_t k_to_v = reinterpret_cast<const char*>(a.v_cache) - reinterpret_cast<const char*>(a.k_cache);
     // rows w * 32 + i * kPer + sub: their 8-row groups are 1024 bytes, column blocks of 64 channels apart
-    const uint32_t dst_lane = (uint32_t)((w * 32 + sub) * 128 + (piece >> 3) * (kTile * 128));
-    const uint32_t col_lane = (uint32_t)(((piece & 7) ^ sub) << 4);
-    const uint32_t ring_at = smem_addr(ring);
+    uint32_t dst_lane[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+      dst_lane[i] = smem_addr(ring) + (uint32_t)((w * 32 + i * kPer + sub) * 128 + (piece >> 3) * (kTile * 128) +
+                                                 (((piece & 7) ^ (i * kPer + sub)) << 4));
 
-    int64_t group = 0;        // groups of copies issued: 2 a unit
-    int slot = 0;
-    uint32_t turn = 0;
-    int done_slot = 0;        // the next slot to be told about
-    int64_t done = 0;
+    int64_t told = 0;         // units that the issuer may use
+    int k_slot = 0, v_slot = 1, told_slot = 0;
+    uint32_t k_turn = 0, v_turn = 0;
     int64_t segment = -1;     // of this CTA, counted
-    int hist_step[5] = {kTile, kTile, kTile, kTile, kTile};  // of the last units: where the step's rows begin
-    int hist_seg[5] = {};
+    int hist_step[kLag + 2], hist_seg[kLag + 2];  // of the last units: where the step's rows begin
+#pragma unroll
+    for (int i = 0; i < kLag + 2; ++i) hist_step[i] = kTile, hist_seg[i] = 0;
     bool ok = true;
     // Values of the step's rows that are not finite: 0, and their rows noted.
     auto check_values = [&](int step, int seg_no, int s) {
@@ -340,53 +356,43 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
       if (any)
         atomicOr(reinterpret_cast<unsigned long long*>(smem + L::kBad) + seg_no, 1ull << (y - step));
     };
-    // Group `done` has arrived: the issuer may use it.  `back`: units since its own.
+    // Unit `told` has arrived: the issuer may use it.  `back`: units issued behind it.
     auto tell = [&](int back) {
-      if (done & 1) {
-        int step = kTile, seg_no = 0;
+      const int s0 = told_slot, s1 = s0 + 1 == a.slots ? 0 : s0 + 1;
+      int step = kTile, seg_no = 0;
 #pragma unroll
-        for (int i = 0; i < 5; ++i)
-          if (i == back) step = hist_step[i], seg_no = hist_seg[i];
-        if (step < kTile) {
-          __syncwarp();
-          check_values(step, seg_no, done_slot);
-        }
+      for (int i = 0; i < kLag + 2; ++i)
+        if (i == back) step = hist_step[i], seg_no = hist_seg[i];
+      if (step < kTile) {
+        __syncwarp();
+        check_values(step, seg_no, s1);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[done_slot]);
-      ++done;
-      if (++done_slot == a.slots) done_slot = 0;
-    };
-    auto advance_slot = [&]() {
-      copy_commit();
-      ++group;
-      if (++slot == a.slots) {
-        slot = 0;
-        ++turn;
+      if (lane == 0) {
+        mbar_arrive(&full[s0]);
+        mbar_arrive(&full[s1]);
       }
+      ++told;
+      told_slot = s1 + 1 == a.slots ? 0 : s1 + 1;
     };
-    // The issuer needs what is in flight to get to the end of a wait of this role: the oldest groups
-    // are told about until it is over.
-    auto wait_telling = [&](uint64_t* b, uint32_t parity) {
-      while (done < group && !__any_sync(kFull, mbar_try_wait(b, parity & 1))) {
-        switch ((int)(group - done)) {
-          case 1: copy_wait<0>(); break;
-          case 2: copy_wait<1>(); break;
-          case 3: copy_wait<2>(); break;
-          case 4: copy_wait<3>(); break;
-          case 5: copy_wait<4>(); break;
-          case 6: copy_wait<5>(); break;
-          default: copy_wait<6>(); break;
-        }
-        tell((int)((group - 1) / 2 - done / 2));
+    // The issuer may need units in flight to get to the end of a wait of this role: the oldest ones
+    // are told about until it is over.  `issued`: units whose copies are under way or done.
+    auto wait_telling = [&](uint64_t* b, uint32_t parity, int64_t issued) {
+      while (told < issued && !__any_sync(kFull, mbar_try_wait(b, parity & 1))) {
+        const int back = (int)(issued - 1 - told);  // groups behind the oldest, kLag at most
+        if (back == 0) copy_wait<0>();
+        else if (back == 1) copy_wait<1>();
+        else if (back == 2) copy_wait<2>();
+        else copy_wait<3>();
+        tell(back + 1);  // the next unit is in the history already
       }
       return wait(b, parity);
     };
     bool first_run = true;
     for (int64_t u = 0; ok && u < count; ++u) {
-      // this unit, then the next one's place (its table entries arrive meanwhile)
-      const int64_t here = at;
+      // this unit, then the next one's table entries
+      const uint32_t here = token();
       const Req req = now;
       const int here_r = r, here_seg = seg, here_tile = tile;
       const bool first = first_run || tile == 0;
@@ -407,7 +413,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
             take();
           }
         }
-        at = place();
+        look_up();
       }
       if (first) {
         ++segment;
@@ -416,13 +422,13 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
       const int64_t tile_at = (int64_t)req.lo + (int64_t)here_tile * kTile;
       const int step = (int)max((int64_t)-kTile, min((int64_t)kTile, (int64_t)req.ctx - tile_at));
 #pragma unroll
-      for (int i = 4; i > 0; --i) hist_step[i] = hist_step[i - 1], hist_seg[i] = hist_seg[i - 1];
+      for (int i = kLag + 1; i > 0; --i) hist_step[i] = hist_step[i - 1], hist_seg[i] = hist_seg[i - 1];
       hist_step[0] = step;
       hist_seg[0] = (int)(segment & (kBadRing - 1));
       // describe it
       if (u >= kNotes) ok = wait(&note_free[u & (kNotes - 1)], (uint32_t)(u >> 3) - 1);
       if (!ok) break;
-      const uint32_t valid = __ballot_sync(kFull, here >= 0);
+      const uint32_t valid = __ballot_sync(kFull, here != kNowhere);
       if (lane == 0) {
         Note* n = &notes[u & (kNotes - 1)];
         n->valid[w] = valid;
@@ -443,12 +449,13 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
         mbar_arrive(&note_full[u & (kNotes - 1)]);
       }
       const int head = here_seg / a.passes;
-      // Q with the segment's first K
-      if (turn > 0) ok = wait(&empty[slot], turn - 1);
-      if (ok && first && segment >= a.q_bufs)
-        ok = wait_telling(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1);
+      if (first && segment >= a.q_bufs)
+        ok = wait_telling(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1, u);
+      ok = ok && (k_turn == 0 || mbar_wait_role(&empty[k_slot], (k_turn - 1) & 1, abort)) &&
+           (v_turn == 0 || mbar_wait_role(&empty[v_slot], (v_turn - 1) & 1, abort));
+      ok = all(ok);
       if (!ok) break;
-      if (first) {
+      if (first) {  // Q with the segment's first unit
         const int pass = here_seg - head * a.passes;
         for (int t = 0; t < kRows; ++t) {
           const int row0 = (pass * kRows + t) * kTile, left = req.count * a.group - row0;  // rows of this tile
@@ -462,34 +469,44 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
           }
         }
       }
-      const int64_t off = (here * a.kv_heads + head) * a.head_dim;   // of this lane's row
-      auto rows = [&](const __nv_bfloat16* cache) {
-        const uint32_t to = ring_at + slot * L::kSlot + dst_lane;
+      {
+        const char* const src = k_lane + head * a.head_dim * 2;
+        const uint32_t k_to = k_slot * L::kSlot, v_to = v_slot * L::kSlot;
+        if (valid == kFull && dense) {
 #pragma unroll
-        for (int i = 0; i < 32 / kPer; ++i) {
-          const int64_t o = __shfl_sync(kFull, here >= 0 ? off : (int64_t)-1, i * kPer + sub);
-          const bool real = o >= 0 && piece_real;
-          copy16(to + i * kPer * 128 + (col_lane ^ (((i * kPer) & 7) << 4)),
-                 cache + (real ? o + piece * 8 : 0), real);
+          for (int i = 0; i < 32 / kPer; ++i) {
+            const char* p = src + (uint64_t)__shfl_sync(kFull, here, i * kPer + sub) * row_bytes;
+            const uint32_t to = dst_lane[i % kTurns] + (i / kTurns) * 1024;
+            copy16(to + k_to, p);
+            copy16(to + v_to, p + k_to_v);
+          }
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < 32 / kPer; ++i) {
+            const uint32_t x = __shfl_sync(kFull, here, i * kPer + sub);
+            const bool real = x != kNowhere && piece_real;
+            const char* p = real ? src + (uint64_t)x * row_bytes : src;
+            const uint32_t to = dst_lane[i % kTurns] + (i / kTurns) * 1024;
+            copy16(to + k_to, p, real);
+            copy16(to + v_to, p + k_to_v, real);
+          }
         }
-      };
-      rows(a.k_cache);
-      advance_slot();
-      if (group - done > kLag) {
-        copy_wait<kLag>();
-        tell((int)((group - 1) / 2 - done / 2));
       }
-      if (turn > 0) ok = wait(&empty[slot], turn - 1);
-      if (!ok) break;
-      rows(a.v_cache);
-      advance_slot();
-      if (group - done > kLag) {
+      copy_commit();
+      auto two_on = [&](int& slot, uint32_t& turn) {
+        slot += 2;
+        if (slot >= a.slots) slot -= a.slots, ++turn;
+      };
+      two_on(k_slot, k_turn);
+      two_on(v_slot, v_turn);
+      if (u - told >= kLag) {
         copy_wait<kLag>();
-        tell((int)((group - 1) / 2 - done / 2));
+        tell((int)(u - told));
       }
     }
     copy_wait<0>();
-    while (ok && done < group) tell((int)((group - 1) / 2 - done / 2));
+    const int64_t issued = count;
+    while (ok && told < issued) tell((int)(issued - 1 - told));
     report(a.err, err);
   } else if (warp >= kIssuer) {
     // ---------------------------------------------------------------- matrix instructions
@@ -1017,6 +1034,8 @@ extern "C" int kv_attention_tree(const void* query, int64_t query_stride, const 
   const int64_t row = (int64_t)num_q_heads * head_dim;
   if (query_stride < row) return KV_EINVAL;
   if (query_stride % 8 != 0) return KV_EUNSUPPORTED;
+  if (num_blocks > INT32_MAX / block_size || (int64_t)num_kv_heads * head_dim > INT32_MAX / 2)
+    return KV_EUNSUPPORTED;  // tokens of the pool and bytes of a row are counted in 32 bits
   if (num_reqs == 0 || num_rows == 0) return KV_OK;
   if (query == nullptr || out == nullptr || k_cache == nullptr || v_cache == nullptr ||
       q_start_loc == nullptr || context_len == nullptr || !aligned(query, 16) ||

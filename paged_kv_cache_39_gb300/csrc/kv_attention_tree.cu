@@ -44,7 +44,8 @@ namespace kvp {
 namespace {
 
 constexpr int kTile = 128;             // keys of a unit, rows of a tile
-constexpr int kCopiers = 4;            // warps
+constexpr int kCopiers = 4;            // warps, where they copy; where TMA does:
+constexpr int kHelpers = 3;            // that load Q and check values, beside the one that issues copies
 constexpr int kNotes = 8;              // units described ahead (a power of two: 2^3)
 constexpr int kBadRing = 16;           // segments whose values are noted
 constexpr float kLazy = 8.0f;          // log2 of the most a weight may pass the reference
@@ -77,6 +78,7 @@ struct TreeArgs {
   int32_t q_rows;    // rows of a tile's Q in shared memory (a multiple of 8)
   int32_t q_bufs;    // Q of this segment and the next, where there is room
   int32_t slots;     // of the ring
+  int32_t box;       // tokens of a TMA box (a power of two that divides the block), or 1
   int32_t warps;     // softmax warps of a tile that can have rows
   int4* joins;       // [CTAs]: the segment a CTA began and did not end: request, segment, last gang
   float* parts;      // [CTAs][2][part_rows][DP], then (reference, sum) [CTAs][2][part_rows]
@@ -86,12 +88,13 @@ struct TreeArgs {
 struct Req {
   int32_t first, count;   // rows
   uint32_t lo, hi, ctx;   // positions [lo, hi); the step's rows begin at ctx
+  uint32_t base;          // of the first unit: lo, down to a multiple of a box
   int32_t units;
 };
 __device__ __forceinline__ Req request(const TreeArgs& a, int r, uint32_t& err) {
   const StepRows rows = step_rows(a.q_start, r, a.num_rows, a.max_rows);
   const int32_t s0 = a.span_start != nullptr ? a.span_start[r] : 0, c = a.context_len[r];
-  Req q = {rows.first, rows.count, 0, 0, 0, 0};
+  Req q = {rows.first, rows.count, 0, 0, 0, 0, 0};
   if (rows.count < 0) err |= KV_ERR_BAD_QSL;
   if (rows.count <= 0) return q;
   if (s0 < 0 || c < s0) {
@@ -103,7 +106,8 @@ __device__ __forceinline__ Req request(const TreeArgs& a, int r, uint32_t& err) 
   q.ctx = (uint32_t)c;
   q.lo = (uint32_t)s0;
   q.hi = (uint32_t)(end < reach ? end : reach);
-  q.units = q.hi > q.lo ? (int32_t)((q.hi - q.lo + kTile - 1) / kTile) : 0;
+  q.base = q.lo & ~(uint32_t)(a.box - 1);
+  q.units = q.hi > q.lo ? (int32_t)((q.hi - q.base + kTile - 1) / kTile) : 0;
   return q;
 }
 
@@ -115,11 +119,12 @@ struct __align__(16) Note {
   int32_t flags;
   int32_t first, count;    // the request's rows
   uint32_t ctx;
-  int32_t pad;
+  int32_t seen;            // keys [seen & 255, seen >> 8) of the unit are positions of the request
 };
-enum Flags { kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8 };  // of this CTA's share; of the segment
+// of this CTA's share; of the segment; kEdge: values to check (loaded by TMA)
+enum Flags { kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8, kEdge = 16 };
 
-constexpr int kNumBars = 2 * 12 + 2 * kNotes + 2 + 4 + 2 + 2 + 2 + 1;
+constexpr int kNumBars = 2 * 12 + 2 * kNotes + 2 + 4 + 2 + 2 + 2 + 1 + 2 + 2 * kNotes;
 template <int DP>
 struct Smem {
   static constexpr int kSlot = kTile * DP * 2;
@@ -148,8 +153,10 @@ __device__ __forceinline__ void copy_wait() {
 template <int kRows>
 constexpr int kThreadsOf = 128 * kRows + 256;
 
-template <int DP, int kRows>
-__global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(const __grid_constant__ TreeArgs a) {
+template <int DP, int kRows, bool kTma>
+__global__ void __launch_bounds__(kThreadsOf<kRows>, 1)
+attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap k_map,
+                      const __grid_constant__ CUtensorMap v_map) {
   using L = Smem<DP>;
   constexpr int kThreads = kThreadsOf<kRows>;
   constexpr int kIssuer = 4 * kRows, kCopy = kIssuer + 4;
@@ -170,6 +177,9 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
   uint64_t* o_free = o_full + 2;            // one tile: by segment & 1; two: by tile
   uint64_t* q_free = o_free + 2;            // by segment % q_bufs
   uint64_t* drain = q_free + 2;
+  uint64_t* q_full = drain + 1;             // kTma: by segment % q_bufs
+  uint64_t* edge = q_full + 2;              // kTma: V of units whose values are checked, in turn: arrived,
+  uint64_t* checked = edge + kNotes;        // and checked
   Note* notes = reinterpret_cast<Note*>(smem + L::kNote);
   volatile uint64_t* bad = reinterpret_cast<uint64_t*>(smem + L::kBad);
   int* misc = reinterpret_cast<int*>(smem + L::kMisc);
@@ -185,9 +195,10 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
   if (tid < kNumBars) {
     const uint64_t* b = &bars[tid];
     int count = 1;
-    if (b < empty) count = kCopiers;
-    if (b >= note_full && b < note_free) count = kCopiers;
-    if (b >= note_free && b < s_full) count = kRows * a.warps + 1;
+    if (b < empty) count = kTma ? 1 : kCopiers;
+    if (b >= note_full && b < note_free) count = kTma ? 1 : kCopiers;
+    if (b >= note_free && b < s_full) count = kRows * a.warps + 1 + (kTma ? kHelpers : 0);
+    if ((b >= q_full && b < edge) || b >= checked) count = kHelpers;
     if (b >= p_full && b < o_full) count = a.warps;
     if (b >= o_free && b < q_free) count = a.warps;
     mbar_init(&bars[tid], count);
@@ -228,6 +239,10 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
   const int64_t begin = my_gang * share;
   const int64_t count = my_gang < a.gangs && begin < total ? min(share, total - begin) : 0;
 
+  // what the issuing copier leaves behind: the ring's slots and edge barriers in use
+  uint32_t turns = 0;
+  int slots_used = 0;
+  int64_t edges_used = 0;
   auto all = [](bool ok) { return __all_sync(kFull, ok) != 0; };
   auto wait = [&](uint64_t* b, uint32_t parity) { return all(mbar_wait_role(b, parity & 1, abort)); };
   // a reader's next note; its lanes have all of it
@@ -265,13 +280,95 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
       seg = (int)(rest / units) * a.gang + member;
       tile = (int)(rest % units);
     }
+    fence_proxy_async_smem();
     asm volatile("bar.sync 2, 128;" ::: "memory");  // before the ring is written
+    // Values of the step's rows (key `step` on) that are not finite: 0, and their rows noted.
+    auto check_values = [&](int y, int step, int seg_no, int s) {
+      if (y < step) return;
+      unsigned char* row = ring + s * L::kSlot + y * 128;
+      bool any = false;
+#pragma unroll 4
+      for (int c = 0; c < kPieces; ++c) {
+        uint4* p = reinterpret_cast<uint4*>(row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (y & 7)) << 4));
+        uint4 v = *p;
+        uint32_t e[4] = {v.x, v.y, v.z, v.w};
+        bool hit = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
+          if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0xffffu, hit = true;
+        }
+        if (hit) *p = make_uint4(e[0], e[1], e[2], e[3]);
+        any |= hit;
+      }
+      if (any)
+        atomicOr(reinterpret_cast<unsigned long long*>(smem + L::kBad) + seg_no, 1ull << (y - step));
+    };
+    const int sub = lane / kPieces, piece = lane % kPieces;
+    constexpr int kPer = 32 / kPieces;      // rows of a copy instruction
+    const bool piece_real = piece * 8 < a.head_dim;
+    // Rows of Q of a segment, shared by `warps` warps of which this is number `me`.
+    auto copy_q = [&](int first, int rows, int head, int pass, int buf, int me, int warps) {
+      for (int t = 0; t < kRows; ++t) {
+        const int row0 = (pass * kRows + t) * kTile, left = rows * a.group - row0;  // rows of this tile
+        const uint32_t q_at = smem_addr(q_smem) + (buf * kRows + t) * q_tile;
+        for (int y = me * kPer + sub; y < min(left, kTile); y += warps * kPer) {
+          const int tok = (row0 + y) / a.group, g = row0 + y - tok * a.group;
+          const __nv_bfloat16* src = a.q + (int64_t)(first + tok) * a.q_stride +
+                                     (int64_t)(head * a.group + g) * a.head_dim + piece * 8;
+          copy16(q_at + (piece >> 3) * (a.q_rows * 128) + y * 128 + (((piece & 7) ^ (y & 7)) << 4),
+                 piece_real ? src : a.q, piece_real);
+        }
+      }
+    };
+    if (kTma && w > 0) {
+      // -------------------------------------------------------------- Q, and values at the edges
+      int64_t segment = -1, edges = 0;
+      int slot = 1;              // V of the unit
+      for (int64_t u = 0; u < count; ++u) {
+        Note n;
+        if (!read_note(u, n)) break;
+        const int head = n.seg / a.passes;
+        if (n.flags & kFirst) {
+          ++segment;
+          if (segment >= a.q_bufs && !wait(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1)) break;
+          copy_q(n.first, n.count, head, n.seg - head * a.passes, (int)(segment & q_odd), w - 1, kHelpers);
+          copy_commit();
+          copy_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[segment & q_odd]);
+        }
+        if (n.flags & kEdge) {
+          if (!wait(&edge[edges & (kNotes - 1)], (uint32_t)(edges >> 3))) break;
+          ++edges;
+          for (int y = (w - 1) * 32 + lane; y < kTile; y += kHelpers * 32) {
+            if (y < (n.seen & 255) || y >= n.seen >> 8) {  // of the block, but not of the request
+#pragma unroll
+              for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  *reinterpret_cast<uint4*>(ring + slot * L::kSlot + c * (kTile * 128) + y * 128 +
+                                            ((k ^ (y & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+            } else {
+              check_values(y, n.step, (int)(segment & (kBadRing - 1)), slot);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&checked[(edges - 1) & (kNotes - 1)]);
+        }
+        slot += 2;
+        if (slot >= a.slots) slot -= a.slots;
+      }
+    } else {
+    // ---------------------------------------------------------------- units, in order
     // 32 requests at a time, one a lane
     int base = r;
     Req mine = {};
     auto look = [&]() {
       uint32_t ignore = 0;
-      mine = Req{0, 0, 0, 0, 0, 0};
+      mine = Req{0, 0, 0, 0, 0, 0, 0};
       if (base + lane < a.num_reqs) mine = request(a, base + lane, ignore);
     };
     Req now;
@@ -281,17 +378,19 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
       now.lo = __shfl_sync(kFull, mine.lo, r - base);
       now.hi = __shfl_sync(kFull, mine.hi, r - base);
       now.ctx = __shfl_sync(kFull, mine.ctx, r - base);
+      now.base = __shfl_sync(kFull, mine.base, r - base);
       now.units = __shfl_sync(kFull, mine.units, r - base);
     };
-    // This lane's row of a unit, in two steps, so that its table entry arrives while the unit before
-    // it is copied: block and offset, then the token's number in the pool (kNowhere: none).
+    // This lane's row (kTma: box) of a unit, in two steps, so that its table entry arrives while the unit
+    // before it is copied: block and offset, then the token's number in the pool (kNowhere: none).
+    const int boxes = kTile / a.box;
     constexpr uint32_t kNowhere = ~0u;
     int32_t next_block = kNull;
     uint32_t next_off = 0;
     auto look_up = [&]() {
-      const uint32_t p = now.lo + (uint32_t)tile * kTile + w * 32 + lane;
+      const uint32_t p = now.base + (uint32_t)tile * kTile + (kTma ? lane * a.box : w * 32 + lane);
       next_block = kNull;
-      if (p < now.hi) {
+      if (p < now.hi && (!kTma || lane < boxes)) {
         int64_t lb, off;
         a.div.divmod((int64_t)p, lb, off);
         next_off = (uint32_t)off;
@@ -311,10 +410,8 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
       take();
       look_up();
     }
-    const int sub = lane / kPieces, piece = lane % kPieces;
-    constexpr int kPer = 32 / kPieces;      // rows of a copy instruction
     constexpr int kTurns = 8 / kPer;        // instructions after which the swizzle repeats
-    const bool piece_real = piece * 8 < a.head_dim, dense = a.head_dim == DP;
+    const bool dense = a.head_dim == DP;
     const uint32_t row_bytes = (uint32_t)(a.kv_heads * a.head_dim * 2);
     const char* const k_lane = reinterpret_cast<const char*>(a.k_cache) + (piece_real ? piece * 16 : 0);
     const int64_t k_to_v = reinterpret_cast<const char*>(a.v_cache) - reinterpret_cast<const char*>(a.k_cache);
@@ -333,29 +430,6 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
 #pragma unroll
     for (int i = 0; i < kLag + 2; ++i) hist_step[i] = kTile, hist_seg[i] = 0;
     bool ok = true;
-    // Values of the step's rows that are not finite: 0, and their rows noted.
-    auto check_values = [&](int step, int seg_no, int s) {
-      const int y = w * 32 + lane;
-      if (y < step) return;
-      unsigned char* row = ring + s * L::kSlot + y * 128;
-      bool any = false;
-#pragma unroll 4
-      for (int c = 0; c < kPieces; ++c) {
-        uint4* p = reinterpret_cast<uint4*>(row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (y & 7)) << 4));
-        uint4 v = *p;
-        uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-        bool hit = false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
-          if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0xffffu, hit = true;
-        }
-        if (hit) *p = v;
-        any |= hit;
-      }
-      if (any)
-        atomicOr(reinterpret_cast<unsigned long long*>(smem + L::kBad) + seg_no, 1ull << (y - step));
-    };
     // Unit `told` has arrived: the issuer may use it.  `back`: units issued behind it.
     auto tell = [&](int back) {
       const int s0 = told_slot, s1 = s0 + 1 == a.slots ? 0 : s0 + 1;
@@ -365,7 +439,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
         if (i == back) step = hist_step[i], seg_no = hist_seg[i];
       if (step < kTile) {
         __syncwarp();
-        check_values(step, seg_no, s1);
+        check_values(w * 32 + lane, step, seg_no, s1);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -389,6 +463,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
       }
       return wait(b, parity);
     };
+    int64_t edges = 0;        // units whose V went through an edge barrier
     bool first_run = true;
     for (int64_t u = 0; ok && u < count; ++u) {
       // this unit, then the next one's table entries
@@ -419,7 +494,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
         ++segment;
         if (w == 0 && lane == 0) bad[(segment + 7) & (kBadRing - 1)] = 0;  // all have read that one, none written
       }
-      const int64_t tile_at = (int64_t)req.lo + (int64_t)here_tile * kTile;
+      const int64_t tile_at = (int64_t)req.base + (int64_t)here_tile * kTile;
       const int step = (int)max((int64_t)-kTile, min((int64_t)kTile, (int64_t)req.ctx - tile_at));
 #pragma unroll
       for (int i = kLag + 1; i > 0; --i) hist_step[i] = hist_step[i - 1], hist_seg[i] = hist_seg[i - 1];
@@ -428,20 +503,43 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
       // describe it
       if (u >= kNotes) ok = wait(&note_free[u & (kNotes - 1)], (uint32_t)(u >> 3) - 1);
       if (!ok) break;
-      const uint32_t valid = __ballot_sync(kFull, here != kNowhere);
-      if (lane == 0) {
-        Note* n = &notes[u & (kNotes - 1)];
+      uint32_t valid = __ballot_sync(kFull, here != kNowhere);
+      // keys of the unit that are positions of the request
+      const int lo = (int)max((int64_t)0, (int64_t)req.lo - tile_at);
+      const int hi = (int)min((int64_t)kTile, (int64_t)req.hi - tile_at);
+      const bool check = kTma && (step < kTile || lo > 0 || hi % a.box != 0);
+      Note* n = &notes[u & (kNotes - 1)];
+      if constexpr (kTma) {
+        if (lane < 4) {  // word `lane`: its boxes' bits, spread over their keys
+          uint32_t word = 0;
+          if (a.box >= 32) {
+            if ((valid >> (32 * lane / a.box)) & 1u) word = kFull;
+          } else {
+            const int some = 32 / a.box;
+            for (int k = 0; k < some; ++k)
+              if ((valid >> (lane * some + k)) & 1u) word |= ((1u << a.box) - 1u) << (k * a.box);
+          }
+          const int from = lo - 32 * lane, to = hi - 32 * lane;
+          if (from > 0) word &= from < 32 ? kFull << from : 0u;
+          if (to < 32) word &= to > 0 ? (1u << to) - 1u : 0u;
+          n->valid[lane] = word;
+        }
+        __syncwarp();
+      } else if (lane == 0) {
         n->valid[w] = valid;
+      }
+      if (lane == 0) {
         if (w == 0) {
           n->r = here_r;
           n->seg = here_seg;
           n->step = step;
-          n->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (to_end ? kToEnd : 0);
+          // a segment that begins here and ends with another CTA: how far the join reaches
+          n->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (to_end ? kToEnd : 0) |
+                     (first && here_tile == 0 ? kFromStart : 0) | (check ? kEdge : 0);
           n->first = req.first;
           n->count = req.count;
           n->ctx = req.ctx;
-          // a segment that begins here and ends with another CTA: how far the join reaches
-          if (first && here_tile == 0) n->flags |= kFromStart;
+          n->seen = lo | hi << 8;
           const int64_t from = begin + u - here_tile;  // the segment's first unit
           if (u + 1 == count && !to_end && from >= begin)
             a.joins[blockIdx.x] = make_int4(here_r, here_seg, (int)((from + req.units - 1) / share), req.count);
@@ -449,26 +547,47 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
         mbar_arrive(&note_full[u & (kNotes - 1)]);
       }
       const int head = here_seg / a.passes;
+      auto two_on = [&](int& slot, uint32_t& turn) {
+        slot += 2;
+        if (slot >= a.slots) slot -= a.slots, ++turn;
+      };
+      if constexpr (kTma) {
+        ok = (k_turn == 0 || mbar_wait_role(&empty[k_slot], (k_turn - 1) & 1, abort)) &&
+             (v_turn == 0 || mbar_wait_role(&empty[v_slot], (v_turn - 1) & 1, abort));
+        ok = all(ok);
+        if (!ok) break;
+        uint64_t* const v_bar = check ? &edge[edges & (kNotes - 1)] : &full[v_slot];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[k_slot], L::kSlot);
+          mbar_arrive_expect_tx(v_bar, L::kSlot);
+          if (check) mbar_arrive(&full[v_slot]);  // its phases count the turns of the ring
+        }
+        edges += check;
+        __syncwarp();
+        // boxes of 64 channels: lanes take (K or V, channels, tokens) in turn; tokens that are nowhere read zeros
+        const int token_at = here == kNowhere ? -a.box : (int)here;
+        for (int i0 = 0; i0 < 2 * (DP / 64) * boxes; i0 += 32) {
+          const int i = i0 + lane, box = i & (boxes - 1), which = i / boxes;  // boxes: a power of two
+          const int c = which % (DP / 64);
+          const int z = __shfl_sync(kFull, token_at, box);
+          const bool is_v = which >= DP / 64;
+          if (which < 2 * (DP / 64))
+            tma_load_3d(ring + (is_v ? v_slot : k_slot) * L::kSlot + c * (kTile * 128) + box * a.box * 128,
+                      is_v ? &v_map : &k_map, 64 * c, head, z, is_v ? v_bar : &full[k_slot]);
+        }
+        two_on(k_slot, k_turn);
+        two_on(v_slot, v_turn);
+        __syncwarp();
+        continue;
+      }
       if (first && segment >= a.q_bufs)
         ok = wait_telling(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1, u);
       ok = ok && (k_turn == 0 || mbar_wait_role(&empty[k_slot], (k_turn - 1) & 1, abort)) &&
            (v_turn == 0 || mbar_wait_role(&empty[v_slot], (v_turn - 1) & 1, abort));
       ok = all(ok);
       if (!ok) break;
-      if (first) {  // Q with the segment's first unit
-        const int pass = here_seg - head * a.passes;
-        for (int t = 0; t < kRows; ++t) {
-          const int row0 = (pass * kRows + t) * kTile, left = req.count * a.group - row0;  // rows of this tile
-          const uint32_t q_at = smem_addr(q_smem) + ((int)(segment & q_odd) * kRows + t) * q_tile;
-          for (int y = w * kPer + sub; y < min(left, kTile); y += kCopiers * kPer) {
-            const int tok = (row0 + y) / a.group, g = row0 + y - tok * a.group;
-            const __nv_bfloat16* src = a.q + (int64_t)(req.first + tok) * a.q_stride +
-                                       (int64_t)(head * a.group + g) * a.head_dim + piece * 8;
-            copy16(q_at + (piece >> 3) * (a.q_rows * 128) + y * 128 + (((piece & 7) ^ (y & 7)) << 4),
-                   piece_real ? src : a.q, piece_real);
-          }
-        }
-      }
+      if (first)  // Q with the segment's first unit
+        copy_q(req.first, req.count, head, here_seg - head * a.passes, (int)(segment & q_odd), w, kCopiers);
       {
         const char* const src = k_lane + head * a.head_dim * 2;
         const uint32_t k_to = k_slot * L::kSlot, v_to = v_slot * L::kSlot;
@@ -493,10 +612,6 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
         }
       }
       copy_commit();
-      auto two_on = [&](int& slot, uint32_t& turn) {
-        slot += 2;
-        if (slot >= a.slots) slot -= a.slots, ++turn;
-      };
       two_on(k_slot, k_turn);
       two_on(v_slot, v_turn);
       if (u - told >= kLag) {
@@ -504,10 +619,17 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
         tell((int)(u - told));
       }
     }
-    copy_wait<0>();
-    const int64_t issued = count;
-    while (ok && told < issued) tell((int)(issued - 1 - told));
+    if constexpr (kTma) {
+      // slots in order of use: the next K slot says how far
+      turns = k_turn;
+      slots_used = k_slot;
+      edges_used = edges;
+    } else {
+      copy_wait<0>();
+      while (ok && told < count) tell((int)(count - 1 - told));
+    }
     report(a.err, err);
+    }
   } else if (warp >= kIssuer) {
     // ---------------------------------------------------------------- matrix instructions
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));  // the whole warpgroup
@@ -545,17 +667,23 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
           ++turn;
         }
       };
-      int64_t segment = -1;
+      int64_t segment = -1, edges = 0;
+      // V of a unit, through the warps that check it where it has values to check
+      auto wait_values = [&](uint64_t* b, uint32_t parity, bool check) {
+        if (!kTma || !check) return wait(b, parity);
+        ++edges;
+        return wait(&checked[(edges - 1) & (kNotes - 1)], (uint32_t)((edges - 1) >> 3));
+      };
       if constexpr (kRows == 1) {
         // unit u's scores, then unit u - 1's products with V
         int v_slot = 0;
         uint32_t v_turn = 0;
         int64_t v_segment = 0;
-        bool v_first = false;
+        bool v_first = false, v_check = false;
         auto products = [&](int64_t u) {
           const uint32_t d = tmem + 2 * kTile + (uint32_t)(v_segment & 1) * DP, p = tmem + (uint32_t)(u & 1) * kTile;
           if (v_first && v_segment >= 2 && !wait(&o_free[v_segment & 1], (uint32_t)(v_segment / 2 - 1))) return false;
-          if (!wait(&full[v_slot], v_turn)) return false;
+          if (!wait_values(&full[v_slot], v_turn, v_check)) return false;
           if (!wait(&p_full[2 * (u & 1)], (uint32_t)(u >> 1))) return false;
           tc_fence_after();
           values(d, p, v_slot, !v_first, 0);
@@ -572,6 +700,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
           if (!ok) break;
           if (n.flags & kFirst) ++segment;
           ok = wait(&full[slot], turn);
+          if (ok && kTma && (n.flags & kFirst)) ok = wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd));
           if (!ok) break;
           tc_fence_after();
           scores(tmem + (uint32_t)(u & 1) * kTile, q_base + (uint32_t)(segment & q_odd) * q_tile, slot);
@@ -584,6 +713,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
           v_turn = turn;
           v_segment = segment;
           v_first = n.flags & kFirst;
+          v_check = n.flags & kEdge;
           step();
         }
         if (ok && count > 0) ok = products(count - 1);
@@ -604,6 +734,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
           ++segment;
           two = rows_two(n);
           if (!wait(&full[slot], turn)) return false;
+          if (kTma && !wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd))) return false;
           tc_fence_after();
           const uint32_t q_at = q_base + (uint32_t)(segment & q_odd) * 2 * q_tile;
           for (int t = 0; t < (two ? 2 : 1); ++t) {
@@ -622,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
           const uint32_t v_turn = turn;
           const bool first = n.flags & kFirst, last = n.flags & kLast;
           step();
-          ok = wait(&full[v_slot], v_turn);
+          ok = wait_values(&full[v_slot], v_turn, n.flags & kEdge);
           if (!ok) break;
           Note next = n;
           if (!last) {
@@ -737,15 +868,23 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
 #pragma unroll
           for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[z + y]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        // One tile: the last unit's P V may still run (S of this one came behind the one before that; two
+        // tiles: behind the last one).  A barrier tells its last phase from the one before and no
+        // further, so it is looked at before this warp lets this unit's P V run: for the rescale,
+        // and ahead of the output's own wait.
+        if (kRows == 1 && u > 0 && (n.flags & kLast)) {
+          ok = wait(&o_full[0], (uint32_t)u - 1);
+          if (!ok) break;
+          tc_fence_after();
+        }
         if (n.flags & kFirst) {
           ref = top > -INFINITY ? top : kRefStart;
           part[0] = part[1] = 0;
         } else {
           const bool raise = mine && top > ref + kLazy;
           if (__any_sync(kFull, raise)) {
-            // one tile: the last unit's P V may still run (two: S of this unit came behind it)
-            if (kRows == 1) {
-              ok = wait(&o_full[0], (uint32_t)(u - 1));
+            if (kRows == 1 && !(n.flags & kLast)) {
+              ok = wait(&o_full[0], (uint32_t)u - 1);
               if (!ok) break;
               tc_fence_after();
             }
@@ -795,9 +934,7 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
           unpair(part[1], b0, b1);
           sum = (a0 + a1) + (b0 + b1);
         }
-        // a wait sees the last phase only: those before it in turn (S of this unit came behind u - 2's)
-        if (kRows == 1) ok = (u == 0 || wait(&o_full[0], (uint32_t)u - 1)) && wait(&o_full[0], (uint32_t)u);
-        else ok = wait(&o_full[t], segments);
+        ok = kRows == 1 ? wait(&o_full[0], (uint32_t)u) : wait(&o_full[t], segments);
         if (!ok) break;
         ++segments;
         tc_fence_after();
@@ -882,6 +1019,17 @@ __global__ void __launch_bounds__(kThreadsOf<kRows>, 1) attention_tree_kernel(co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (kTma && warp == kCopy && __any_sync(kFull, *abort != 0)) {
+    // where a wait ran out: the copies in flight end before the shared memory goes to another CTA
+    for (int i = 0; i < a.slots; ++i) {
+      const uint32_t uses = turns + (i < slots_used ? 1u : 0u);
+      if (uses > 0) mbar_wait_bounded(&full[i], (uses - 1) & 1);
+    }
+    for (int i = 0; i < kNotes; ++i) {
+      const int64_t uses = (edges_used >> 3) + (i < (edges_used & 7) ? 1 : 0);
+      if (uses > 0) mbar_wait_bounded(&edge[i], (uint32_t)(uses - 1) & 1);
+    }
+  }
   if (warp == kIssuer) {
     tmem_dealloc(tmem, 512);
     if (lane == 0 && *abort != 0 && a.err != nullptr) atomicOr(a.err, KV_ERR_TIMEOUT);
@@ -976,19 +1124,25 @@ Plan plan_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_
   return p;
 }
 
-template <int DP, int kRows>
-int launch(const TreeArgs& a, cudaStream_t stream) {
-  auto kernel = attention_tree_kernel<DP, kRows>;
+template <int DP, int kRows, bool kTma>
+int launch(const TreeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
+  auto kernel = attention_tree_kernel<DP, kRows, kTma>;
   const int q_bytes = (a.q_bufs * kRows * a.q_rows * DP * 2 + 1023) / 1024 * 1024;
   // Q's matrix instructions read whole tiles of 128 rows: the ring lies behind it
   const int smem = Smem<DP>::kHead + q_bytes + a.slots * Smem<DP>::kSlot;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return KV_ECUDA;
   const unsigned ctas = (unsigned)(a.gangs * a.gang);
-  const int rc = launch_pdl(kernel, ctas, kThreadsOf<kRows>, smem, stream, a);
+  const int rc = launch_pdl(kernel, ctas, kThreadsOf<kRows>, smem, stream, a, k_map, v_map);
   if (rc != KV_OK) return rc;
   const unsigned chunks = (unsigned)(a.part_rows + 15) / 16;
   return launch_pdl(join_tree_kernel<DP, kRows>, dim3(ctas, chunks), kJoinThreads, 0, stream, a);
+}
+
+template <int DP, int kRows>
+int launch(const TreeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
+  return a.box > 1 ? launch<DP, kRows, true>(a, k_map, v_map, stream)
+                   : launch<DP, kRows, false>(a, k_map, v_map, stream);
 }
 
 int sizes(int32_t num_reqs, int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads,
@@ -1064,6 +1218,15 @@ extern "C" int kv_attention_tree(const void* query, int64_t query_stride, const 
   if (over_input(out, out_bytes) || over_input(workspace, need) ||
       overlap(out, out_bytes, workspace, need))
     return KV_EINVAL;
+  // the largest box of 8, 16, .. tokens that never crosses a block
+  int box = 1;
+  if (block_size % 8 == 0)
+    for (box = 8; box < kTile && block_size % (2 * box) == 0;) box *= 2;
+  CUtensorMap k_map = {}, v_map = {};
+  const int64_t tokens = num_blocks * block_size, kv_row = (int64_t)num_kv_heads * head_dim;
+  if (box > 1 && (!rows_map(&k_map, k_layer, kv_row, tokens, num_kv_heads, head_dim, 1, box) ||
+                  !rows_map(&v_map, v_layer, kv_row, tokens, num_kv_heads, head_dim, 1, box)))
+    return KV_ECUDA;
   const Plan p = plan_of(max_rows, num_q_heads, num_kv_heads, head_dim);
   const TreeArgs a{static_cast<const __nv_bfloat16*>(query), query_stride,
                    reinterpret_cast<const __nv_bfloat16*>(k_layer),
@@ -1073,8 +1236,9 @@ extern "C" int kv_attention_tree(const void* query, int64_t query_stride, const 
                    context_len, tree_mask, num_reqs, num_rows, max_rows,
                    fminf(scale * 1.44269504088896340736f, FLT_MAX),
                    static_cast<__nv_bfloat16*>(out), d_err, p.passes, p.gang, p.gangs, p.part_rows,
-                   p.q_rows, p.q_bufs, p.slots, p.warps, static_cast<int4*>(workspace),
+                   p.q_rows, p.q_bufs, p.slots, box, p.warps, static_cast<int4*>(workspace),
                    reinterpret_cast<float*>(static_cast<char*>(workspace) + p.joins_bytes())};
-  if (p.dp == 64) return p.rows == 1 ? launch<64, 1>(a, stream) : launch<64, 2>(a, stream);
-  return p.rows == 1 ? launch<128, 1>(a, stream) : launch<128, 2>(a, stream);
+  if (p.dp == 64)
+    return p.rows == 1 ? launch<64, 1>(a, k_map, v_map, stream) : launch<64, 2>(a, k_map, v_map, stream);
+  return p.rows == 1 ? launch<128, 1>(a, k_map, v_map, stream) : launch<128, 2>(a, k_map, v_map, stream);
 }

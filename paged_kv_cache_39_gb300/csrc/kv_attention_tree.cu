@@ -45,7 +45,7 @@ namespace {
 
 constexpr int kTile = 128;             // keys of a unit, rows of a tile
 constexpr int kCopiers = 4;            // warps, where they copy; where TMA does:
-constexpr int kHelpers = 3;            // that load Q and check values, beside the one that issues copies
+constexpr int kReaders = 3;            // that read what the first one describes: K's copies, V's, Q and checks
 constexpr int kNotes = 8;              // units described ahead (a power of two: 2^3)
 constexpr int kBadRing = 16;           // segments whose values are noted
 constexpr float kLazy = 8.0f;          // log2 of the most a weight may pass the reference
@@ -111,18 +111,24 @@ __device__ __forceinline__ Req request(const TreeArgs& a, int r, uint32_t& err) 
   return q;
 }
 
-// What the copiers tell the others about a unit.
+// What the copiers tell the others about a unit, and, with a segment's first unit here, about the
+// segment.
 struct __align__(16) Note {
-  uint32_t valid[4];       // keys that some row may see, a warp of copiers a word
-  int32_t r, seg;
+  uint32_t valid[4];       // keys that some row may see
   int32_t step;            // the step's row 0 is key `step` of the unit
   int32_t flags;
+  int32_t head;
+  int32_t seen;            // keys [seen & 255, seen >> 8) of the unit are positions of the request
+  int32_t tokens[16];      // kTma: each box's first token in the pool, < 0: none
+};
+struct __align__(16) SegNote {
+  int32_t r, head, pass;
   int32_t first, count;    // the request's rows
   uint32_t ctx;
-  int32_t seen;            // keys [seen & 255, seen >> 8) of the unit are positions of the request
+  int32_t pad[2];
 };
-// of this CTA's share; of the segment; kEdge: values to check (loaded by TMA)
-enum Flags { kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8, kEdge = 16 };
+// of this CTA's share; of the segment; values to check (kTma); more rows than a tile in this pass
+enum Flags { kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8, kEdge = 16, kTwo = 32 };
 
 constexpr int kNumBars = 2 * 12 + 2 * kNotes + 2 + 4 + 2 + 2 + 2 + 1 + 2 + 2 * kNotes;
 template <int DP>
@@ -130,7 +136,8 @@ struct Smem {
   static constexpr int kSlot = kTile * DP * 2;
   static constexpr int kBars = 0;
   static constexpr int kNote = (kNumBars * 8 + 15) / 16 * 16;
-  static constexpr int kBad = kNote + kNotes * (int)sizeof(Note);
+  static constexpr int kSegNote = kNote + kNotes * (int)sizeof(Note);
+  static constexpr int kBad = kSegNote + kNotes * (int)sizeof(SegNote);
   static constexpr int kMisc = kBad + kBadRing * 8;
   static constexpr int kScan = kMisc + 16;                              // int64_t[17]: units by warp, all
   static constexpr int kHead = (kScan + 17 * 8 + 1023) / 1024 * 1024;   // Q, then the ring
@@ -181,6 +188,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
   uint64_t* edge = q_full + 2;              // kTma: V of units whose values are checked, in turn: arrived,
   uint64_t* checked = edge + kNotes;        // and checked
   Note* notes = reinterpret_cast<Note*>(smem + L::kNote);
+  SegNote* seg_notes = reinterpret_cast<SegNote*>(smem + L::kSegNote);  // by segment & (kNotes - 1)
   volatile uint64_t* bad = reinterpret_cast<uint64_t*>(smem + L::kBad);
   int* misc = reinterpret_cast<int*>(smem + L::kMisc);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(misc);
@@ -197,8 +205,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     int count = 1;
     if (b < empty) count = kTma ? 1 : kCopiers;
     if (b >= note_full && b < note_free) count = kTma ? 1 : kCopiers;
-    if (b >= note_free && b < s_full) count = kRows * a.warps + 1 + (kTma ? kHelpers : 0);
-    if ((b >= q_full && b < edge) || b >= checked) count = kHelpers;
+    if (b >= note_free && b < s_full) count = kRows * a.warps + 1 + (kTma ? kReaders : 0);
     if (b >= p_full && b < o_full) count = a.warps;
     if (b >= o_free && b < q_free) count = a.warps;
     mbar_init(&bars[tid], count);
@@ -239,19 +246,14 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
   const int64_t begin = my_gang * share;
   const int64_t count = my_gang < a.gangs && begin < total ? min(share, total - begin) : 0;
 
-  // what the issuing copier leaves behind: the ring's slots and edge barriers in use
-  uint32_t turns = 0;
-  int slots_used = 0;
-  int64_t edges_used = 0;
+  int64_t issued = 0, edges_used = 0;        // copying warps (kTma): units, of them through edge barriers
   auto all = [](bool ok) { return __all_sync(kFull, ok) != 0; };
   auto wait = [&](uint64_t* b, uint32_t parity) { return all(mbar_wait_role(b, parity & 1, abort)); };
-  // a reader's next note; its lanes have all of it
-  auto read_note = [&](int64_t u, Note& n) {
-    if (!wait(&note_full[u & (kNotes - 1)], (uint32_t)(u >> 3))) return false;
-    n = notes[u & (kNotes - 1)];
+  // A reader waits for its next note, reads what it wants of it and gives it back.
+  auto note_there = [&](int64_t u) { return wait(&note_full[u & (kNotes - 1)], (uint32_t)(u >> 3)); };
+  auto note_done = [&](int64_t u) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&note_free[u & (kNotes - 1)]);
-    return true;
   };
 
   if (warp >= kCopy) {
@@ -321,275 +323,291 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         }
       }
     };
-    if (kTma && w > 0) {
+    if (kTma && w == 3) {
       // -------------------------------------------------------------- Q, and values at the edges
       int64_t segment = -1, edges = 0;
       int slot = 1;              // V of the unit
       for (int64_t u = 0; u < count; ++u) {
-        Note n;
-        if (!read_note(u, n)) break;
-        const int head = n.seg / a.passes;
-        if (n.flags & kFirst) {
-          ++segment;
+        if (!note_there(u)) break;
+        const Note& n = notes[u & (kNotes - 1)];
+        const int flags = n.flags, step = n.step, from = n.seen & 255, to = n.seen >> 8;
+        if (flags & kFirst) ++segment;
+        const SegNote g = seg_notes[segment & (kNotes - 1)];
+        note_done(u);
+        if (flags & kFirst) {
           if (segment >= a.q_bufs && !wait(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1)) break;
-          copy_q(n.first, n.count, head, n.seg - head * a.passes, (int)(segment & q_odd), w - 1, kHelpers);
+          copy_q(g.first, g.count, g.head, g.pass, (int)(segment & q_odd), 0, 1);
           copy_commit();
           copy_wait<0>();
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_full[segment & q_odd]);
         }
-        if (n.flags & kEdge) {
+        if (flags & kEdge) {
           if (!wait(&edge[edges & (kNotes - 1)], (uint32_t)(edges >> 3))) break;
-          ++edges;
-          for (int y = (w - 1) * 32 + lane; y < kTile; y += kHelpers * 32) {
-            if (y < (n.seen & 255) || y >= n.seen >> 8) {  // of the block, but not of the request
+          for (int y = lane; y < kTile; y += 32) {
+            if (y < from || y >= to) {  // of the block, but not of the request
 #pragma unroll
-              for (int c = 0; c < DP / 64; ++c)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  *reinterpret_cast<uint4*>(ring + slot * L::kSlot + c * (kTile * 128) + y * 128 +
-                                            ((k ^ (y & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+              for (int c = 0; c < kPieces; ++c)
+                *reinterpret_cast<uint4*>(ring + slot * L::kSlot + (c >> 3) * (kTile * 128) + y * 128 +
+                                          (((c & 7) ^ (y & 7)) << 4)) = make_uint4(0, 0, 0, 0);
             } else {
-              check_values(y, n.step, (int)(segment & (kBadRing - 1)), slot);
+              check_values(y, step, (int)(segment & (kBadRing - 1)), slot);
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&checked[(edges - 1) & (kNotes - 1)]);
+          if (lane == 0) mbar_arrive(&checked[edges & (kNotes - 1)]);
+          ++edges;
         }
         slot += 2;
         if (slot >= a.slots) slot -= a.slots;
       }
-    } else {
-    // ---------------------------------------------------------------- units, in order
-    // 32 requests at a time, one a lane
-    int base = r;
-    Req mine = {};
-    auto look = [&]() {
-      uint32_t ignore = 0;
-      mine = Req{0, 0, 0, 0, 0, 0, 0};
-      if (base + lane < a.num_reqs) mine = request(a, base + lane, ignore);
-    };
-    Req now;
-    auto take = [&]() {
-      now.first = __shfl_sync(kFull, mine.first, r - base);
-      now.count = __shfl_sync(kFull, mine.count, r - base);
-      now.lo = __shfl_sync(kFull, mine.lo, r - base);
-      now.hi = __shfl_sync(kFull, mine.hi, r - base);
-      now.ctx = __shfl_sync(kFull, mine.ctx, r - base);
-      now.base = __shfl_sync(kFull, mine.base, r - base);
-      now.units = __shfl_sync(kFull, mine.units, r - base);
-    };
-    // This lane's row (kTma: box) of a unit, in two steps, so that its table entry arrives while the unit
-    // before it is copied: block and offset, then the token's number in the pool (kNowhere: none).
-    const int boxes = kTile / a.box;
-    constexpr uint32_t kNowhere = ~0u;
-    int32_t next_block = kNull;
-    uint32_t next_off = 0;
-    auto look_up = [&]() {
-      const uint32_t p = now.base + (uint32_t)tile * kTile + (kTma ? lane * a.box : w * 32 + lane);
-      next_block = kNull;
-      if (p < now.hi && (!kTma || lane < boxes)) {
-        int64_t lb, off;
-        a.div.divmod((int64_t)p, lb, off);
-        next_off = (uint32_t)off;
-        next_block = a.table[(int64_t)r * a.stride + lb];
-      }
-    };
-    auto token = [&]() {
-      if (next_block == kNull) return kNowhere;
-      if (next_block < 0 || next_block >= a.num_blocks) {
-        err |= KV_ERR_BAD_BLOCK;
-        return kNowhere;
-      }
-      return (uint32_t)next_block * (uint32_t)a.div.size + next_off;
-    };
-    if (count > 0) {
-      look();
-      take();
-      look_up();
-    }
-    constexpr int kTurns = 8 / kPer;        // instructions after which the swizzle repeats
-    const bool dense = a.head_dim == DP;
-    const uint32_t row_bytes = (uint32_t)(a.kv_heads * a.head_dim * 2);
-    const char* const k_lane = reinterpret_cast<const char*>(a.k_cache) + (piece_real ? piece * 16 : 0);
-    const int64_t k_to_v = reinterpret_cast<const char*>(a.v_cache) - reinterpret_cast<const char*>(a.k_cache);
-    // rows w * 32 + i * kPer + sub: their 8-row groups are 1024 bytes, column blocks of 64 channels apart
-    uint32_t dst_lane[kTurns];
-#pragma unroll
-    for (int i = 0; i < kTurns; ++i)
-      dst_lane[i] = smem_addr(ring) + (uint32_t)((w * 32 + i * kPer + sub) * 128 + (piece >> 3) * (kTile * 128) +
-                                                 (((piece & 7) ^ (i * kPer + sub)) << 4));
-
-    int64_t told = 0;         // units that the issuer may use
-    int k_slot = 0, v_slot = 1, told_slot = 0;
-    uint32_t k_turn = 0, v_turn = 0;
-    int64_t segment = -1;     // of this CTA, counted
-    int hist_step[kLag + 2], hist_seg[kLag + 2];  // of the last units: where the step's rows begin
-#pragma unroll
-    for (int i = 0; i < kLag + 2; ++i) hist_step[i] = kTile, hist_seg[i] = 0;
-    bool ok = true;
-    // Unit `told` has arrived: the issuer may use it.  `back`: units issued behind it.
-    auto tell = [&](int back) {
-      const int s0 = told_slot, s1 = s0 + 1 == a.slots ? 0 : s0 + 1;
-      int step = kTile, seg_no = 0;
-#pragma unroll
-      for (int i = 0; i < kLag + 2; ++i)
-        if (i == back) step = hist_step[i], seg_no = hist_seg[i];
-      if (step < kTile) {
+    } else if (kTma && w > 0) {
+      // -------------------------------------------------------------- copies of K (1) or V (2)
+      const bool is_v = w == 2, leader = elect_one();
+      const CUtensorMap* const map = is_v ? &v_map : &k_map;
+      if (leader) tma_prefetch_map(map);
+      const int boxes = kTile / a.box, box_bytes = a.box * 128;
+      int slot = is_v ? 1 : 0;
+      uint32_t turn = 0;
+      for (int64_t u = 0; u < count; ++u) {
+        if (!note_there(u)) break;
+        const Note& n = notes[u & (kNotes - 1)];
+        const int flags = n.flags, head = n.head, token = n.tokens[lane & 15];
+        note_done(u);
+        if (turn > 0 && !wait(&empty[slot], turn - 1)) break;
+        const bool check = is_v && (flags & kEdge);
+        uint64_t* const bar = check ? &edge[edges_used & (kNotes - 1)] : &full[slot];
+        unsigned char* const to = ring + slot * L::kSlot;
+        if (leader) {
+          mbar_arrive_expect_tx(bar, L::kSlot);
+          if (check) mbar_arrive(&full[slot]);  // its phases count the turns of the ring
+        }
         __syncwarp();
-        check_values(w * 32 + lane, step, seg_no, s1);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&full[s0]);
-        mbar_arrive(&full[s1]);
-      }
-      ++told;
-      told_slot = s1 + 1 == a.slots ? 0 : s1 + 1;
-    };
-    // The issuer may need units in flight to get to the end of a wait of this role: the oldest ones
-    // are told about until it is over.  `issued`: units whose copies are under way or done.
-    auto wait_telling = [&](uint64_t* b, uint32_t parity, int64_t issued) {
-      while (told < issued && !__any_sync(kFull, mbar_try_wait(b, parity & 1))) {
-        const int back = (int)(issued - 1 - told);  // groups behind the oldest, kLag at most
-        if (back == 0) copy_wait<0>();
-        else if (back == 1) copy_wait<1>();
-        else if (back == 2) copy_wait<2>();
-        else copy_wait<3>();
-        tell(back + 1);  // the next unit is in the history already
-      }
-      return wait(b, parity);
-    };
-    int64_t edges = 0;        // units whose V went through an edge barrier
-    bool first_run = true;
-    for (int64_t u = 0; ok && u < count; ++u) {
-      // this unit, then the next one's table entries
-      const uint32_t here = token();
-      const Req req = now;
-      const int here_r = r, here_seg = seg, here_tile = tile;
-      const bool first = first_run || tile == 0;
-      first_run = false;
-      const bool to_end = tile + 1 == now.units, last = to_end || u + 1 == count;
-      if (u + 1 < count) {
-        if (++tile == now.units) {
-          tile = 0;
-          seg += a.gang;
-          if (seg >= segs) {
-            seg = member;
-            do {
-              if (++r >= base + 32) {
-                base = r;
-                look();
-              }
-            } while (__shfl_sync(kFull, mine.units, r - base) == 0);
-            take();
+#pragma unroll 4
+        for (int i = 0; i < boxes; ++i) {
+          const int z = __shfl_sync(kFull, token, i);  // a box that is nowhere reads zeros
+          if (leader) {
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c)
+              tma_load_3d(to + c * (kTile * 128) + i * box_bytes, map, 64 * c, head, z, bar);
           }
         }
+        edges_used += check;
+        ++issued;
+        slot += 2;
+        if (slot >= a.slots) slot -= a.slots, ++turn;
+      }
+    } else {
+      // -------------------------------------------------------------- units, in order
+      // 32 requests at a time, one a lane
+      int base = r;
+      Req mine = {};
+      auto look = [&]() {
+        uint32_t ignore = 0;
+        mine = Req{0, 0, 0, 0, 0, 0, 0};
+        if (base + lane < a.num_reqs) mine = request(a, base + lane, ignore);
+      };
+      Req now = {};
+      // of the unit: where it is in the request, its first position and table row
+      uint32_t pos = 0;
+      const int32_t* row = nullptr;
+      auto take = [&]() {
+        now.first = __shfl_sync(kFull, mine.first, r - base);
+        now.count = __shfl_sync(kFull, mine.count, r - base);
+        now.lo = __shfl_sync(kFull, mine.lo, r - base);
+        now.hi = __shfl_sync(kFull, mine.hi, r - base);
+        now.ctx = __shfl_sync(kFull, mine.ctx, r - base);
+        now.base = __shfl_sync(kFull, mine.base, r - base);
+        now.units = __shfl_sync(kFull, mine.units, r - base);
+        row = a.table + (int64_t)r * a.stride;
+      };
+      // This lane's row (kTma: box) of a unit, in two steps, so that its table entry arrives while the
+      // unit before it is dealt with: block and offset, then the token in the pool (kNowhere: none).
+      constexpr uint32_t kNowhere = ~0u;
+      const int boxes = kTile / a.box;
+      const uint32_t lane_at = kTma ? lane * a.box : w * 32 + lane;
+      const uint32_t T = (uint32_t)a.div.size;
+      int32_t next_block = kNull;
+      uint32_t next_off = 0;
+      auto look_up = [&]() {
+        const uint32_t p = pos + lane_at;
+        next_block = kNull;
+        if (p < now.hi && (!kTma || lane < boxes)) {
+          const uint32_t lb = a.div.shift >= 0 ? p >> a.div.shift : p / T;
+          next_off = p - lb * T;
+          next_block = row[lb];
+        }
+      };
+      auto token = [&]() {
+        if (next_block == kNull) return kNowhere;
+        if (next_block < 0 || next_block >= a.num_blocks) {
+          err |= KV_ERR_BAD_BLOCK;
+          return kNowhere;
+        }
+        return (uint32_t)next_block * T + next_off;
+      };
+      if (count > 0) {
+        look();
+        take();
+        pos = now.base + (uint32_t)tile * kTile;
         look_up();
       }
-      if (first) {
-        ++segment;
-        if (w == 0 && lane == 0) bad[(segment + 7) & (kBadRing - 1)] = 0;  // all have read that one, none written
-      }
-      const int64_t tile_at = (int64_t)req.base + (int64_t)here_tile * kTile;
-      const int step = (int)max((int64_t)-kTile, min((int64_t)kTile, (int64_t)req.ctx - tile_at));
+      constexpr int kTurns = 8 / kPer;        // copy instructions after which the swizzle repeats
+      const bool dense = a.head_dim == DP;
+      const uint32_t row_bytes = (uint32_t)(a.kv_heads * a.head_dim * 2);
+      const char* const k_lane = reinterpret_cast<const char*>(a.k_cache) + (piece_real ? piece * 16 : 0);
+      const int64_t k_to_v = reinterpret_cast<const char*>(a.v_cache) - reinterpret_cast<const char*>(a.k_cache);
+      // rows w * 32 + i * kPer + sub: their 8-row groups are 1024 bytes, column blocks of 64 channels apart
+      uint32_t dst_lane[kTurns];
 #pragma unroll
-      for (int i = kLag + 1; i > 0; --i) hist_step[i] = hist_step[i - 1], hist_seg[i] = hist_seg[i - 1];
-      hist_step[0] = step;
-      hist_seg[0] = (int)(segment & (kBadRing - 1));
-      // describe it
-      if (u >= kNotes) ok = wait(&note_free[u & (kNotes - 1)], (uint32_t)(u >> 3) - 1);
-      if (!ok) break;
-      uint32_t valid = __ballot_sync(kFull, here != kNowhere);
-      // keys of the unit that are positions of the request
-      const int lo = (int)max((int64_t)0, (int64_t)req.lo - tile_at);
-      const int hi = (int)min((int64_t)kTile, (int64_t)req.hi - tile_at);
-      const bool check = kTma && (step < kTile || lo > 0 || hi % a.box != 0);
-      Note* n = &notes[u & (kNotes - 1)];
-      if constexpr (kTma) {
-        if (lane < 4) {  // word `lane`: its boxes' bits, spread over their keys
+      for (int i = 0; i < kTurns; ++i)
+        dst_lane[i] = smem_addr(ring) + (uint32_t)((w * 32 + i * kPer + sub) * 128 + (piece >> 3) * (kTile * 128) +
+                                                   (((piece & 7) ^ (i * kPer + sub)) << 4));
+
+      int64_t told = 0;         // units that the issuer may use
+      int k_slot = 0, v_slot = 1, told_slot = 0;
+      uint32_t k_turn = 0, v_turn = 0;
+      int64_t segment = -1;     // of this CTA, counted
+      int hist_step[kLag + 2], hist_seg[kLag + 2];  // of the last units: where the step's rows begin
+#pragma unroll
+      for (int i = 0; i < kLag + 2; ++i) hist_step[i] = kTile, hist_seg[i] = 0;
+      bool ok = true;
+      // Unit `told` has arrived: the issuer may use it.  `back`: units issued behind it.
+      auto tell = [&](int back) {
+        const int s0 = told_slot, s1 = s0 + 1 == a.slots ? 0 : s0 + 1;
+        int step = kTile, seg_no = 0;
+#pragma unroll
+        for (int i = 0; i < kLag + 2; ++i)
+          if (i == back) step = hist_step[i], seg_no = hist_seg[i];
+        if (step < kTile) {
+          __syncwarp();
+          check_values(w * 32 + lane, step, seg_no, s1);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[s0]);
+          mbar_arrive(&full[s1]);
+        }
+        ++told;
+        told_slot = s1 + 1 == a.slots ? 0 : s1 + 1;
+      };
+      // The issuer may need units in flight to get to the end of a wait of this role: the oldest ones
+      // are told about until it is over.  `so_far`: units whose copies are under way or done.
+      auto wait_telling = [&](uint64_t* b, uint32_t parity, int64_t so_far) {
+        while (told < so_far && !__any_sync(kFull, mbar_try_wait(b, parity & 1))) {
+          const int back = (int)(so_far - 1 - told);  // groups behind the oldest, kLag at most
+          if (back == 0) copy_wait<0>();
+          else if (back == 1) copy_wait<1>();
+          else if (back == 2) copy_wait<2>();
+          else copy_wait<3>();
+          tell(back + 1);  // the next unit is in the history already
+        }
+        return wait(b, parity);
+      };
+      int head = seg / a.passes;
+      for (int64_t u = 0; ok && u < count; ++u) {
+        // this unit
+        const uint32_t here = token();
+        const bool first = u == 0 || tile == 0, from_start = tile == 0;
+        const bool to_end = tile + 1 == now.units, last = to_end || u + 1 == count;
+        const int step = max(-kTile, min(kTile, (int)(now.ctx - pos)));
+        const int lo = from_start ? (int)(now.lo - pos) : 0;  // its keys [lo, hi) are positions of the request
+        const int hi = (int)min((uint32_t)kTile, now.hi - pos);
+        const Req req = now;
+        const int here_r = r, here_head = head, here_pass = seg - head * a.passes;
+        if (last && !to_end) {  // a segment that begins here and ends with another CTA: how far the join reaches
+          const int64_t from = begin + u - tile;  // the segment's first unit
+          if (w == 0 && lane == 0 && from >= begin)
+            a.joins[blockIdx.x] = make_int4(r, seg, (int)((from + now.units - 1) / share), now.count);
+        }
+        // the next one, and its table entries
+        if (u + 1 < count) {
+          pos += kTile;
+          if (++tile == now.units) {
+            tile = 0;
+            seg += a.gang;
+            if (seg >= segs) {
+              seg = member;
+              do {
+                if (++r >= base + 32) {
+                  base = r;
+                  look();
+                }
+              } while (__shfl_sync(kFull, mine.units, r - base) == 0);
+              take();
+            }
+            head = seg / a.passes;
+            pos = now.base;
+          }
+          look_up();
+        }
+        if (first) ++segment;
+        if constexpr (!kTma) {
+#pragma unroll
+          for (int i = kLag + 1; i > 0; --i) hist_step[i] = hist_step[i - 1], hist_seg[i] = hist_seg[i - 1];
+          hist_step[0] = step;
+          hist_seg[0] = (int)(segment & (kBadRing - 1));
+        }
+        // describe it
+        if (u >= kNotes) ok = wait(&note_free[u & (kNotes - 1)], (uint32_t)(u >> 3) - 1);
+        if (!ok) break;
+        uint32_t valid = __ballot_sync(kFull, here != kNowhere);
+        Note& n = notes[u & (kNotes - 1)];
+        if constexpr (kTma) {
+          if (lane < boxes) n.tokens[lane] = here == kNowhere ? -a.box : (int)here;
+          // word `lane`: its boxes' bits, spread over their keys
           uint32_t word = 0;
           if (a.box >= 32) {
-            if ((valid >> (32 * lane / a.box)) & 1u) word = kFull;
+            if ((valid >> (32 * lane / a.box & 31)) & 1u) word = kFull;
           } else {
             const int some = 32 / a.box;
-            for (int k = 0; k < some; ++k)
-              if ((valid >> (lane * some + k)) & 1u) word |= ((1u << a.box) - 1u) << (k * a.box);
+            const uint32_t ones = (1u << a.box) - 1u;
+            valid >>= lane * some & 31;
+            word = (valid & 1u ? ones : 0u) | (valid & 2u ? ones << a.box : 0u);
+            if (some == 4) word |= (valid & 4u ? ones << 16 : 0u) | (valid & 8u ? ones << 24 : 0u);
           }
           const int from = lo - 32 * lane, to = hi - 32 * lane;
           if (from > 0) word &= from < 32 ? kFull << from : 0u;
           if (to < 32) word &= to > 0 ? (1u << to) - 1u : 0u;
-          n->valid[lane] = word;
+          if (lane < 4) n.valid[lane] = word;
+        } else if (lane == 0) {
+          n.valid[w] = valid;
+        }
+        if (w == 0 && lane == 0) {
+          n.step = step;
+          n.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (to_end ? kToEnd : 0) |
+                    (first && from_start ? kFromStart : 0) |
+                    (kTma && (step < kTile || lo > 0 || hi % a.box != 0) ? kEdge : 0) |
+                    (req.count * a.group > (here_pass * kRows + 1) * kTile ? kTwo : 0);
+          n.head = here_head;
+          n.seen = lo | hi << 8;
+          if (first) {
+            SegNote& g = seg_notes[segment & (kNotes - 1)];
+            g.r = here_r;
+            g.head = here_head;
+            g.pass = here_pass;
+            g.first = req.first;
+            g.count = req.count;
+            g.ctx = req.ctx;
+            bad[(segment + 7) & (kBadRing - 1)] = 0;  // all have read that one, none written
+          }
         }
         __syncwarp();
-      } else if (lane == 0) {
-        n->valid[w] = valid;
-      }
-      if (lane == 0) {
-        if (w == 0) {
-          n->r = here_r;
-          n->seg = here_seg;
-          n->step = step;
-          // a segment that begins here and ends with another CTA: how far the join reaches
-          n->flags = (first ? kFirst : 0) | (last ? kLast : 0) | (to_end ? kToEnd : 0) |
-                     (first && here_tile == 0 ? kFromStart : 0) | (check ? kEdge : 0);
-          n->first = req.first;
-          n->count = req.count;
-          n->ctx = req.ctx;
-          n->seen = lo | hi << 8;
-          const int64_t from = begin + u - here_tile;  // the segment's first unit
-          if (u + 1 == count && !to_end && from >= begin)
-            a.joins[blockIdx.x] = make_int4(here_r, here_seg, (int)((from + req.units - 1) / share), req.count);
-        }
-        mbar_arrive(&note_full[u & (kNotes - 1)]);
-      }
-      const int head = here_seg / a.passes;
-      auto two_on = [&](int& slot, uint32_t& turn) {
-        slot += 2;
-        if (slot >= a.slots) slot -= a.slots, ++turn;
-      };
-      if constexpr (kTma) {
-        ok = (k_turn == 0 || mbar_wait_role(&empty[k_slot], (k_turn - 1) & 1, abort)) &&
+        if (lane == 0) mbar_arrive(&note_full[u & (kNotes - 1)]);
+        if constexpr (kTma) continue;
+        // copy it
+        if (first && segment >= a.q_bufs)
+          ok = wait_telling(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1, u);
+        ok = ok && (k_turn == 0 || mbar_wait_role(&empty[k_slot], (k_turn - 1) & 1, abort)) &&
              (v_turn == 0 || mbar_wait_role(&empty[v_slot], (v_turn - 1) & 1, abort));
         ok = all(ok);
         if (!ok) break;
-        uint64_t* const v_bar = check ? &edge[edges & (kNotes - 1)] : &full[v_slot];
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[k_slot], L::kSlot);
-          mbar_arrive_expect_tx(v_bar, L::kSlot);
-          if (check) mbar_arrive(&full[v_slot]);  // its phases count the turns of the ring
-        }
-        edges += check;
-        __syncwarp();
-        // boxes of 64 channels: lanes take (K or V, channels, tokens) in turn; tokens that are nowhere read zeros
-        const int token_at = here == kNowhere ? -a.box : (int)here;
-        for (int i0 = 0; i0 < 2 * (DP / 64) * boxes; i0 += 32) {
-          const int i = i0 + lane, box = i & (boxes - 1), which = i / boxes;  // boxes: a power of two
-          const int c = which % (DP / 64);
-          const int z = __shfl_sync(kFull, token_at, box);
-          const bool is_v = which >= DP / 64;
-          if (which < 2 * (DP / 64))
-            tma_load_3d(ring + (is_v ? v_slot : k_slot) * L::kSlot + c * (kTile * 128) + box * a.box * 128,
-                      is_v ? &v_map : &k_map, 64 * c, head, z, is_v ? v_bar : &full[k_slot]);
-        }
-        two_on(k_slot, k_turn);
-        two_on(v_slot, v_turn);
-        __syncwarp();
-        continue;
-      }
-      if (first && segment >= a.q_bufs)
-        ok = wait_telling(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1, u);
-      ok = ok && (k_turn == 0 || mbar_wait_role(&empty[k_slot], (k_turn - 1) & 1, abort)) &&
-           (v_turn == 0 || mbar_wait_role(&empty[v_slot], (v_turn - 1) & 1, abort));
-      ok = all(ok);
-      if (!ok) break;
-      if (first)  // Q with the segment's first unit
-        copy_q(req.first, req.count, head, here_seg - head * a.passes, (int)(segment & q_odd), w, kCopiers);
-      {
-        const char* const src = k_lane + head * a.head_dim * 2;
+        if (first)  // Q with the segment's first unit
+          copy_q(req.first, req.count, here_head, here_pass, (int)(segment & q_odd), w, kCopiers);
+        const char* const src = k_lane + here_head * a.head_dim * 2;
         const uint32_t k_to = k_slot * L::kSlot, v_to = v_slot * L::kSlot;
         if (valid == kFull && dense) {
 #pragma unroll
@@ -610,26 +628,22 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             copy16(to + v_to, p + k_to_v, real);
           }
         }
+        copy_commit();
+        k_slot += 2;
+        if (k_slot >= a.slots) k_slot -= a.slots, ++k_turn;
+        v_slot += 2;
+        if (v_slot >= a.slots) v_slot -= a.slots, ++v_turn;
+        if (u - told >= kLag) {
+          copy_wait<kLag>();
+          tell((int)(u - told));
+        }
       }
-      copy_commit();
-      two_on(k_slot, k_turn);
-      two_on(v_slot, v_turn);
-      if (u - told >= kLag) {
-        copy_wait<kLag>();
-        tell((int)(u - told));
+      if constexpr (!kTma) {
+        copy_wait<0>();
+        while (ok && told < count) tell((int)(count - 1 - told));
       }
-    }
-    if constexpr (kTma) {
-      // slots in order of use: the next K slot says how far
-      turns = k_turn;
-      slots_used = k_slot;
-      edges_used = edges;
-    } else {
-      copy_wait<0>();
-      while (ok && told < count) tell((int)(count - 1 - told));
     }
     report(a.err, err);
-    }
   } else if (warp >= kIssuer) {
     // ---------------------------------------------------------------- matrix instructions
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));  // the whole warpgroup
@@ -695,44 +709,41 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           return true;
         };
         for (int64_t u = 0; ok && u < count; ++u) {
-          Note n;
-          ok = read_note(u, n);
+          ok = note_there(u);
           if (!ok) break;
-          if (n.flags & kFirst) ++segment;
+          const int flags = notes[u & (kNotes - 1)].flags;
+          note_done(u);
+          if (flags & kFirst) ++segment;
           ok = wait(&full[slot], turn);
-          if (ok && kTma && (n.flags & kFirst)) ok = wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd));
+          if (ok && kTma && (flags & kFirst)) ok = wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd));
           if (!ok) break;
           tc_fence_after();
           scores(tmem + (uint32_t)(u & 1) * kTile, q_base + (uint32_t)(segment & q_odd) * q_tile, slot);
           commit(&s_full[u & 1]);
           commit(&empty[slot]);
-          if (n.flags & kLast) commit(&q_free[segment & q_odd]);
+          if (flags & kLast) commit(&q_free[segment & q_odd]);
           step();
           if (u > 0) ok = products(u - 1);
           v_slot = slot;
           v_turn = turn;
           v_segment = segment;
-          v_first = n.flags & kFirst;
-          v_check = n.flags & kEdge;
+          v_first = flags & kFirst;
+          v_check = flags & kEdge;
           step();
         }
         if (ok && count > 0) ok = products(count - 1);
       } else {
         // the tiles take turns: P V of a tile, then its next scores behind it
-        Note n;
-        n.flags = 0;
-        n.count = 0;
+        int flags = 0;           // of the unit
         bool two = false;
         uint32_t p_at = 0;       // parities of the next p_full
         uint32_t segs_of[2] = {0, 0};
-        auto rows_two = [&](const Note& x) {
-          const int pass = x.seg % a.passes;
-          return x.count * a.group > (pass * 2 + 1) * kTile;
-        };
         auto first_scores = [&](int64_t u) {  // of a segment's first unit here
-          if (!read_note(u, n)) return false;
+          if (!note_there(u)) return false;
+          flags = notes[u & (kNotes - 1)].flags;
+          note_done(u);
           ++segment;
-          two = rows_two(n);
+          two = flags & kTwo;
           if (!wait(&full[slot], turn)) return false;
           if (kTma && !wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd))) return false;
           tc_fence_after();
@@ -742,7 +753,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             commit(&s_full[t]);
           }
           commit(&empty[slot]);
-          if (n.flags & kLast) commit(&q_free[segment & q_odd]);
+          if (flags & kLast) commit(&q_free[segment & q_odd]);
           step();
           return true;
         };
@@ -751,13 +762,17 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           // slot: V of this unit
           const int v_slot = slot;
           const uint32_t v_turn = turn;
-          const bool first = n.flags & kFirst, last = n.flags & kLast;
+          const bool first = flags & kFirst, last = flags & kLast;
           step();
-          ok = wait_values(&full[v_slot], v_turn, n.flags & kEdge);
+          ok = wait_values(&full[v_slot], v_turn, flags & kEdge);
           if (!ok) break;
-          Note next = n;
+          int next = 0;
           if (!last) {
-            ok = read_note(u + 1, next) && wait(&full[slot], turn);
+            ok = note_there(u + 1);
+            if (!ok) break;
+            next = notes[(u + 1) & (kNotes - 1)].flags;
+            note_done(u + 1);
+            ok = wait(&full[slot], turn);
             if (!ok) break;
           }
           const uint32_t q_at = q_base + (uint32_t)(segment & q_odd) * 2 * q_tile;
@@ -785,9 +800,9 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           commit(&empty[v_slot]);
           if (!last) {
             commit(&empty[slot]);
-            if (next.flags & kLast) commit(&q_free[segment & q_odd]);
+            if (next & kLast) commit(&q_free[segment & q_odd]);
             step();
-            n = next;
+            flags = next;
           } else if (u + 1 < count) {
             ok = first_scores(u + 1);
           }
@@ -822,21 +837,27 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
       int tok = 0, g = 0;
       bool mine = false, from_start = false;
       bool ok = true;
+      SegNote g_note = {};
       for (int64_t u = 0; u < count; ++u) {
-        Note n;
-        if (!read_note(u, n)) break;
-        const int head = n.seg / a.passes, pass = n.seg - head * a.passes;
-        const int row = (pass * kRows + t) * kTile + (tid & 127);
-        if (n.flags & kFirst) {
+        if (!note_there(u)) break;
+        const Note& n = notes[u & (kNotes - 1)];
+        const int flags = n.flags, step = n.step;
+        uint32_t valid[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) valid[b] = n.valid[b];
+        if (flags & kFirst) g_note = seg_notes[(segment + 1) & (kNotes - 1)];
+        note_done(u);
+        if (flags & kFirst) {
           ++segment;
+          const int row = (g_note.pass * kRows + t) * kTile + (tid & 127);
           tok = row / a.group;
           g = row - tok * a.group;
-          mine = tok < n.count;
-          from_start = n.flags & kFromStart;
+          mine = tok < g_note.count;
+          from_start = flags & kFromStart;
           mask = 0;
-          if (mine) mask = a.tree_mask != nullptr ? (uint64_t)a.tree_mask[n.first + tok] : ~0ull >> (63 - tok);
+          if (mine) mask = a.tree_mask != nullptr ? (uint64_t)a.tree_mask[g_note.first + tok] : ~0ull >> (63 - tok);
         }
-        if (kRows == 2 && t == 1 && n.count * a.group <= (pass * 2 + 1) * kTile) continue;
+        if (kRows == 2 && t == 1 && !(flags & kTwo)) continue;
         const int sb = kRows == 1 ? (int)(u & 1) : t;
         const uint32_t s_at = tmem + lanes + sb * kTile;
         const uint32_t o_at = tmem + lanes + 2 * kTile + (kRows == 1 ? (uint32_t)(segment & 1) : (uint32_t)t) * DP;
@@ -848,15 +869,15 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 #pragma unroll
         for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, s + 32 * b);
         tmem_wait_ld();
-        if (n.step < kTile || (n.valid[0] & n.valid[1] & n.valid[2] & n.valid[3]) != kFull) {
+        if (step < kTile || (valid[0] & valid[1] & valid[2] & valid[3]) != kFull) {
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             // word b of what this row sees: the context before `step`, its mask from there on
-            const int from = n.step - 32 * b;
+            const int from = step - 32 * b;
             uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
             if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
             else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
-            see &= n.valid[b];
+            see &= valid[b];
 #pragma unroll
             for (int y = 0; y < 32; ++y)
               if (!((see >> y) & 1u)) s[32 * b + y] = 0xff800000u;
@@ -872,18 +893,18 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         // tiles: behind the last one).  A barrier tells its last phase from the one before and no
         // further, so it is looked at before this warp lets this unit's P V run: for the rescale,
         // and ahead of the output's own wait.
-        if (kRows == 1 && u > 0 && (n.flags & kLast)) {
+        if (kRows == 1 && u > 0 && (flags & kLast)) {
           ok = wait(&o_full[0], (uint32_t)u - 1);
           if (!ok) break;
           tc_fence_after();
         }
-        if (n.flags & kFirst) {
+        if (flags & kFirst) {
           ref = top > -INFINITY ? top : kRefStart;
           part[0] = part[1] = 0;
         } else {
           const bool raise = mine && top > ref + kLazy;
           if (__any_sync(kFull, raise)) {
-            if (kRows == 1 && !(n.flags & kLast)) {
+            if (kRows == 1 && !(flags & kLast)) {
               ok = wait(&o_full[0], (uint32_t)u - 1);
               if (!ok) break;
               tc_fence_after();
@@ -925,7 +946,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             if (lane == 0) mbar_arrive(&p_full[2 * sb + (b >> 1)]);
           }
         }
-        if (!(n.flags & kLast)) continue;
+        if (!(flags & kLast)) continue;
         // ------------------------------------------------------------ output
         float sum;
         {
@@ -938,7 +959,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         if (!ok) break;
         ++segments;
         tc_fence_after();
-        const bool whole = from_start && (n.flags & kToEnd);
+        const bool whole = from_start && (flags & kToEnd);
         uint64_t spoilt = bad[segment & (kBadRing - 1)];
         spoilt &= mask;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -947,7 +968,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         // 4 lanes hold 4 rows; they exchange 16-byte pieces, so that a store writes 64 bytes of
         // each of 8 rows
         const int64_t own = !mine ? -1
-                            : whole ? ((int64_t)(n.first + tok) * a.q_heads + head * a.group + g) * a.head_dim
+                            : whole ? ((int64_t)(g_note.first + tok) * a.q_heads + g_note.head * a.group + g) * a.head_dim
                                     : (int64_t)in_part * DP;
         int64_t to[4];
 #pragma unroll
@@ -959,11 +980,11 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           tmem_wait_ld();
           // values that were set to 0, where this row sees them
           for (uint64_t left = spoilt; left != 0; left &= left - 1) {
-            const int64_t p = (int64_t)n.ctx + __ffsll((long long)left) - 1;
+            const int64_t p = (int64_t)g_note.ctx + __ffsll((long long)left) - 1;
             int64_t lb, off;
             a.div.divmod(p, lb, off);
-            const int64_t blk = a.table[(int64_t)n.r * a.stride + lb];
-            const __nv_bfloat16* v = a.v_cache + ((blk * a.div.size + off) * a.kv_heads + head) * a.head_dim;
+            const int64_t blk = a.table[(int64_t)g_note.r * a.stride + lb];
+            const __nv_bfloat16* v = a.v_cache + ((blk * a.div.size + off) * a.kv_heads + g_note.head) * a.head_dim;
 #pragma unroll
             for (int y = 0; y < 32; ++y)
               if (32 * b + y < a.head_dim &&
@@ -1019,16 +1040,14 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (kTma && warp == kCopy && __any_sync(kFull, *abort != 0)) {
-    // where a wait ran out: the copies in flight end before the shared memory goes to another CTA
-    for (int i = 0; i < a.slots; ++i) {
-      const uint32_t uses = turns + (i < slots_used ? 1u : 0u);
-      if (uses > 0) mbar_wait_bounded(&full[i], (uses - 1) & 1);
+  if (kTma && (warp == kCopy + 1 || warp == kCopy + 2) && __any_sync(kFull, *abort != 0)) {
+    // where a wait ran out: this warp's copies in flight end before the shared memory goes to another CTA
+    for (int64_t u = max((int64_t)0, issued - 6); u < issued; ++u) {
+      const int64_t at = 2 * u + (warp == kCopy + 2 ? 1 : 0);
+      mbar_wait_bounded(&full[at % a.slots], (uint32_t)(at / a.slots) & 1);
     }
-    for (int i = 0; i < kNotes; ++i) {
-      const int64_t uses = (edges_used >> 3) + (i < (edges_used & 7) ? 1 : 0);
-      if (uses > 0) mbar_wait_bounded(&edge[i], (uint32_t)(uses - 1) & 1);
-    }
+    for (int64_t e = max((int64_t)0, edges_used - 6); e < edges_used; ++e)
+      mbar_wait_bounded(&edge[e & (kNotes - 1)], (uint32_t)(e >> 3) & 1);
   }
   if (warp == kIssuer) {
     tmem_dealloc(tmem, 512);

@@ -167,9 +167,10 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
   using L = Smem<DP>;
   constexpr int kThreads = kThreadsOf<kRows>;
   constexpr int kIssuer = 4 * kRows, kCopy = kIssuer + 4;
-  // registers of the warpgroups: 384 threads x 168 at launch >= 128 x (224 + 104 + 168), 512 x 128 >= 128 x
+  // registers of the warpgroups: 384 threads x 168 at launch = 128 x (240 + 104 + 160), 512 x 128 >= 128 x
   // (184 + 184 + 56 + 80)
-  constexpr int kSoftmaxRegs = kRows == 1 ? 224 : 184, kIssueRegs = kRows == 1 ? 104 : 56, kCopyRegs = 80;
+  constexpr int kSoftmaxRegs = kRows == 1 ? 240 : 184, kIssueRegs = kRows == 1 ? 104 : 56;
+  constexpr int kCopyRegs = kRows == 1 ? 160 : 80;
   constexpr int kLag = DP == 128 ? 1 : 3;   // units in flight beside the newest: 128 KB with it
   constexpr int kPieces = DP / 8;           // 16-byte pieces of a row
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -258,7 +259,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 
   if (warp >= kCopy) {
     // ---------------------------------------------------------------- copies
-    if (kRows == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
     const int w = warp - kCopy;
     uint32_t err = 0;
     if (w == 0 && lane == 0) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);  // until it is known better

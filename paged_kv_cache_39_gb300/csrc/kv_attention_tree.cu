@@ -866,29 +866,37 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         if (!ok) break;
         ++mine_u;
         tc_fence_after();
-        uint32_t s[kTile];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld32(s_at + 32 * b, s + 32 * b);
-        tmem_wait_ld();
-        if (step < kTile || (valid[0] & valid[1] & valid[2] & valid[3]) != kFull) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            // word b of what this row sees: the context before `step`, its mask from there on
-            const int from = step - 32 * b;
-            uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
-            if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
-            else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
-            see &= valid[b];
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!((see >> y) & 1u)) s[32 * b + y] = 0xff800000u;
-          }
-        }
+        // Half of the keys at a time, in loops: unrolled over the whole tile, the four schedulers wait for
+        // instructions (twice the time with four warps as with one).
+        const bool hide = step < kTile || (valid[0] & valid[1] & valid[2] & valid[3]) != kFull;
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[kTile / 2];
+          tmem_ld32(s_at + 64 * h, s);
+          tmem_ld32(s_at + 64 * h + 32, s + 32);
+          tmem_wait_ld();
+          if (hide) {
 #pragma unroll
-        for (int z = 0; z < kTile; z += 4)
+            for (int b = 0; b < 2; ++b) {
+              // word 2 h + b of what this row sees: the context before `step`, its mask from there on
+              const int from = step - 64 * h - 32 * b;
+              uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
+              if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
+              else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
+              see &= h == 0 ? valid[b] : valid[2 + b];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[z + y]));
+              for (int y = 0; y < 32; ++y)
+                if (!((see >> y) & 1u)) s[32 * b + y] = 0xff800000u;
+              tmem_st32(s_at + 64 * h + 32 * b, s + 32 * b);
+            }
+            tmem_wait_st();
+          }
+#pragma unroll
+          for (int z = 0; z < kTile / 2; z += 4)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[z + y]));
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         // One tile: the last unit's P V may still run (S of this one came behind the one before that; two
         // tiles: behind the last one).  A barrier tells its last phase from the one before and no
@@ -926,26 +934,26 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           }
         }
         const uint64_t c2 = pair(c, c), r2 = pair(-ref, -ref);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[kTile / 2], p[kTile / 4];
+          tmem_ld32(s_at + 64 * h, s);
+          tmem_ld32(s_at + 64 * h + 32, s + 32);
+          tmem_wait_ld();
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t p[16];
-#pragma unroll
-          for (int y = 0; y < 16; ++y) {
+          for (int y = 0; y < kTile / 4; ++y) {
             float e0, e1;
-            unpair(fma2(pair(__uint_as_float(s[32 * b + 2 * y]), __uint_as_float(s[32 * b + 2 * y + 1])), c2, r2),
-                   e0, e1);
+            unpair(fma2(pair(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, r2), e0, e1);
             e0 = ex2(e0);
             e1 = ex2(e1);
             part[y & 1] = add2(part[y & 1], pair(e0, e1));
             p[y] = pack_bf16(e0, e1);
           }
-          tmem_st16(s_at + 16 * b, p);
-          if (b & 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * sb + (b >> 1)]);
-          }
+          tmem_st32(s_at + 32 * h, p);  // where the first half of the logits was: they are used up
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * sb + h]);
         }
         if (!(flags & kLast)) continue;
         // ------------------------------------------------------------ output

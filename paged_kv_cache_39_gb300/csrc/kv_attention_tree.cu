@@ -45,12 +45,12 @@ namespace {
 
 constexpr int kTile = 128;             // keys of a unit, rows of a tile
 constexpr int kCopiers = 4;            // warps, where they copy; where TMA does:
-constexpr int kReaders = 3;            // that read what the first one describes: K's copies, V's, Q and checks
+constexpr int kReaders = 4;            // that read what the first one describes: K's copies, V's, Q, checks
 constexpr int kNotes = 8;              // units described ahead (a power of two: 2^3)
 constexpr int kBadRing = 16;           // segments whose values are noted
 constexpr float kLazy = 8.0f;          // log2 of the most a weight may pass the reference
 constexpr float kRefStart = -1e30f;    // of a row with no finite logit yet
-constexpr int kSmemMax = 232448 - 64;  // of a CTA, less static
+constexpr int kSmemMax = 232448;       // of a CTA
 constexpr int kJoinThreads = 128;
 
 struct TreeArgs {
@@ -130,17 +130,18 @@ struct __align__(16) SegNote {
 // of this CTA's share; of the segment; values to check (kTma); more rows than a tile in this pass
 enum Flags { kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8, kEdge = 16, kTwo = 32 };
 
-constexpr int kNumBars = 2 * 12 + 2 * kNotes + 2 + 4 + 2 + 2 + 2 + 1 + 2 + 2 * kNotes;
+constexpr int kNumBars = 2 * 12 + 2 * kNotes + 2 + 4 + 2 + 2 + 2 + 1 + 2 + 2 * kNotes + 8;
 template <int DP>
-struct Smem {
+struct Layout {
   static constexpr int kSlot = kTile * DP * 2;
   static constexpr int kBars = 0;
   static constexpr int kNote = (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSegNote = kNote + kNotes * (int)sizeof(Note);
   static constexpr int kBad = kSegNote + kNotes * (int)sizeof(SegNote);
-  static constexpr int kMisc = kBad + kBadRing * 8;
-  static constexpr int kScan = kMisc + 16;                              // int64_t[17]: units by warp, all
-  static constexpr int kHead = (kScan + 17 * 8 + 1023) / 1024 * 1024;   // Q, then the ring
+  static constexpr int kMisc = kBad + kBadRing * 8;                // tensor memory, abort; int64_t: all units
+  static constexpr int kWords = kMisc + 32;                        // uint32_t[2][2][4][2]: rows that rise
+  static constexpr int kTops = kWords + 128;                       // float[2][128]
+  static_assert(kTops + 2 * kTile * 4 <= 3072, "");               // Q, then the ring
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
@@ -156,21 +157,30 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Threads: kRows tiles of 4 softmax warps, the issuer and 3 others, 4 copiers.
+// A whole warp's wait.  It is voted on, so the lanes of a role never part: what they issue takes its
+// operands from uniform registers and wants all of them there.
+__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(kFull, mbar_wait_role(bar, parity, abort)) != 0;
+}
+
+// Threads: the softmax warps (4 for one tile; 8 for each of two, each warp half of the keys), the issuer's
+// four, 4 copiers.
 template <int kRows>
-constexpr int kThreadsOf = 128 * kRows + 256;
+constexpr int kThreadsOf = 128 * kRows * kRows + 256;
+constexpr int kHead = 3072;            // bytes of shared memory before Q
 
 template <int DP, int kRows, bool kTma>
 __global__ void __launch_bounds__(kThreadsOf<kRows>, 1)
 attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map) {
-  using L = Smem<DP>;
+  using L = Layout<DP>;
   constexpr int kThreads = kThreadsOf<kRows>;
-  constexpr int kIssuer = 4 * kRows, kCopy = kIssuer + 4;
-  // registers of the warpgroups: 384 threads x 168 at launch = 128 x (240 + 104 + 160), 512 x 128 >= 128 x
-  // (184 + 184 + 56 + 80)
-  constexpr int kSoftmaxRegs = kRows == 1 ? 240 : 184, kIssueRegs = kRows == 1 ? 104 : 56;
-  constexpr int kCopyRegs = kRows == 1 ? 160 : 80;
+  constexpr int kHalves = kRows;            // softmax warps that share 32 rows
+  constexpr int kIssuer = 4 * kRows * kHalves, kCopy = kIssuer + 4;
+  // registers of the warpgroups: 384 threads x 168 at launch = 128 x (240 + 104 + 160), 768 x 80 = 128 x
+  // (4 x 88 + 64 + 64)
+  constexpr int kSoftmaxRegs = kRows == 1 ? 240 : 88, kIssueRegs = kRows == 1 ? 104 : 64;
+  constexpr int kCopyRegs = kRows == 1 ? 160 : 64;
   constexpr int kLag = DP == 128 ? 1 : 3;   // units in flight beside the newest: 128 KB with it
   constexpr int kPieces = DP / 8;           // 16-byte pieces of a row
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -188,15 +198,17 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
   uint64_t* q_full = drain + 1;             // kTma: by segment % q_bufs
   uint64_t* edge = q_full + 2;              // kTma: V of units whose values are checked, in turn: arrived,
   uint64_t* checked = edge + kNotes;        // and checked
+  uint64_t* pairs = checked + kNotes;       // of softmax warps that share rows, by tile and quarter
   Note* notes = reinterpret_cast<Note*>(smem + L::kNote);
   SegNote* seg_notes = reinterpret_cast<SegNote*>(smem + L::kSegNote);  // by segment & (kNotes - 1)
   volatile uint64_t* bad = reinterpret_cast<uint64_t*>(smem + L::kBad);
   int* misc = reinterpret_cast<int*>(smem + L::kMisc);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort = misc + 1;
+  int64_t* s_total = reinterpret_cast<int64_t*>(misc + 2);
   const int q_tile = a.q_rows * DP * 2;     // bytes of a tile's Q
   const int q_odd = a.q_bufs - 1;           // 1: segments take turns with Q
-  unsigned char* const q_smem = smem + L::kHead;
+  unsigned char* const q_smem = smem + kHead;
   unsigned char* const ring = q_smem + (a.q_bufs * kRows * q_tile + 1023) / 1024 * 1024;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform for the compiler, too
@@ -206,9 +218,10 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     int count = 1;
     if (b < empty) count = kTma ? 1 : kCopiers;
     if (b >= note_full && b < note_free) count = kTma ? 1 : kCopiers;
-    if (b >= note_free && b < s_full) count = kRows * a.warps + 1 + (kTma ? kReaders : 0);
+    if (b >= note_free && b < s_full) count = 1 + (kTma ? kReaders : 0);
     if (b >= p_full && b < o_full) count = a.warps;
-    if (b >= o_free && b < q_free) count = a.warps;
+    if (b >= o_free && b < q_free) count = kHalves * a.warps;
+    if (b >= pairs) count = 2;
     mbar_init(&bars[tid], count);
     mbar_fence_init();
   }
@@ -222,7 +235,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
   const int segs = a.kv_heads * a.passes, rounds = segs / a.gang;
   const int per = (a.num_reqs + kThreads - 1) / kThreads;
   int64_t* s_before = reinterpret_cast<int64_t*>(ring);   // [kThreads] units before each thread's requests
-  int64_t* s_warp = reinterpret_cast<int64_t*>(smem + L::kScan);
+  int64_t* s_warp = s_before + kThreads;
   {
     const int r_lo = min(a.num_reqs, tid * per), r_hi = min(a.num_reqs, r_lo + per);
     uint32_t err = 0;
@@ -235,21 +248,20 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     int64_t before = incl - mine;
     for (int w = 0; w < warp; ++w) before += s_warp[w];
     s_before[tid] = before;
-    if (tid == kThreads - 1) s_warp[kThreads / 32] = before + mine;
+    if (tid == kThreads - 1) *s_total = before + mine;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, *tmem_ptr, 0);
-  const int64_t total = s_warp[kThreads / 32];
+  const int64_t total = *s_total;
   const int64_t share = (total + a.gangs - 1) / a.gangs;
   const int my_gang = blockIdx.x / a.gang, member = blockIdx.x - my_gang * a.gang;
   const int64_t begin = my_gang * share;
   const int64_t count = my_gang < a.gangs && begin < total ? min(share, total - begin) : 0;
 
   int64_t issued = 0, edges_used = 0;        // copying warps (kTma): units, of them through edge barriers
-  auto all = [](bool ok) { return __all_sync(kFull, ok) != 0; };
-  auto wait = [&](uint64_t* b, uint32_t parity) { return all(mbar_wait_role(b, parity & 1, abort)); };
+  auto wait = [&](uint64_t* b, uint32_t parity) { return role_wait(b, parity & 1, abort); };
   // A reader waits for its next note, reads what it wants of it and gives it back.
   auto note_there = [&](int64_t u) { return wait(&note_full[u & (kNotes - 1)], (uint32_t)(u >> 3)); };
   auto note_done = [&](int64_t u) {
@@ -257,6 +269,28 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     if (lane == 0) mbar_arrive(&note_free[u & (kNotes - 1)]);
   };
 
+  // Values of the step's rows (key `step` on) that are not finite: 0, and their rows noted.
+  auto check_values = [&](int y, int step, int seg_no, int s) {
+    if (y < step) return;
+    unsigned char* row = ring + s * L::kSlot + y * 128;
+    bool any = false;
+#pragma unroll 4
+    for (int c = 0; c < kPieces; ++c) {
+      uint4* p = reinterpret_cast<uint4*>(row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (y & 7)) << 4));
+      uint4 v = *p;
+      uint32_t e[4] = {v.x, v.y, v.z, v.w};
+      bool hit = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
+        if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0xffffu, hit = true;
+      }
+      if (hit) *p = make_uint4(e[0], e[1], e[2], e[3]);
+      any |= hit;
+    }
+    if (any)
+      atomicOr(reinterpret_cast<unsigned long long*>(smem + L::kBad) + seg_no, 1ull << (y - step));
+  };
   if (warp >= kCopy) {
     // ---------------------------------------------------------------- copies
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
@@ -285,28 +319,6 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     }
     fence_proxy_async_smem();
     asm volatile("bar.sync 2, 128;" ::: "memory");  // before the ring is written
-    // Values of the step's rows (key `step` on) that are not finite: 0, and their rows noted.
-    auto check_values = [&](int y, int step, int seg_no, int s) {
-      if (y < step) return;
-      unsigned char* row = ring + s * L::kSlot + y * 128;
-      bool any = false;
-#pragma unroll 4
-      for (int c = 0; c < kPieces; ++c) {
-        uint4* p = reinterpret_cast<uint4*>(row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (y & 7)) << 4));
-        uint4 v = *p;
-        uint32_t e[4] = {v.x, v.y, v.z, v.w};
-        bool hit = false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, hit = true;
-          if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0xffffu, hit = true;
-        }
-        if (hit) *p = make_uint4(e[0], e[1], e[2], e[3]);
-        any |= hit;
-      }
-      if (any)
-        atomicOr(reinterpret_cast<unsigned long long*>(smem + L::kBad) + seg_no, 1ull << (y - step));
-    };
     const int sub = lane / kPieces, piece = lane % kPieces;
     constexpr int kPer = 32 / kPieces;      // rows of a copy instruction
     const bool piece_real = piece * 8 < a.head_dim;
@@ -325,13 +337,11 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
       }
     };
     if (kTma && w == 3) {
-      // -------------------------------------------------------------- Q, and values at the edges
-      int64_t segment = -1, edges = 0;
-      int slot = 1;              // V of the unit
+      // -------------------------------------------------------------- Q
+      int64_t segment = -1;
       for (int64_t u = 0; u < count; ++u) {
         if (!note_there(u)) break;
-        const Note& n = notes[u & (kNotes - 1)];
-        const int flags = n.flags, step = n.step, from = n.seen & 255, to = n.seen >> 8;
+        const int flags = notes[u & (kNotes - 1)].flags;
         if (flags & kFirst) ++segment;
         const SegNote g = seg_notes[segment & (kNotes - 1)];
         note_done(u);
@@ -344,25 +354,6 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_full[segment & q_odd]);
         }
-        if (flags & kEdge) {
-          if (!wait(&edge[edges & (kNotes - 1)], (uint32_t)(edges >> 3))) break;
-          for (int y = lane; y < kTile; y += 32) {
-            if (y < from || y >= to) {  // of the block, but not of the request
-#pragma unroll
-              for (int c = 0; c < kPieces; ++c)
-                *reinterpret_cast<uint4*>(ring + slot * L::kSlot + (c >> 3) * (kTile * 128) + y * 128 +
-                                          (((c & 7) ^ (y & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-            } else {
-              check_values(y, step, (int)(segment & (kBadRing - 1)), slot);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&checked[edges & (kNotes - 1)]);
-          ++edges;
-        }
-        slot += 2;
-        if (slot >= a.slots) slot -= a.slots;
       }
     } else if (kTma && w > 0) {
       // -------------------------------------------------------------- copies of K (1) or V (2)
@@ -602,9 +593,8 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         // copy it
         if (first && segment >= a.q_bufs)
           ok = wait_telling(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1, u);
-        ok = ok && (k_turn == 0 || mbar_wait_role(&empty[k_slot], (k_turn - 1) & 1, abort)) &&
-             (v_turn == 0 || mbar_wait_role(&empty[v_slot], (v_turn - 1) & 1, abort));
-        ok = all(ok);
+        ok = ok && (k_turn == 0 || role_wait(&empty[k_slot], (k_turn - 1) & 1, abort)) &&
+             (v_turn == 0 || role_wait(&empty[v_slot], (v_turn - 1) & 1, abort));
         if (!ok) break;
         if (first)  // Q with the segment's first unit
           copy_q(req.first, req.count, here_head, here_pass, (int)(segment & q_odd), w, kCopiers);
@@ -661,17 +651,20 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             mma_ss(d, qd + (k / 4) * q_cols + (k % 4) * 2, kd + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4),
                    s_desc, k > 0);
         }
+        __syncwarp();
       };
       auto values = [&](uint32_t d, uint32_t p, int slot, bool add, int half) {
         const uint64_t vd = smem_desc(ring_at + slot * L::kSlot, kTile * 128) + half * ((kTile / 2 * 128) >> 4);
         if (leader) {
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            mma_ts(d, p + half * (kTile / 4) + k * 8, vd + k * (2048 >> 4), o_desc, add || k > 0);
+            mma_ts(d, p + half * (kTile / 2) + k * 8, vd + k * (2048 >> 4), o_desc, add || k > 0);
         }
+        __syncwarp();
       };
       auto commit = [&](uint64_t* b) {
         if (leader) mma_commit(b);
+        __syncwarp();
       };
       bool ok = true;
       int slot = 0;
@@ -683,129 +676,130 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         }
       };
       int64_t segment = -1, edges = 0;
-      // V of a unit, through the warps that check it where it has values to check
-      auto wait_values = [&](uint64_t* b, uint32_t parity, bool check) {
+      // V of a unit, through the warp that checks it where it has values to check
+      auto values_there = [&](uint64_t* b, uint32_t parity, bool check) {
         if (!kTma || !check) return wait(b, parity);
         ++edges;
         return wait(&checked[(edges - 1) & (kNotes - 1)], (uint32_t)((edges - 1) >> 3));
       };
+      // the first unit's flags, the next ones' ahead of time
+      int flags = 0;
+      auto read_flags = [&](int64_t u) {
+        if (!wait(&note_full[u & (kNotes - 1)], (uint32_t)(u >> 3))) return false;
+        flags = notes[u & (kNotes - 1)].flags;
+        return true;
+      };
+      // all have read a unit's note once its weights are there
+      auto give_back = [&](int64_t u) {
+        if (leader) mbar_arrive(&note_free[u & (kNotes - 1)]);
+        __syncwarp();
+      };
+      if (count > 0) ok = read_flags(0);
       if constexpr (kRows == 1) {
-        // unit u's scores, then unit u - 1's products with V
-        int v_slot = 0;
+        // unit u's scores, then unit u - 1's products with V; behind a segment's end the products first, as
+        // the next one's Q may be late
+        int v_slot = 0, v_flags = 0;
         uint32_t v_turn = 0;
         int64_t v_segment = 0;
-        bool v_first = false, v_check = false;
         auto products = [&](int64_t u) {
           const uint32_t d = tmem + 2 * kTile + (uint32_t)(v_segment & 1) * DP, p = tmem + (uint32_t)(u & 1) * kTile;
-          if (v_first && v_segment >= 2 && !wait(&o_free[v_segment & 1], (uint32_t)(v_segment / 2 - 1))) return false;
-          if (!wait_values(&full[v_slot], v_turn, v_check)) return false;
-          if (!wait(&p_full[2 * (u & 1)], (uint32_t)(u >> 1))) return false;
+          const bool first = v_flags & kFirst;
+          if (first && v_segment >= 2 && !wait(&o_free[v_segment & 1], (uint32_t)(v_segment >> 1) - 1)) return false;
+          if (!values_there(&full[v_slot], v_turn, v_flags & kEdge) || !wait(&p_full[2 * (u & 1)], (uint32_t)(u >> 1)))
+            return false;
           tc_fence_after();
-          values(d, p, v_slot, !v_first, 0);
+          values(d, p, v_slot, !first, 0);
           if (!wait(&p_full[2 * (u & 1) + 1], (uint32_t)(u >> 1))) return false;
           tc_fence_after();
           values(d, p, v_slot, true, 1);
-          commit(&empty[v_slot]);
           commit(&o_full[0]);
+          commit(&empty[v_slot]);
+          give_back(u);
           return true;
         };
         for (int64_t u = 0; ok && u < count; ++u) {
-          ok = note_there(u);
-          if (!ok) break;
-          const int flags = notes[u & (kNotes - 1)].flags;
-          note_done(u);
-          if (flags & kFirst) ++segment;
-          ok = wait(&full[slot], turn);
-          if (ok && kTma && (flags & kFirst)) ok = wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd));
-          if (!ok) break;
-          tc_fence_after();
-          scores(tmem + (uint32_t)(u & 1) * kTile, q_base + (uint32_t)(segment & q_odd) * q_tile, slot);
-          commit(&s_full[u & 1]);
-          commit(&empty[slot]);
-          if (flags & kLast) commit(&q_free[segment & q_odd]);
+          const bool first = flags & kFirst;
+          if (first) {
+            ++segment;
+            if (u > 0) ok = products(u - 1);
+          }
+          ok = ok && wait(&full[slot], turn) &&
+               (!kTma || !first || wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd)));
+          if (ok) {
+            tc_fence_after();
+            scores(tmem + (uint32_t)(u & 1) * kTile, q_base + (uint32_t)(segment & q_odd) * q_tile, slot);
+            commit(&s_full[u & 1]);
+            commit(&empty[slot]);
+            if (flags & kLast) commit(&q_free[segment & q_odd]);
+          }
           step();
-          if (u > 0) ok = products(u - 1);
+          if (ok && !first) ok = products(u - 1);
           v_slot = slot;
           v_turn = turn;
           v_segment = segment;
-          v_first = flags & kFirst;
-          v_check = flags & kEdge;
+          v_flags = flags;
           step();
+          if (ok && u + 1 < count) ok = read_flags(u + 1);
         }
-        if (ok && count > 0) ok = products(count - 1);
+        if (ok && count > 0) products(count - 1);
       } else {
-        // the tiles take turns: P V of a tile, then its next scores behind it
-        int flags = 0;           // of the unit
-        bool two = false;
-        uint32_t p_at = 0;       // parities of the next p_full
-        uint32_t segs_of[2] = {0, 0};
-        auto first_scores = [&](int64_t u) {  // of a segment's first unit here
-          if (!note_there(u)) return false;
-          flags = notes[u & (kNotes - 1)].flags;
-          note_done(u);
-          ++segment;
-          two = flags & kTwo;
-          if (!wait(&full[slot], turn)) return false;
-          if (kTma && !wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd))) return false;
-          tc_fence_after();
-          const uint32_t q_at = q_base + (uint32_t)(segment & q_odd) * 2 * q_tile;
-          for (int t = 0; t < (two ? 2 : 1); ++t) {
-            scores(tmem + t * kTile, q_at + t * q_tile, slot);
-            commit(&s_full[t]);
-          }
+        // The tiles take turns: P V of a tile, then its next scores behind it.  A tile without rows in this
+        // segment goes through the same waits with no instruction.
+        uint32_t segments = 0;   // ended
+        int v_slot = 0;
+        auto tile_scores = [&](int t, bool two) {
+          if (t == 0 || two)
+            scores(tmem + t * kTile, q_base + ((uint32_t)(segment & q_odd) * 2 + t) * q_tile, slot);
+          commit(&s_full[t]);
+        };
+        auto scores_done = [&]() {  // of the unit whose flags these are
           commit(&empty[slot]);
           if (flags & kLast) commit(&q_free[segment & q_odd]);
           step();
+        };
+        auto first_scores = [&]() {  // of a segment's first unit here
+          ++segment;
+          if (!wait(&full[slot], turn) ||
+              (kTma && !wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd))))
+            return false;
+          tc_fence_after();
+          tile_scores(0, flags & kTwo);
+          tile_scores(1, flags & kTwo);
+          scores_done();
           return true;
         };
-        if (count > 0) ok = first_scores(0);
+        if (count > 0) ok = ok && first_scores();
         for (int64_t u = 0; ok && u < count; ++u) {
-          // slot: V of this unit
-          const int v_slot = slot;
+          v_slot = slot;         // V of this unit
           const uint32_t v_turn = turn;
-          const bool first = flags & kFirst, last = flags & kLast;
+          const int now = flags;
+          const bool first = now & kFirst, last = now & kLast, two = now & kTwo;
           step();
-          ok = wait_values(&full[v_slot], v_turn, flags & kEdge);
-          if (!ok) break;
-          int next = 0;
-          if (!last) {
-            ok = note_there(u + 1);
-            if (!ok) break;
-            next = notes[(u + 1) & (kNotes - 1)].flags;
-            note_done(u + 1);
-            ok = wait(&full[slot], turn);
-            if (!ok) break;
-          }
-          const uint32_t q_at = q_base + (uint32_t)(segment & q_odd) * 2 * q_tile;
-          for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
+          ok = values_there(&full[v_slot], v_turn, now & kEdge) && (u + 1 == count || read_flags(u + 1)) &&
+               (last || wait(&full[slot], turn));
+#pragma unroll 1
+          for (int t = 0; ok && t < 2; ++t) {
             const uint32_t d = tmem + 2 * kTile + t * DP, p = tmem + t * kTile;
-            if (first && segs_of[t] > 0) ok = wait(&o_free[t], segs_of[t] - 1);
-            if (ok) ok = wait(&p_full[2 * t], p_at >> t);
+            ok = (!first || segments == 0 || wait(&o_free[t], segments - 1)) && wait(&p_full[2 * t], (uint32_t)u);
             if (!ok) break;
             tc_fence_after();
-            values(d, p, v_slot, !first, 0);
-            ok = wait(&p_full[2 * t + 1], p_at >> t);
+            if (t == 0 || two) values(d, p, v_slot, !first, 0);
+            ok = wait(&p_full[2 * t + 1], (uint32_t)u);
             if (!ok) break;
             tc_fence_after();
-            values(d, p, v_slot, true, 1);
-            if (!last) {
-              scores(tmem + t * kTile, q_at + t * q_tile, slot);
-              commit(&s_full[t]);
-            } else {
-              commit(&o_full[t]);
-              ++segs_of[t];
-            }
-            p_at ^= 1u << t;
+            if (t == 0 || two) values(d, p, v_slot, true, 1);
+            if (!last) tile_scores(t, two);
+            else commit(&o_full[t]);
           }
-          if (!ok) break;
-          commit(&empty[v_slot]);
-          if (!last) {
-            commit(&empty[slot]);
-            if (next & kLast) commit(&q_free[segment & q_odd]);
-            step();
-            flags = next;
-          } else if (u + 1 < count) {
-            ok = first_scores(u + 1);
+          if (ok) {
+            commit(&empty[v_slot]);
+            give_back(u);
+            if (!last) {
+              scores_done();
+            } else {
+              ++segments;
+              if (u + 1 < count) ok = first_scores();
+            }
           }
         }
       }
@@ -813,6 +807,36 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
       __syncwarp();
       if (leader) mma_commit(drain);
       mbar_wait_bounded(drain, 0);
+    } else if (kTma && warp == kIssuer + 1) {
+      // -------------------------------------------------------------- values at the edges
+      int64_t segment = -1, edges = 0;
+      int slot = 1;              // V of the unit
+      for (int64_t u = 0; u < count; ++u) {
+        if (!note_there(u)) break;
+        const Note& n = notes[u & (kNotes - 1)];
+        const int flags = n.flags, step = n.step, from = n.seen & 255, to = n.seen >> 8;
+        note_done(u);
+        if (flags & kFirst) ++segment;
+        if (flags & kEdge) {
+          if (!wait(&edge[edges & (kNotes - 1)], (uint32_t)(edges >> 3))) break;
+          for (int y = lane; y < kTile; y += 32) {
+            if (y < from || y >= to) {  // of the block, but not of the request
+#pragma unroll
+              for (int c = 0; c < kPieces; ++c)
+                *reinterpret_cast<uint4*>(ring + slot * L::kSlot + (c >> 3) * (kTile * 128) + y * 128 +
+                                          (((c & 7) ^ (y & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+            } else {
+              check_values(y, step, (int)(segment & (kBadRing - 1)), slot);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&checked[edges & (kNotes - 1)]);
+          ++edges;
+        }
+        slot += 2;
+        if (slot >= a.slots) slot -= a.slots;
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -823,34 +847,60 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
       const Req q = request(a, r, ignore);
       if (q.units > 0 || q.count <= 0) continue;
       uint4* o = reinterpret_cast<uint4*>(a.out) + q.first * vecs;
-      for (int64_t i = tid; i < q.count * vecs; i += 128 * kRows) o[i] = make_uint4(0, 0, 0, 0);
+      for (int64_t i = tid; i < q.count * vecs; i += 128 * kRows * kHalves) o[i] = make_uint4(0, 0, 0, 0);
     }
-    const int t = warp >> 2;                 // the tile
-    if ((warp & 3) < a.warps) {
+    // With two tiles, two warps share 32 rows: each takes half of a unit's keys, and half of O's channels.
+    const int t = kHalves == 2 ? warp >> 3 : 0, half = kHalves == 2 ? (warp >> 2) & 1 : 0, quarter = warp & 3;
+    constexpr int kKeys = kTile / kHalves, kChannels = DP / kHalves;
+    constexpr int kChunk = kRows == 1 ? 64 : 32;  // keys in registers at a time
+    if (quarter < a.warps) {
       // -------------------------------------------------------------- softmax
-      const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes, in bits 16..
+      const uint32_t lanes = (uint32_t)quarter << 21;     // this warp's 32 lanes, in bits 16..
       const float c = a.scale_log2;
-      int64_t segment = -1, mine_u = 0;      // mine_u: units of this tile so far
+      const int in_tile = quarter * 32 + lane;
+      uint64_t* const pair_bar = &pairs[t * 4 + quarter];
+      float* const top_at = reinterpret_cast<float*>(smem + L::kTops) + t * kTile + in_tile;
+      uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kWords) + (t * 4 + quarter) * 2;
+      uint32_t meets = 0;
+      auto meet = [&]() {  // with the other warp of these rows
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pair_bar);
+        return wait(pair_bar, meets++);
+      };
+      // what `both` makes of the two warps' values, in both
+      auto join = [&](float& x, auto both) {
+        if (kHalves == 1) return true;
+        if (half == 0) *top_at = x;
+        if (!meet()) return false;
+        if (half == 1) *top_at = x = both(*top_at, x);
+        if (!meet()) return false;
+        if (half == 0) x = *top_at;
+        return true;
+      };
+      int64_t segment = -1;
       uint32_t segments = 0;                 // of this tile
       float ref = 0.f;
-      uint64_t part[2] = {0, 0};             // sums of weights, two by two
+      uint64_t part[2] = {0, 0};             // sums of this warp's weights, two by two
       uint64_t mask = 0;
       int tok = 0, g = 0;
       bool mine = false, from_start = false;
       bool ok = true;
       SegNote g_note = {};
       for (int64_t u = 0; u < count; ++u) {
-        if (!note_there(u)) break;
+        const int sb = kRows == 1 ? (int)(u & 1) : t;
+        ok = wait(&s_full[sb], (uint32_t)(kRows == 1 ? u >> 1 : u));
+        if (!ok) break;
+        tc_fence_after();
+        // the issuer has read the note that this unit's scores came behind
         const Note& n = notes[u & (kNotes - 1)];
         const int flags = n.flags, step = n.step;
-        uint32_t valid[4];
+        uint32_t valid[kKeys / 32], all_valid = kFull;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) valid[b] = n.valid[b];
-        if (flags & kFirst) g_note = seg_notes[(segment + 1) & (kNotes - 1)];
-        note_done(u);
+        for (int b = 0; b < kKeys / 32; ++b) all_valid &= valid[b] = n.valid[half * (kKeys / 32) + b];
         if (flags & kFirst) {
           ++segment;
-          const int row = (g_note.pass * kRows + t) * kTile + (tid & 127);
+          g_note = seg_notes[segment & (kNotes - 1)];
+          const int row = (g_note.pass * kRows + t) * kTile + in_tile;
           tok = row / a.group;
           g = row - tok * a.group;
           mine = tok < g_note.count;
@@ -858,46 +908,52 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           mask = 0;
           if (mine) mask = a.tree_mask != nullptr ? (uint64_t)a.tree_mask[g_note.first + tok] : ~0ull >> (63 - tok);
         }
-        if (kRows == 2 && t == 1 && !(flags & kTwo)) continue;
-        const int sb = kRows == 1 ? (int)(u & 1) : t;
-        const uint32_t s_at = tmem + lanes + sb * kTile;
-        const uint32_t o_at = tmem + lanes + 2 * kTile + (kRows == 1 ? (uint32_t)(segment & 1) : (uint32_t)t) * DP;
-        ok = wait(&s_full[sb], (uint32_t)(kRows == 1 ? u >> 1 : mine_u));
-        if (!ok) break;
-        ++mine_u;
-        tc_fence_after();
-        // Half of the keys at a time, in loops: unrolled over the whole tile, the four schedulers wait for
-        // instructions (twice the time with four warps as with one).
-        const bool hide = step < kTile || (valid[0] & valid[1] & valid[2] & valid[3]) != kFull;
+        if (kRows == 2 && t == 1 && !(flags & kTwo)) {  // no rows here
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * sb + half]);
+          if (flags & kLast) {
+            ok = wait(&o_full[t], segments);
+            if (!ok) break;
+            ++segments;
+            if (lane == 0) mbar_arrive(&o_free[t]);
+          }
+          continue;
+        }
+        const uint32_t s_at = tmem + lanes + sb * kTile + half * kKeys;
+        const uint32_t o_at = tmem + lanes + 2 * kTile + (kRows == 1 ? (uint32_t)(segment & 1) : (uint32_t)t) * DP +
+                              half * kChannels;
+        // kChunk keys at a time, in loops: the code of a whole tile, unrolled, has the four schedulers wait for
+        // instructions (twice the time with four warps as with one)
+        const bool hide = step < kTile || all_valid != kFull;
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t s[kTile / 2];
-          tmem_ld32(s_at + 64 * h, s);
-          tmem_ld32(s_at + 64 * h + 32, s + 32);
+        for (int b = 0; b < kKeys / kChunk; ++b) {
+          uint32_t s[kChunk];
+#pragma unroll
+          for (int i = 0; i < kChunk / 32; ++i) tmem_ld32(s_at + kChunk * b + 32 * i, s + 32 * i);
           tmem_wait_ld();
           if (hide) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              // word 2 h + b of what this row sees: the context before `step`, its mask from there on
-              const int from = step - 64 * h - 32 * b;
+            for (int i = 0; i < kChunk / 32; ++i) {
+              // what this row sees of these keys: the context before `step`, its mask from there on
+              const int from = step - kKeys * half - kChunk * b - 32 * i;
               uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
               if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
               else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
-              see &= h == 0 ? valid[b] : valid[2 + b];
+              see &= b == 0 ? valid[i] : valid[kChunk / 32 + i];
 #pragma unroll
               for (int y = 0; y < 32; ++y)
-                if (!((see >> y) & 1u)) s[32 * b + y] = 0xff800000u;
-              tmem_st32(s_at + 64 * h + 32 * b, s + 32 * b);
+                if (!((see >> y) & 1u)) s[32 * i + y] = 0xff800000u;
+              tmem_st32(s_at + kChunk * b + 32 * i, s + 32 * i);
             }
             tmem_wait_st();
           }
 #pragma unroll
-          for (int z = 0; z < kTile / 2; z += 4)
+          for (int z = 0; z < kChunk; z += 4)
 #pragma unroll
             for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[z + y]));
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         // One tile: the last unit's P V may still run (S of this one came behind the one before that; two
         // tiles: behind the last one).  A barrier tells its last phase from the one before and no
         // further, so it is looked at before this warp lets this unit's P V run: for the rescale,
@@ -907,23 +963,38 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           if (!ok) break;
           tc_fence_after();
         }
-        if (flags & kFirst) {
-          ref = top > -INFINITY ? top : kRefStart;
-          part[0] = part[1] = 0;
-        } else {
-          const bool raise = mine && top > ref + kLazy;
-          if (__any_sync(kFull, raise)) {
+        // does a row's maximum pass the reference, here or in the other warp?
+        bool rise = flags & kFirst;
+        if (!rise) {
+          const uint32_t word = __ballot_sync(kFull, mine && top > ref + kLazy);
+          rise = word != 0;
+          if (kHalves == 2) {
+            uint32_t* const at = words + (u & 1) * 16;
+            if (lane == 0) at[half] = word;
+            ok = meet();
+            if (!ok) break;
+            rise |= *(volatile uint32_t*)&at[half ^ 1] != 0;
+          }
+        }
+        if (rise) {
+          ok = join(top, [](float x, float y) { return fmaxf(x, y); });
+          if (!ok) break;
+          if (flags & kFirst) {
+            ref = top > -INFINITY ? top : kRefStart;
+            part[0] = part[1] = 0;
+          } else {
             if (kRows == 1 && !(flags & kLast)) {
               ok = wait(&o_full[0], (uint32_t)u - 1);
               if (!ok) break;
               tc_fence_after();
             }
+            const bool raise = mine && top > ref + kLazy;
             const float f = raise ? ex2(ref - top) : 1.f;
             if (raise) ref = top;
             part[0] = mul2(part[0], pair(f, f));
             part[1] = mul2(part[1], pair(f, f));
 #pragma unroll 1
-            for (int b = 0; b < DP / 32; ++b) {
+            for (int b = 0; b < kChannels / 32; ++b) {
               uint32_t o[32];
               tmem_ld32(o_at + 32 * b, o);
               tmem_wait_ld();
@@ -935,13 +1006,13 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         }
         const uint64_t c2 = pair(c, c), r2 = pair(-ref, -ref);
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t s[kTile / 2], p[kTile / 4];
-          tmem_ld32(s_at + 64 * h, s);
-          tmem_ld32(s_at + 64 * h + 32, s + 32);
+        for (int b = 0; b < kKeys / kChunk; ++b) {
+          uint32_t s[kChunk], p[kChunk / 2];
+#pragma unroll
+          for (int i = 0; i < kChunk / 32; ++i) tmem_ld32(s_at + kChunk * b + 32 * i, s + 32 * i);
           tmem_wait_ld();
 #pragma unroll
-          for (int y = 0; y < kTile / 4; ++y) {
+          for (int y = 0; y < kChunk / 2; ++y) {
             float e0, e1;
             unpair(fma2(pair(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, r2), e0, e1);
             e0 = ex2(e0);
@@ -949,11 +1020,15 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             part[y & 1] = add2(part[y & 1], pair(e0, e1));
             p[y] = pack_bf16(e0, e1);
           }
-          tmem_st32(s_at + 32 * h, p);  // where the first half of the logits was: they are used up
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * sb + h]);
+          // over logits of the same 64 keys that are used up
+          if constexpr (kChunk == 64) tmem_st32(s_at + 64 * b, p);
+          else tmem_st16(s_at + 16 * b, p);
+          if (kChunk == 64 || b == kKeys / kChunk - 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * sb + (kHalves == 2 ? half : b)]);
+          }
         }
         if (!(flags & kLast)) continue;
         // ------------------------------------------------------------ output
@@ -964,7 +1039,8 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           unpair(part[1], b0, b1);
           sum = (a0 + a1) + (b0 + b1);
         }
-        ok = kRows == 1 ? wait(&o_full[0], (uint32_t)u) : wait(&o_full[t], segments);
+        ok = join(sum, [](float x, float y) { return x + y; }) &&
+             wait(&o_full[kRows == 1 ? 0 : t], kRows == 1 ? (uint32_t)u : segments);
         if (!ok) break;
         ++segments;
         tc_fence_after();
@@ -972,7 +1048,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         uint64_t spoilt = bad[segment & (kBadRing - 1)];
         spoilt &= mask;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int in_part = t * kTile + (tid & 127);
+        const int in_part = t * kTile + in_tile;
         float* part_at = a.parts + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * a.part_rows * DP;
         // 4 lanes hold 4 rows; they exchange 16-byte pieces, so that a store writes 64 bytes of
         // each of 8 rows
@@ -983,7 +1059,8 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 #pragma unroll
         for (int y = 0; y < 4; ++y) to[y] = __shfl_sync(kFull, own, (lane & 28) + y);
 #pragma unroll 1
-        for (int b = 0; b < DP / 32; ++b) {
+        for (int b = 0; b < kChannels / 32; ++b) {
+          const int col = half * kChannels + 32 * b;
           uint32_t o[32];
           tmem_ld32(o_at + 32 * b, o);
           tmem_wait_ld();
@@ -996,8 +1073,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             const __nv_bfloat16* v = a.v_cache + ((blk * a.div.size + off) * a.kv_heads + g_note.head) * a.head_dim;
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-              if (32 * b + y < a.head_dim &&
-                  (__bfloat16_as_ushort(v[32 * b + y]) & 0x7f80u) == 0x7f80u)
+              if (col + y < a.head_dim && (__bfloat16_as_ushort(v[col + y]) & 0x7f80u) == 0x7f80u)
                 o[y] = 0x7fc00000u;
           }
           if (whole) {
@@ -1016,8 +1092,8 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             exchange(z[1], z[3], lane & 2, 2);
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              if (to[y] >= 0 && 32 * b + 8 * (lane & 3) < a.head_dim)
-                *reinterpret_cast<uint4*>(a.out + to[y] + 32 * b + 8 * (lane & 3)) = z[y];
+              if (to[y] >= 0 && col + 8 * (lane & 3) < a.head_dim)
+                *reinterpret_cast<uint4*>(a.out + to[y] + col + 8 * (lane & 3)) = z[y];
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1032,11 +1108,11 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 if (to[y] >= 0)
-                  *reinterpret_cast<uint4*>(part_at + to[y] + 32 * b + 16 * h + 4 * (lane & 3)) = z[y];
+                  *reinterpret_cast<uint4*>(part_at + to[y] + col + 16 * h + 4 * (lane & 3)) = z[y];
             }
           }
         }
-        if (!whole && mine)
+        if (!whole && mine && half == 0)
           reinterpret_cast<float2*>(a.parts + (int64_t)gridDim.x * 2 * a.part_rows * DP)[
               ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * a.part_rows + in_part] = make_float2(ref, sum);
         tc_fence_before();
@@ -1045,18 +1121,26 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
       }
     }
   }
-  // all roles have come so far: no copy, matrix instruction or arrival is left
+  // all roles have come so far: no matrix instruction or arrival is left, and no copy unless a wait ran out
+  const bool copies = kTma && (warp == kCopy + 1 || warp == kCopy + 2);
+  int64_t* const s_issued = reinterpret_cast<int64_t*>(smem + L::kTops);  // of K, of V
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (kTma && (warp == kCopy + 1 || warp == kCopy + 2) && __any_sync(kFull, *abort != 0)) {
-    // where a wait ran out: this warp's copies in flight end before the shared memory goes to another CTA
-    for (int64_t u = max((int64_t)0, issued - 6); u < issued; ++u) {
-      const int64_t at = 2 * u + (warp == kCopy + 2 ? 1 : 0);
-      mbar_wait_bounded(&full[at % a.slots], (uint32_t)(at / a.slots) & 1);
+  if (kTma && *abort != 0) {
+    // this warp's copies in flight end before the shared memory goes to another CTA
+    const int is_v = warp == kCopy + 2;
+    if (copies && lane == 0) s_issued[is_v] = issued;
+    __syncthreads();
+    if (copies) {
+      for (int64_t u = max((int64_t)0, issued - (a.slots + 1) / 2); u < issued; ++u) {
+        // a slot whose next turn has begun was read, and its barrier may be a phase further
+        const int64_t at = 2 * u + is_v, next = at + a.slots;
+        if (next / 2 >= s_issued[next & 1]) mbar_wait_bounded(&full[at % a.slots], (uint32_t)(at / a.slots) & 1);
+      }
+      for (int64_t e = max((int64_t)0, edges_used - 6); e < edges_used; ++e)
+        mbar_wait_bounded(&edge[e & (kNotes - 1)], (uint32_t)(e >> 3) & 1);
     }
-    for (int64_t e = max((int64_t)0, edges_used - 6); e < edges_used; ++e)
-      mbar_wait_bounded(&edge[e & (kNotes - 1)], (uint32_t)(e >> 3) & 1);
   }
   if (warp == kIssuer) {
     tmem_dealloc(tmem, 512);
@@ -1143,7 +1227,7 @@ Plan plan_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_
   const int tile_rows = rows < kTile ? rows : kTile;
   p.q_rows = (tile_rows + 7) / 8 * 8;
   p.warps = (tile_rows + 31) / 32;
-  const int head = p.dp == 64 ? Smem<64>::kHead : Smem<128>::kHead;
+  const int head = kHead;
   const int q_bytes = (p.q_rows * p.dp * 2 * p.rows + 1023) / 1024 * 1024, slot = kTile * p.dp * 2;
   const int want = p.dp == 64 ? 10 : 5;
   p.q_bufs = head + 2 * q_bytes + want * slot <= kSmemMax ? 2 : 1;
@@ -1157,7 +1241,7 @@ int launch(const TreeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map
   auto kernel = attention_tree_kernel<DP, kRows, kTma>;
   const int q_bytes = (a.q_bufs * kRows * a.q_rows * DP * 2 + 1023) / 1024 * 1024;
   // Q's matrix instructions read whole tiles of 128 rows: the ring lies behind it
-  const int smem = Smem<DP>::kHead + q_bytes + a.slots * Smem<DP>::kSlot;
+  const int smem = kHead + q_bytes + a.slots * Layout<DP>::kSlot;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return KV_ECUDA;
   const unsigned ctas = (unsigned)(a.gangs * a.gang);

@@ -30,9 +30,8 @@
 namespace kvp {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kClusterMax = 8;
+constexpr int kThreadsPerSm = 1024;  // at 64 registers
 constexpr float kLowBias = 0x1.8p-23f;
 constexpr double kUnit = 0x1p-46;
 
@@ -59,32 +58,57 @@ __device__ __forceinline__ float value(__nv_bfloat16 x) { return __saturatef(__b
 // What a pass sums: p, p - q, or the s of several refusals.
 enum Kind { kWhole, kFirst, kMore };
 
-// s as h + l.  `zh`, `zl`: Z_1 .. Z_(count - 1) in two parts.
-template <Kind kind>
-__device__ __forceinline__ void left_of(float p, float q, const float2* z, int count, float& h,
-                                        float& l) {
-  h = p;
-  l = 0.f;
-  if constexpr (kind != kWhole) {
-    h = p - q;
-    l = (p - h) - q;  // exact where p >= q; else s is 0 anyway
-    if (!(p > q)) h = l = 0.f;
+// s of 2 N elements as h + l, two in a register pair.  z: Z_1 .. Z_(count - 1) in two parts.
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+__device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) { return fma2(y, both(-1.f), x); }
+template <Kind kind, int N>
+__device__ __forceinline__ void left_of(const float (&p)[2 * N], const float (&q)[2 * N], const float2* z,
+                                        int count, uint64_t (&h)[N], uint64_t (&l)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t pp = pair(p[2 * i], p[2 * i + 1]);
+    h[i] = pp;
+    l[i] = 0;
+    if constexpr (kind != kWhole) {
+      // q no larger than p: the difference, and what its rounding leaves, are exact and not below 0
+      const uint64_t qq = pair(fminf(q[2 * i], p[2 * i]), fminf(q[2 * i + 1], p[2 * i + 1]));
+      h[i] = sub2(pp, qq);
+      l[i] = sub2(sub2(pp, h[i]), qq);
+    }
   }
-  for (int j = 1; kind == kMore && j < count; ++j) {
-    const float2 zj = z[j];
-    const float a = __fmul_rn(zj.x, q), b = fmaf(zj.y, q, fmaf(zj.x, q, -a));  // Z q = a + b
-    const float d = h - a, back = d - h;
-    const float rest = ((h - (d - back)) - (a + back)) + (l - b);
-    h = d + rest;
-    l = rest - (h - d);
-    if (!(h > 0.f)) h = l = 0.f;
+  if constexpr (kind == kMore) {
+#pragma unroll 1
+    for (int j = 1; j < count; ++j) {
+      const float2 zj = z[j];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint64_t qq = pair(q[2 * i], q[2 * i + 1]);
+        const uint64_t less = mul2(both(-zj.x), qq);                                // -Z q = less - more
+        const uint64_t more = fma2(both(zj.y), qq, fma2(both(zj.x), qq, less));
+        const uint64_t d = add2(h[i], less), back = sub2(d, h[i]);
+        const uint64_t rest = add2(sub2(sub2(h[i], sub2(d, back)), sub2(back, less)), sub2(l[i], more));
+        float x[2], y[2];
+        h[i] = add2(d, rest);
+        l[i] = sub2(rest, sub2(h[i], d));
+        unpair(h[i], x[0], x[1]);
+        unpair(l[i], y[0], y[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[e] = x[e] > 0.f ? y[e] : 0.f;
+          x[e] = fmaxf(x[e], 0.f);
+        }
+        h[i] = pair(x[0], x[1]);
+        l[i] = pair(y[0], y[1]);
+      }
+    }
   }
 }
-// The two integers of s, biased: their sums are taken off again by count.
-__device__ __forceinline__ void add_weight(float h, float l, uint32_t& hi, uint32_t& lo) {
-  const float t = 1.f + h;
-  hi += __float_as_uint(t);
-  lo += __float_as_uint(((h - (t - 1.f)) + l) + kLowBias);
+// The two integers of each s, biased: their sums are taken off again by count.
+__device__ __forceinline__ void add_weights(uint64_t h, uint64_t l, uint32_t& hi, uint32_t& lo) {
+  const uint64_t t = add2(h, both(1.f));
+  const uint64_t low = add2(add2(sub2(h, add2(t, both(-1.f))), l), both(kLowBias));
+  hi += (uint32_t)t + (uint32_t)(t >> 32);
+  lo += (uint32_t)low + (uint32_t)(low >> 32);
 }
 __device__ __forceinline__ uint64_t weight_sum(uint32_t hi, uint32_t lo, uint32_t count) {
   hi -= count * 0x3f800000u;
@@ -93,11 +117,12 @@ __device__ __forceinline__ uint64_t weight_sum(uint32_t hi, uint32_t lo, uint32_
 }
 template <Kind kind>
 __device__ __forceinline__ uint64_t weight_of(float p, float q, const float2* z, int count) {
-  float h, l;
+  const float p2[2] = {p, 0.f}, q2[2] = {q, 0.f};
+  uint64_t h[1], l[1];
   uint32_t hi = 0, lo = 0;
-  left_of<kind>(p, q, z, count, h, l);
-  add_weight(h, l, hi, lo);
-  return weight_sum(hi, lo, 1);
+  left_of<kind, 1>(p2, q2, z, count, h, l);
+  add_weights(h[0], l[0], hi, lo);
+  return weight_sum(hi, lo, 2);  // the other one is 0
 }
 
 template <typename T>
@@ -145,7 +170,7 @@ struct Cut {
 template <typename T, Kind kind>
 __device__ uint64_t run_sum(const T* p, const T* q, int V, int g, int parts, const float2* z,
                             int count) {
-  constexpr int E = Vec<T>::kElems, U = 4;
+  constexpr int E = Vec<T>::kElems, U = 2;  // vectors asked for at once
   const int lane = threadIdx.x & 31;
   const Cut<T> cut(p, kind == kWhole ? nullptr : q, V);
   uint64_t sum = 0;
@@ -173,11 +198,17 @@ __device__ uint64_t run_sum(const T* p, const T* q, int V, int g, int parts, con
         float x[E], y[E];
         unpack(a[k], x);
         if (kind != kWhole) unpack(b[k], y);
+        else unpack(make_uint4(0, 0, 0, 0), y);
+        constexpr int N = kind == kMore ? E / 2 : 1;  // pairs at a time: more where they wait for one another's Z
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float h, l;
-          left_of<kind>(x[e], kind != kWhole ? y[e] : 0.f, z, count, h, l);
-          add_weight(h, l, hi, lo);
+        for (int e = 0; e < E; e += 2 * N) {
+          float p2[2 * N], q2[2 * N];
+          uint64_t h[N], l[N];
+#pragma unroll
+          for (int i = 0; i < 2 * N; ++i) p2[i] = x[e + i], q2[i] = y[e + i];
+          left_of<kind, N>(p2, q2, z, count, h, l);
+#pragma unroll
+          for (int i = 0; i < N; ++i) add_weights(h[i], l[i], hi, lo);
         }
       }
       sum += weight_sum(hi, lo, U * E);
@@ -195,8 +226,9 @@ __device__ __forceinline__ void store_far(uint64_t* mine, int rank, uint64_t v) 
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(mine, rank)), "l"(v) : "memory");
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads) verify_kernel(VerifyArgs a) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ uint64_t s_sums[2][kClusterMax * kWarps];  // of the runs; passes take turns
   __shared__ uint64_t s_scan[kWarps];
   __shared__ int s_token[kTreeRows], s_parent[kTreeRows], s_path[kTreeRows];
@@ -204,7 +236,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
   __shared__ int s_gone[kTreeRows];                     // tokens that s lost (no q)
   __shared__ float2 s_z[kTreeRows + 1];
   __shared__ double s_zd[kTreeRows + 1];
-  __shared__ int s_at, s_count, s_pass, s_kept, s_final;
+  __shared__ int s_at, s_count, s_pass, s_kept, s_final, s_run;
+  __shared__ uint64_t s_want;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = blockIdx.x / a.cluster, rank = blockIdx.x - r * a.cluster;
   pdl_allow_next();
@@ -329,8 +362,12 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
       s_sums[turn][g] = sum;
     }
     __syncthreads();
-    whole = 0;
-    for (int i = 0; i < parts; ++i) whole += s_sums[turn][i];
+    if (warp == 0) {
+      whole = 0;
+      for (int i = lane; i < parts; i += 32) whole += s_sums[turn][i];
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) whole += __shfl_xor_sync(kFull, whole, d);
+    }
     if (tid == 0) {
       if (pass == 1) {
         const double z = (double)whole * kUnit;
@@ -344,45 +381,105 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
       }
     }
     turn ^= 1;
-    __syncthreads();
   }
   // ---- the last token: the run it falls into, then the element
   const int n = s_count, here = s_at, n_kept = s_kept;
   const T* p = target + here * a.target_stride;
   const T* q = draft == nullptr ? nullptr : draft + here * a.draft_stride;
-  const uint64_t* sums = s_sums[turn ^ 1];
-  uint64_t want = (uint64_t)((double)s_u[0] * (double)whole);
-  int run = 0;
-  for (; run < parts - 1 && sums[run] <= want; ++run) want -= sums[run];
-  if (run / kWarps != rank) return;
-  if (tid == 0) s_final = -1;
-  const Cut<T> cut(p, draft == nullptr || n == 0 ? nullptr : q, V);
-  const int lo = cut.element(run, parts, V), hi = cut.element(run + 1, parts, V);
-  const int each = (hi - lo + kThreads - 1) / kThreads;
-  const int i0 = min(hi, lo + tid * each), i1 = min(hi, i0 + each);
-  auto weight = [&](int i) {
-    const float x = value(p[i]);
-    if (draft == nullptr) {
-      for (int j = 0; j < n; ++j)
-        if (s_gone[j] == i) return (uint64_t)0;
-      return weight_of<kWhole>(x, 0.f, s_z, 0);
+  if (warp == 0) {
+    const uint64_t* sums = s_sums[turn ^ 1];
+    const uint64_t want = (uint64_t)((double)s_u[0] * (double)whole);
+    // runs lane * each .. of this lane, their sum and that of all up to them
+    const int each = (parts + 31) / 32;
+    uint64_t mine = 0;
+    for (int i = lane * each; i < min(parts, (lane + 1) * each); ++i) mine += sums[i];
+    const uint64_t incl = warp_inclusive_scan<uint64_t>(mine);
+    const uint32_t past = __ballot_sync(kFull, incl > want);
+    if (lane == (past != 0 ? __ffs(past) - 1 : 0)) {  // none: nothing has a weight
+      uint64_t rest = want - (incl - mine);
+      int run = lane * each;
+      while (past != 0 && sums[run] <= rest) rest -= sums[run++];
+      s_run = run;
+      s_want = rest;
+      s_final = -1;
     }
-    return n == 0 ? weight_of<kWhole>(x, 0.f, s_z, 0) : weight_of<kMore>(x, value(q[i]), s_z, n);
+  }
+  __syncthreads();
+  const int run = s_run;
+  const uint64_t want = s_want;
+  if (run / kWarps != rank) return;
+  // Its elements once more, a piece in a row for every thread; then the 32 lanes around the thread whose
+  // piece it is take that one element by element.  Short code: it runs once, and waits for itself.
+  const bool only_p = draft == nullptr || n == 0;
+  const Cut<T> cut(p, only_p ? nullptr : q, V);
+  const int lo = cut.element(run, parts, V), hi = cut.element(run + 1, parts, V);
+  auto weight = [&](int i) {
+    const float x = value(p[i]), y = only_p ? 0.f : value(q[i]);
+    uint64_t w = only_p ? weight_of<kWhole>(x, y, s_z, 0) : weight_of<kMore>(x, y, s_z, n);
+    if (draft == nullptr)
+      for (int j = 0; j < n; ++j)
+        if (s_gone[j] == i) w = 0;
+    return w;
   };
+  // [i0, i1): this thread's piece, of whole vectors but for what the run has before and behind them
+  constexpr int E = Vec<T>::kElems, kAtOnce = 2;
+  const int v0 = cut.from(run, parts), vecs = cut.from(run + 1, parts) - v0;
+  const int each = (vecs + kThreads - 1) / kThreads, a0 = min(vecs, tid * each), a1 = min(vecs, a0 + each);
+  const int size = cut.vector ? E : 1, body = cut.head + v0 * size;
+  const int i0 = tid == 0 ? lo : body + a0 * size, i1 = tid == kThreads - 1 ? hi : body + a1 * size;
   uint64_t mine = 0;
-  for (int i = i0; i < i1; ++i) mine += weight(i);
+  for (int i = i0; i < body; ++i) mine += weight(i);
+  for (int i = body + vecs * size; i < i1; ++i) mine += weight(i);
+  if (!cut.vector) {
+#pragma unroll 4
+    for (int i = body + a0; i < body + a1; ++i) mine += weight(i);
+  } else {
+    const uint4* pv = reinterpret_cast<const uint4*>(p + cut.head) + v0;
+    const uint4* qv = only_p ? pv : reinterpret_cast<const uint4*>(q + cut.head) + v0;
+    for (int v = a0; v < a1; v += kAtOnce) {
+      uint4 x[kAtOnce], y[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const bool in = v + k < a1;
+        x[k] = in ? pv[v + k] : make_uint4(0, 0, 0, 0);
+        y[k] = in && !only_p ? qv[v + k] : make_uint4(0, 0, 0, 0);
+      }
+      uint32_t hi32 = 0, lo32 = 0;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        float f[E], g[E];
+        uint64_t h[E / 2], l[E / 2];
+        unpack(x[k], f);
+        unpack(y[k], g);  // zeros leave p as it is
+        left_of<kMore, E / 2>(f, g, s_z, only_p ? 0 : n, h, l);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) add_weights(h[e], l[e], hi32, lo32);
+      }
+      mine += weight_sum(hi32, lo32, kAtOnce * E);
+    }
+    if (draft == nullptr)
+      for (int j = 0; j < n; ++j)
+        if (s_gone[j] >= max(i0, body) && s_gone[j] < min(i1, body + vecs * size))
+          mine -= weight_of<kWhole>(value(p[s_gone[j]]), 0.f, s_z, 0);
+  }
   uint64_t incl = warp_inclusive_scan<uint64_t>(mine);
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
   for (int w = 0; w < warp; ++w) incl += s_scan[w];
-  if (whole > 0 && incl > want && incl - mine <= want) {
-    uint64_t up = incl - mine;
-    int i = i0;
-    for (;; ++i) {
-      up += weight(i);
-      if (up > want) break;
+  const uint32_t found = __ballot_sync(kFull, incl > want && incl - mine <= want);
+  if (found != 0) {  // in this warp; in no warp where nothing has a weight
+    const int src = __ffs(found) - 1;
+    uint64_t up = __shfl_sync(kFull, incl - mine, src);
+    const int from = __shfl_sync(kFull, i0, src), to = __shfl_sync(kFull, i1, src);
+    for (int i = from + lane;; i += 32) {
+      const uint64_t w = warp_inclusive_scan<uint64_t>(i < to ? weight(i) : 0);
+      const uint32_t past = __ballot_sync(kFull, up + w > want);
+      if (past != 0) {
+        if (lane == __ffs(past) - 1) s_final = i;
+        break;
+      }
+      up += __shfl_sync(kFull, w, 31);
     }
-    s_final = i;
   }
   __syncthreads();
   const int last = s_final;
@@ -396,12 +493,21 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
   }
 }
 
+template <typename T, int kThreads>
+int launch(const VerifyArgs& a, int32_t num_reqs, cudaStream_t stream) {
+  return launch_pdl_clusters(verify_kernel<T, kThreads>, (unsigned)num_reqs * a.cluster, a.cluster,
+                             kThreads, 0, stream, a);
+}
+// A request to a CTA where there are more of them than SMs, else as many smaller CTAs to each as run at
+// once, 8 at most.  256 chains of 131072: 43 us so, 47 with two or four of 256 threads; 64 trees of
+// 100003 in bf16: 36 us with 8 of 256 threads, 41 with 8 of 512, 44 with 4 of 512.
 template <typename T>
 int launch(VerifyArgs a, int32_t num_reqs, cudaStream_t stream) {
   a.cluster = 1;
-  while (a.cluster < kClusterMax && num_reqs * a.cluster * 2 <= 2 * sm_count()) a.cluster *= 2;
-  return launch_pdl_clusters(verify_kernel<T>, (unsigned)num_reqs * a.cluster, a.cluster, kThreads,
-                             0, stream, a);
+  if (num_reqs > sm_count()) return launch<T, 512>(a, num_reqs, stream);
+  while (a.cluster < kClusterMax && num_reqs * a.cluster * 2 <= kThreadsPerSm / 256 * sm_count())
+    a.cluster *= 2;
+  return launch<T, 256>(a, num_reqs, stream);
 }
 
 }  // namespace

@@ -131,6 +131,7 @@ struct __align__(16) SegNote {
 enum Flags { kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8, kEdge = 16, kTwo = 32 };
 
 constexpr int kNumBars = 2 * 12 + 2 * kNotes + 2 + 4 + 2 + 2 + 2 + 1 + 2 + 2 * kNotes + 8;
+constexpr int kHead = 3 << 10;         // bytes of shared memory before Q
 template <int DP>
 struct Layout {
   static constexpr int kSlot = kTile * DP * 2;
@@ -141,7 +142,7 @@ struct Layout {
   static constexpr int kMisc = kBad + kBadRing * 8;                // tensor memory, abort; int64_t: all units
   static constexpr int kWords = kMisc + 32;                        // uint32_t[2][2][4][2]: rows that rise
   static constexpr int kTops = kWords + 128;                       // float[2][128]
-  static_assert(kTops + 2 * kTile * 4 <= 3072, "");               // Q, then the ring
+  static_assert(kTops + 2 * kTile * 4 <= kHead, "");              // Q, then the ring
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
@@ -167,7 +168,6 @@ __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volati
 // four, 4 copiers.
 template <int kRows>
 constexpr int kThreadsOf = 128 * kRows * kRows + 256;
-constexpr int kHead = 3072;            // bytes of shared memory before Q
 
 template <int DP, int kRows, bool kTma>
 __global__ void __launch_bounds__(kThreadsOf<kRows>, 1)

@@ -77,6 +77,7 @@ struct TreeArgs {
   int32_t part_rows; // rows of a part in the workspace
   int32_t q_rows;    // rows of a tile's Q in shared memory (a multiple of 8)
   int32_t q_bufs;    // Q of this segment and the next, where there is room
+  int32_t q_box;     // kTma: tokens of a tile, where it begins and ends with a token; else 0
   int32_t slots;     // of the ring
   int32_t box;       // tokens of a TMA box (a power of two that divides the block), or 1
   int32_t warps;     // softmax warps of a tile that can have rows
@@ -171,8 +172,8 @@ constexpr int kThreadsOf = 128 * kRows * kRows + 256;
 
 template <int DP, int kRows, bool kTma>
 __global__ void __launch_bounds__(kThreadsOf<kRows>, 1)
-attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap k_map,
-                      const __grid_constant__ CUtensorMap v_map) {
+attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap q_map,
+                      const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L = Layout<DP>;
   constexpr int kThreads = kThreadsOf<kRows>;
   constexpr int kHalves = kRows;            // softmax warps that share 32 rows
@@ -324,21 +325,34 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     const bool piece_real = piece * 8 < a.head_dim;
     // Rows of Q of a segment, shared by `warps` warps of which this is number `me`.
     auto copy_q = [&](int first, int rows, int head, int pass, int buf, int me, int warps) {
+      // from a row to this warp's next one: tokens and heads, and what that moves the source by
+      const int ahead = warps * kPer, tok_step = ahead / a.group, g_step = ahead - tok_step * a.group;
+      const int64_t move = tok_step * a.q_stride + (int64_t)g_step * a.head_dim;
+      const int64_t wrap = a.q_stride - (int64_t)a.group * a.head_dim;  // a token more, a group of heads less
       for (int t = 0; t < kRows; ++t) {
-        const int row0 = (pass * kRows + t) * kTile, left = rows * a.group - row0;  // rows of this tile
-        const uint32_t q_at = smem_addr(q_smem) + (buf * kRows + t) * q_tile;
-        for (int y = me * kPer + sub; y < min(left, kTile); y += warps * kPer) {
-          const int tok = (row0 + y) / a.group, g = row0 + y - tok * a.group;
-          const __nv_bfloat16* src = a.q + (int64_t)(first + tok) * a.q_stride +
-                                     (int64_t)(head * a.group + g) * a.head_dim + piece * 8;
-          copy16(q_at + (piece >> 3) * (a.q_rows * 128) + y * 128 + (((piece & 7) ^ (y & 7)) << 4),
-                 piece_real ? src : a.q, piece_real);
+        const int row0 = (pass * kRows + t) * kTile, left = min(rows * a.group - row0, kTile);  // rows of this tile
+        int y = me * kPer + sub, g = row0 + y;
+        const int tok = g / a.group;
+        g -= tok * a.group;
+        const __nv_bfloat16* src = a.q + (int64_t)(first + tok) * a.q_stride +
+                                   (int64_t)(head * a.group + g) * a.head_dim + piece * 8;
+        const uint32_t q_at = smem_addr(q_smem) + (buf * kRows + t) * q_tile + (piece >> 3) * (a.q_rows * 128);
+#pragma unroll 4
+        for (; y < left; y += ahead) {
+          copy16(q_at + y * 128 + (((piece & 7) ^ (y & 7)) << 4), piece_real ? src : a.q, piece_real);
+          g += g_step;
+          src += move;
+          if (g >= a.group) g -= a.group, src += wrap;
         }
       }
     };
     if (kTma && w == 3) {
       // -------------------------------------------------------------- Q
-      int64_t segment = -1;
+      // By TMA where a tile's rows are whole tokens; its rows behind the request's are of no use then.
+      const bool leader = elect_one();
+      if (leader && a.q_box > 0) tma_prefetch_map(&q_map);
+      const int box_bytes = a.q_box * a.group * 128;
+      int64_t segment = -1, loaded = 0;
       for (int64_t u = 0; u < count; ++u) {
         if (!note_there(u)) break;
         const int flags = notes[u & (kNotes - 1)].flags;
@@ -347,14 +361,32 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         note_done(u);
         if (flags & kFirst) {
           if (segment >= a.q_bufs && !wait(&q_free[segment & q_odd], (uint32_t)(segment >> q_odd) - 1)) break;
-          copy_q(g.first, g.count, g.head, g.pass, (int)(segment & q_odd), 0, 1);
-          copy_commit();
-          copy_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&q_full[segment & q_odd]);
+          const int buf = (int)(segment & q_odd);
+          if (a.q_box > 0) {
+            if (leader) {
+              const int tiles = flags & kTwo ? 2 : 1;
+              mbar_arrive_expect_tx(&q_full[buf], tiles * (DP / 64) * box_bytes);
+              for (int t = 0; t < tiles; ++t)
+#pragma unroll
+                for (int c = 0; c < DP / 64; ++c)
+                  tma_load_3d(q_smem + (buf * kRows + t) * q_tile + c * (a.q_rows * 128), &q_map, 64 * c,
+                              g.head * a.group, g.first + (g.pass * kRows + t) * a.q_box, &q_full[buf]);
+            }
+            __syncwarp();
+            loaded = segment + 1;
+          } else {
+            copy_q(g.first, g.count, g.head, g.pass, buf, 0, 1);
+            copy_commit();
+            copy_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[buf]);
+          }
         }
       }
+      // none in flight when the shared memory goes to another CTA
+      for (int64_t g = max((int64_t)0, loaded - a.q_bufs); g < loaded; ++g)
+        mbar_wait_bounded(&q_full[g & q_odd], (uint32_t)(g >> q_odd) & 1);
     } else if (kTma && w > 0) {
       // -------------------------------------------------------------- copies of K (1) or V (2)
       const bool is_v = w == 2, leader = elect_one();
@@ -1207,7 +1239,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const __grid_co
 
 // How a call's work is laid out.
 struct Plan {
-  int dp, rows, passes, gang, gangs, part_rows, q_rows, q_bufs, slots, warps;
+  int dp, rows, passes, gang, gangs, part_rows, q_rows, q_bufs, q_box, slots, warps;
   int64_t joins_bytes() const { return ((int64_t)gangs * gang * 16 + 127) / 128 * 128; }
   int64_t bytes() const { return joins_bytes() + (int64_t)gangs * gang * 2 * part_rows * (dp + 2) * 4; }
 };
@@ -1226,6 +1258,7 @@ Plan plan_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_
   p.part_rows = rows < p.rows * kTile ? rows : p.rows * kTile;
   const int tile_rows = rows < kTile ? rows : kTile;
   p.q_rows = (tile_rows + 7) / 8 * 8;
+  p.q_box = tile_rows % group == 0 ? tile_rows / group : 0;
   p.warps = (tile_rows + 31) / 32;
   const int head = kHead;
   const int q_bytes = (p.q_rows * p.dp * 2 * p.rows + 1023) / 1024 * 1024, slot = kTile * p.dp * 2;
@@ -1237,7 +1270,8 @@ Plan plan_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_
 }
 
 template <int DP, int kRows, bool kTma>
-int launch(const TreeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
+int launch(const TreeArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
+           cudaStream_t stream) {
   auto kernel = attention_tree_kernel<DP, kRows, kTma>;
   const int q_bytes = (a.q_bufs * kRows * a.q_rows * DP * 2 + 1023) / 1024 * 1024;
   // Q's matrix instructions read whole tiles of 128 rows: the ring lies behind it
@@ -1245,16 +1279,17 @@ int launch(const TreeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return KV_ECUDA;
   const unsigned ctas = (unsigned)(a.gangs * a.gang);
-  const int rc = launch_pdl(kernel, ctas, kThreadsOf<kRows>, smem, stream, a, k_map, v_map);
+  const int rc = launch_pdl(kernel, ctas, kThreadsOf<kRows>, smem, stream, a, q_map, k_map, v_map);
   if (rc != KV_OK) return rc;
   const unsigned chunks = (unsigned)(a.part_rows + 15) / 16;
   return launch_pdl(join_tree_kernel<DP, kRows>, dim3(ctas, chunks), kJoinThreads, 0, stream, a);
 }
 
 template <int DP, int kRows>
-int launch(const TreeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
-  return a.box > 1 ? launch<DP, kRows, true>(a, k_map, v_map, stream)
-                   : launch<DP, kRows, false>(a, k_map, v_map, stream);
+int launch(const TreeArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
+           cudaStream_t stream) {
+  return a.box > 1 ? launch<DP, kRows, true>(a, q_map, k_map, v_map, stream)
+                   : launch<DP, kRows, false>(a, q_map, k_map, v_map, stream);
 }
 
 int sizes(int32_t num_reqs, int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads,
@@ -1334,23 +1369,27 @@ extern "C" int kv_attention_tree(const void* query, int64_t query_stride, const 
   int box = 1;
   if (block_size % 8 == 0)
     for (box = 8; box < kTile && block_size % (2 * box) == 0;) box *= 2;
-  CUtensorMap k_map = {}, v_map = {};
+  const Plan p = plan_of(max_rows, num_q_heads, num_kv_heads, head_dim);
+  CUtensorMap q_map = {}, k_map = {}, v_map = {};
   const int64_t tokens = num_blocks * block_size, kv_row = (int64_t)num_kv_heads * head_dim;
+  const int group = num_q_heads / num_kv_heads;
   if (box > 1 && (!rows_map(&k_map, k_layer, kv_row, tokens, num_kv_heads, head_dim, 1, box) ||
                   !rows_map(&v_map, v_layer, kv_row, tokens, num_kv_heads, head_dim, 1, box)))
     return KV_ECUDA;
-  const Plan p = plan_of(max_rows, num_q_heads, num_kv_heads, head_dim);
+  const bool q_boxes = box > 1 && p.q_box > 0 && query_stride < ((int64_t)1 << 39);  // bytes below 2^40
+  if (q_boxes && !rows_map(&q_map, query, query_stride, num_rows, num_q_heads, head_dim, group, p.q_box))
+    return KV_ECUDA;
   const TreeArgs a{static_cast<const __nv_bfloat16*>(query), query_stride,
                    reinterpret_cast<const __nv_bfloat16*>(k_layer),
                    reinterpret_cast<const __nv_bfloat16*>(v_layer), num_blocks,
                    BlockDiv::make(block_size), num_q_heads, num_kv_heads, head_dim,
-                   num_q_heads / num_kv_heads, block_table, table_stride, q_start_loc, span_start,
+                   group, block_table, table_stride, q_start_loc, span_start,
                    context_len, tree_mask, num_reqs, num_rows, max_rows,
                    fminf(scale * 1.44269504088896340736f, FLT_MAX),
                    static_cast<__nv_bfloat16*>(out), d_err, p.passes, p.gang, p.gangs, p.part_rows,
-                   p.q_rows, p.q_bufs, p.slots, box, p.warps, static_cast<int4*>(workspace),
+                   p.q_rows, p.q_bufs, q_boxes ? p.q_box : 0, p.slots, box, p.warps, static_cast<int4*>(workspace),
                    reinterpret_cast<float*>(static_cast<char*>(workspace) + p.joins_bytes())};
   if (p.dp == 64)
-    return p.rows == 1 ? launch<64, 1>(a, k_map, v_map, stream) : launch<64, 2>(a, k_map, v_map, stream);
-  return p.rows == 1 ? launch<128, 1>(a, k_map, v_map, stream) : launch<128, 2>(a, k_map, v_map, stream);
+    return p.rows == 1 ? launch<64, 1>(a, q_map, k_map, v_map, stream) : launch<64, 2>(a, q_map, k_map, v_map, stream);
+  return p.rows == 1 ? launch<128, 1>(a, q_map, k_map, v_map, stream) : launch<128, 2>(a, q_map, k_map, v_map, stream);
 }

@@ -1106,7 +1106,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 #pragma unroll
             for (int y = 0; y < 32; ++y)
               if (col + y < a.head_dim && (__bfloat16_as_ushort(v[col + y]) & 0x7f80u) == 0x7f80u)
-                o[y] = 0x7fc00000u;
+                o[y] = __float_as_uint(__uint_as_float(o[y]) + __bfloat162float(v[col + y]));
           }
           if (whole) {
             uint4 z[4];

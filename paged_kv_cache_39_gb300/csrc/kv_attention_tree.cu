@@ -159,10 +159,30 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A whole warp's wait.  It is voted on, so the lanes of a role never part: what they issue takes its
+// A whole warp's wait, bounded: it gives up 1 s after its eighth try, or where another role has (*abort).
+// Short code, as there are many of them and 24 warps share the instruction cache.
+// It is voted on, so the lanes of a role never part: what they issue takes its
 // operands from uniform registers and wants all of them there.
+__device__ __forceinline__ uint32_t timer_low() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(kFull, mbar_wait_role(bar, parity, abort)) != 0;
+  uint32_t tries = 0, t0 = 0;
+  bool ok;
+#pragma unroll 1
+  while (!(ok = mbar_try_wait(bar, parity))) {
+    if (*abort != 0) break;
+    if (++tries < 8) continue;
+    const uint32_t now = timer_low();
+    if (tries == 8) t0 = now;
+    if (now - t0 > (uint32_t)kWaitLimitNs) {
+      *abort = 1;
+      break;
+    }
+  }
+  return __all_sync(kFull, ok) != 0;
 }
 
 // Threads: the softmax warps (4 for one tile; 8 for each of two, each warp half of the keys), the issuer's
@@ -295,7 +315,8 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
   if (warp >= kCopy) {
     // ---------------------------------------------------------------- copies
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-    const int w = warp - kCopy;
+    // TMA: 0 describes, 1 and 2 copy K and V, 3 loads Q, which has the least to do and shares the issuer's scheduler
+    const int w = kTma && (warp - kCopy) % 3 == 0 ? 3 - (warp - kCopy) : warp - kCopy;
     uint32_t err = 0;
     if (w == 0 && lane == 0) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);  // until it is known better
     // the first unit: the request whose units hold `begin`
@@ -749,23 +770,27 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           give_back(u);
           return true;
         };
-        for (int64_t u = 0; ok && u < count; ++u) {
-          const bool first = flags & kFirst;
-          if (first) {
-            ++segment;
-            if (u > 0) ok = products(u - 1);
-          }
-          ok = ok && wait(&full[slot], turn) &&
-               (!kTma || !first || wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd)));
-          if (ok) {
-            tc_fence_after();
-            scores(tmem + (uint32_t)(u & 1) * kTile, q_base + (uint32_t)(segment & q_odd) * q_tile, slot);
-            commit(&s_full[u & 1]);
-            commit(&empty[slot]);
-            if (flags & kLast) commit(&q_free[segment & q_odd]);
+        for (int64_t u = 0; ok && u <= count; ++u) {
+          const bool more = u < count, first = more && (flags & kFirst);
+          if (first) ++segment;
+          // each of the two once in the code
+#pragma unroll 1
+          for (int part = 0; ok && part < 2; ++part) {
+            if ((part == 1) == first) {
+              if (!more) continue;
+              ok = wait(&full[slot], turn) &&
+                   (!kTma || !first || wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd)));
+              if (!ok) break;
+              tc_fence_after();
+              scores(tmem + (uint32_t)(u & 1) * kTile, q_base + (uint32_t)(segment & q_odd) * q_tile, slot);
+              commit(&s_full[u & 1]);
+              commit(&empty[slot]);
+              if (flags & kLast) commit(&q_free[segment & q_odd]);
+            } else if (u > 0) {
+              ok = products(u - 1);
+            }
           }
           step();
-          if (ok && !first) ok = products(u - 1);
           v_slot = slot;
           v_turn = turn;
           v_segment = segment;
@@ -773,7 +798,6 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           step();
           if (ok && u + 1 < count) ok = read_flags(u + 1);
         }
-        if (ok && count > 0) products(count - 1);
       } else {
         // The tiles take turns: P V of a tile, then its next scores behind it.  A tile without rows in this
         // segment goes through the same waits with no instruction.
@@ -795,8 +819,8 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
               (kTma && !wait(&q_full[segment & q_odd], (uint32_t)(segment >> q_odd))))
             return false;
           tc_fence_after();
-          tile_scores(0, flags & kTwo);
-          tile_scores(1, flags & kTwo);
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) tile_scores(t, flags & kTwo);
           scores_done();
           return true;
         };
@@ -884,7 +908,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     // With two tiles, two warps share 32 rows: each takes half of a unit's keys, and half of O's channels.
     const int t = kHalves == 2 ? warp >> 3 : 0, half = kHalves == 2 ? (warp >> 2) & 1 : 0, quarter = warp & 3;
     constexpr int kKeys = kTile / kHalves, kChannels = DP / kHalves;
-    constexpr int kChunk = kRows == 1 ? 64 : 32;  // keys in registers at a time
+    constexpr int kChunk = 32;  // keys in registers at a time
     if (quarter < a.warps) {
       // -------------------------------------------------------------- softmax
       const uint32_t lanes = (uint32_t)quarter << 21;     // this warp's 32 lanes, in bits 16..
@@ -972,7 +996,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
               uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
               if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
               else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
-              see &= b == 0 ? valid[i] : valid[kChunk / 32 + i];
+              see &= b == 0 ? valid[0] : b == 1 ? valid[1] : b == 2 ? valid[kKeys / 32 - 2] : valid[kKeys / 32 - 1];
 #pragma unroll
               for (int y = 0; y < 32; ++y)
                 if (!((see >> y) & 1u)) s[32 * i + y] = 0xff800000u;
@@ -1053,13 +1077,12 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             p[y] = pack_bf16(e0, e1);
           }
           // over logits of the same 64 keys that are used up
-          if constexpr (kChunk == 64) tmem_st32(s_at + 64 * b, p);
-          else tmem_st16(s_at + 16 * b, p);
-          if (kChunk == 64 || b == kKeys / kChunk - 1) {
+          tmem_st16(s_at + (b >> 1) * 64 + (b & 1) * 16, p);
+          if (b & 1) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * sb + (kHalves == 2 ? half : b)]);
+            if (lane == 0) mbar_arrive(&p_full[2 * sb + (kHalves == 2 ? half : b >> 1)]);
           }
         }
         if (!(flags & kLast)) continue;

@@ -157,6 +157,7 @@ class Model:
                 yield from self.settle(self.edge[e % NOTES], e // NOTES)
 
     def q_loader(self):
+        loaded = 0
         for u in range(len(self.units)):
             if (yield from self.gives_up("q", u)):
                 break
@@ -170,10 +171,16 @@ class Model:
                 if g >= self.q_bufs and not (yield from self.wait(self.q_free[b], g // self.q_bufs - 1)):
                     break
                 self.q[b] = None
-                yield
-                self.q[b] = g
-                self.q_full[b].arrive()
+                self.q_full[b].arrive(1)
+                loaded = g + 1
+
+                def landed(g=g, b=b):
+                    self.q[b] = g
+                    self.q_full[b].landed()
+                self.copies.append(landed)
             yield
+        for g in range(max(0, loaded - self.q_bufs), loaded):
+            yield from self.settle(self.q_full[g % self.q_bufs], g // self.q_bufs)
         yield from self.meet_all()
 
     def checker(self):

@@ -908,7 +908,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     // With two tiles, two warps share 32 rows: each takes half of a unit's keys, and half of O's channels.
     const int t = kHalves == 2 ? warp >> 3 : 0, half = kHalves == 2 ? (warp >> 2) & 1 : 0, quarter = warp & 3;
     constexpr int kKeys = kTile / kHalves, kChannels = DP / kHalves;
-    constexpr int kChunk = 32;  // keys in registers at a time
+    constexpr int kLook = kRows == 1 ? 64 : 32, kChunk = 32;  // keys in registers at a time
     if (quarter < a.warps) {
       // -------------------------------------------------------------- softmax
       const uint32_t lanes = (uint32_t)quarter << 21;     // this warp's 32 lanes, in bits 16..
@@ -983,29 +983,29 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         const bool hide = step < kTile || all_valid != kFull;
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int b = 0; b < kKeys / kChunk; ++b) {
-          uint32_t s[kChunk];
+        for (int b = 0; b < kKeys / kLook; ++b) {
+          uint32_t s[kLook];
 #pragma unroll
-          for (int i = 0; i < kChunk / 32; ++i) tmem_ld32(s_at + kChunk * b + 32 * i, s + 32 * i);
+          for (int i = 0; i < kLook / 32; ++i) tmem_ld32(s_at + kLook * b + 32 * i, s + 32 * i);
           tmem_wait_ld();
           if (hide) {
 #pragma unroll
-            for (int i = 0; i < kChunk / 32; ++i) {
+            for (int i = 0; i < kLook / 32; ++i) {
               // what this row sees of these keys: the context before `step`, its mask from there on
-              const int from = step - kKeys * half - kChunk * b - 32 * i;
+              const int from = step - kKeys * half - kLook * b - 32 * i;
               uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
               if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
               else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
-              see &= b == 0 ? valid[0] : b == 1 ? valid[1] : b == 2 ? valid[kKeys / 32 - 2] : valid[kKeys / 32 - 1];
+              see &= b == 0 ? valid[i] : valid[kLook / 32 + i];
 #pragma unroll
               for (int y = 0; y < 32; ++y)
                 if (!((see >> y) & 1u)) s[32 * i + y] = 0xff800000u;
-              tmem_st32(s_at + kChunk * b + 32 * i, s + 32 * i);
+              tmem_st32(s_at + kLook * b + 32 * i, s + 32 * i);
             }
             tmem_wait_st();
           }
 #pragma unroll
-          for (int z = 0; z < kChunk; z += 4)
+          for (int z = 0; z < kLook; z += 4)
 #pragma unroll
             for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(s[z + y]));
         }

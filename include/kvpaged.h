@@ -101,11 +101,12 @@ enum kv_error_bits {
 
 /*
  * Bounded waits.  Only the two bulk-copy calls (kv_cache_gather_bulk,
- * kv_copy_blocks_bulk) wait on the copy engine, and kv_attention_prompt on it
- * and on the matrix unit; every such wait gives up
+ * kv_copy_blocks_bulk) wait on the copy engine, and kv_attention_prompt and
+ * kv_attention_tree on it and on the matrix unit; every such wait gives up
  * after 1 s of GPU time (the global nanosecond timer) or 2^22 tries,
- * whichever comes first (kv_attention_prompt's counts from the fifth try); a CTA that gave up waits once more, with the same
- * bound, for each of its own loads still in flight, then ends.  A healthy
+ * whichever comes first (kv_attention_prompt's counts from the fifth try; kv_attention_tree's
+ * from the eighth, by the timer alone); a CTA that gave up waits once more, with the
+ * bound of the bulk calls, for each of its own loads still in flight, then ends.  A healthy
  * copy completes in microseconds, so a timeout means the GPU is in trouble.
  * After a call has set KV_ERR_TIMEOUT:
  *   - its outputs are undefined: rows may be missing, partly written, or

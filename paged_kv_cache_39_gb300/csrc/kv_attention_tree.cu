@@ -20,19 +20,40 @@
 // whose range ends inside a (request, head) leaves its sums in the workspace, and a second
 // kernel joins those.
 //
-// Roles by warp:
-//   softmax   one row per thread; also the rescale and the output of its tile
-//   issuer    the matrix instructions: S = Q K^T, then O += P V with P in tensor memory
-//   4 copiers look up blocks and copy K and V rows (cp.async: any block size, and rows that are
-//             no position of the request are filled with zeros) into a ring of 128-row tiles
-//             in the 128-byte swizzle; they also find the next unit and describe it
+// Roles by warp (kTma):
+//   softmax    one row per thread (two tiles: per two threads, each half of the keys); also the
+//              rescale and the output
+//   issuer     the matrix instructions: S = Q K^T, then O += P V with P in tensor memory, over the
+//              logits it is made of
+//   checker    V of the units that hold the step's rows or a span's end, before the issuer reads it
+//   describer  the requests' units in order: which keys are there, each box's place in the pool
+//   2 copiers  K and V by TMA boxes of 8 tokens and more into a ring of 128-key tiles in the 128-byte swizzle
+//   Q loader
+// Blocks that are no multiple of 8 tokens have four copiers in place of the last four, which describe the
+// units, look up rows and copy them with cp.async (rows that are no position of the request are
+// zeros), and check V themselves.
 // Tensor memory: S twice and O twice.  One tile: units take turns with S, so the next scores are
 // computed during this softmax, and segments with O.  Two tiles: one S and O each.
 //
 // Hidden keys.  A hidden logit is replaced, so a NaN there is gone, but 0 * NaN in P V is NaN.
-// Hidden from all rows: filled with zeros, never read.  Hidden from some rows are only the step's
+// Hidden from all rows: made zeros.  Hidden from some rows are only the step's
 // own rows: their values are checked when they arrive; what is not finite is set to 0 in
 // shared memory and its row noted, and the output of a row that sees it looks the value up again.
+//
+// Measured, with what the rules choose against (32 query and 8 KV heads of 128 channels, block 16):
+//   256 contexts of 512 to 4096 tokens, a row each: 357 us, 6.7 TB/s; 8 of 131072, 16 rows each: 633 us,
+//   6.8 TB/s (as fast as the card copies); 64 of 512 to 4096, 2 to 25 rows: 123 us, 5.2 TB/s;
+//   64 of 4000: 166 us with a row each, 181 with 16, 190 with 32, 233 with 64 (1160 TFLOP/s);
+//   16 of 1000 to 8192, 57 to 64 rows, 40 and 5 heads of 64 channels: 85 us (500 TFLOP/s).
+//   TMA or cp.async (the same blocks of 16): 357 and 405 us, 633 and 703, 123 and 132, 233 and 333, 85 and 101.
+//   Two tiles at a time for more than 128 rows, or one: 233 and 305 us (64 rows), 85 and 110 (the last case).
+//   Gangs of up to 8 CTAs, or none: 357 and 376 us, 123 and 135, 64 contexts of 8000 and 64 channels 229 and 285.
+//   Two buffers for Q where five tiles (ten of 64 channels) still fit, or one: 195 and 204 us with cp.async
+//   (64 x 16 rows), the same with TMA.
+//   Q by TMA, or by cp.async from one warp: 254 and 263 us for 64 rows.
+// One tile is bound by memory.  Two are bound by the chain from scores to weights to products and back:
+// 4180 cycles a unit, of which the matrix unit works 2048 and the exponential unit 2048; and by the
+// instruction cache: the same waits in longer code cost 5 to 10 %.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -45,7 +66,7 @@ namespace {
 
 constexpr int kTile = 128;             // keys of a unit, rows of a tile
 constexpr int kCopiers = 4;            // warps, where they copy; where TMA does:
-constexpr int kReaders = 4;            // that read what the first one describes: K's copies, V's, Q, checks
+constexpr int kReaders = 4;            // that read what the describer writes: K's copies, V's, Q, checks
 constexpr int kNotes = 8;              // units described ahead (a power of two: 2^3)
 constexpr int kBadRing = 16;           // segments whose values are noted
 constexpr float kLazy = 8.0f;          // log2 of the most a weight may pass the reference
@@ -385,7 +406,7 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
           const int buf = (int)(segment & q_odd);
           if (a.q_box > 0) {
             if (leader) {
-              const int tiles = flags & kTwo ? 2 : 1;
+              const int tiles = kRows == 2 && (flags & kTwo) ? 2 : 1;
               mbar_arrive_expect_tx(&q_full[buf], tiles * (DP / 64) * box_bytes);
               for (int t = 0; t < tiles; ++t)
 #pragma unroll
@@ -1273,7 +1294,7 @@ Plan plan_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_
   p.rows = rows > kTile ? 2 : 1;
   p.passes = (rows + p.rows * kTile - 1) / (p.rows * kTile);
   const int segs = num_kv_heads * p.passes;
-  // the largest divisor of the (KV head, pass) pairs up to 8
+  // the largest divisor of the (KV head, pass) pairs up to 8 (measured above)
   p.gang = segs < 8 ? segs : 8;
   while (segs % p.gang != 0) --p.gang;
   p.gangs = sm_count() / p.gang;

@@ -330,7 +330,13 @@ __global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads) verify_ker
           s_gone[count++] = token;
         }
       }
-      if (pass == 0) pass = known ? 3 : 2;
+      if (pass == 0) {
+        if (known && whole == 0 && count > 0) {  // nothing is left: p again
+          count = 0;
+          known = false;
+        }
+        pass = known ? 3 : 2;
+      }
       s_at = at;
       s_count = count;
       s_pass = pass;
@@ -381,10 +387,6 @@ __global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads) verify_ker
         s_z[n] = make_float2((float)z, (float)(z - (double)(float)z));
       }
       known = true;
-      if (whole == 0 && row >= m && n > 0) {  // nothing is left: p again
-        count = 0;
-        known = false;
-      }
     }
     turn ^= 1;
   }

@@ -251,3 +251,16 @@ def test_distribution_is_the_targets():
         n = 10 * R
         e = p[0].double()
         assert ((counts.double() - n * e).abs() <= 5 * (n * e * (1 - e)).sqrt()).all()
+
+
+@pytest.mark.parametrize("V", [7, 600])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_nothing_left_before_rows_that_hang_elsewhere(dtype, V):
+    """p <= q everywhere, the refused row has rows below it and none beside it: p again."""
+    def larger(target, draft, tokens, parents, uniform):
+        parents[:] = [-1, 0, 1, 2, -1, 0, 1, 1]
+        draft[0], draft[4] = target[0] * 2, target[4] * 4     # exact in either type
+        uniform[1] = uniform[5] = 0.875
+        uniform[0], uniform[4] = 0.6, 0.3
+    got = run([4, 4], V, dtype, True, seed=11, spread=0.5, change=larger)
+    assert got[2].tolist() == [0, 0] and got[0][0].item() >= 0 and got[0][4].item() >= 0

@@ -971,9 +971,9 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         // the issuer has read the note that this unit's scores came behind
         const Note& n = notes[u & (kNotes - 1)];
         const int flags = n.flags, step = n.step;
-        uint32_t valid[kKeys / 32], all_valid = kFull;
+        uint32_t all_valid = kFull;
 #pragma unroll
-        for (int b = 0; b < kKeys / 32; ++b) all_valid &= valid[b] = n.valid[half * (kKeys / 32) + b];
+        for (int b = 0; b < kKeys / 32; ++b) all_valid &= n.valid[half * (kKeys / 32) + b];
         if (flags & kFirst) {
           ++segment;
           g_note = seg_notes[segment & (kNotes - 1)];
@@ -1001,7 +1001,26 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                               half * kChannels;
         // kChunk keys at a time, in loops: the code of a whole tile, unrolled, has the four schedulers wait for
         // instructions (twice the time with four warps as with one)
-        const bool hide = step < kTile || all_valid != kFull;
+        // Hidden logits first, in a loop of their own: few units have any.
+        if (step < kTile || all_valid != kFull) {
+#pragma unroll 1
+          for (int b = 0; b < kKeys / 32; ++b) {
+            // what this row sees of these keys: the context before `step`, its mask from there on
+            const int from = step - kKeys * half - 32 * b;
+            uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
+            if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
+            else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
+            see &= n.valid[half * (kKeys / 32) + b];
+            uint32_t s[32];
+            tmem_ld32(s_at + 32 * b, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!((see >> y) & 1u)) s[y] = 0xff800000u;
+            tmem_st32(s_at + 32 * b, s);
+            tmem_wait_st();
+          }
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
         for (int b = 0; b < kKeys / kLook; ++b) {
@@ -1009,22 +1028,6 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 #pragma unroll
           for (int i = 0; i < kLook / 32; ++i) tmem_ld32(s_at + kLook * b + 32 * i, s + 32 * i);
           tmem_wait_ld();
-          if (hide) {
-#pragma unroll
-            for (int i = 0; i < kLook / 32; ++i) {
-              // what this row sees of these keys: the context before `step`, its mask from there on
-              const int from = step - kKeys * half - kLook * b - 32 * i;
-              uint32_t see = from >= 32 ? kFull : from > 0 ? (1u << from) - 1u : 0u;
-              if (from > 0) see |= from < 32 ? (uint32_t)(mask << from) : 0u;
-              else see |= from > -64 ? (uint32_t)(mask >> -from) : 0u;
-              see &= b == 0 ? valid[i] : valid[kLook / 32 + i];
-#pragma unroll
-              for (int y = 0; y < 32; ++y)
-                if (!((see >> y) & 1u)) s[32 * i + y] = 0xff800000u;
-              tmem_st32(s_at + kLook * b + 32 * i, s + 32 * i);
-            }
-            tmem_wait_st();
-          }
 #pragma unroll
           for (int z = 0; z < kLook; z += 4)
 #pragma unroll

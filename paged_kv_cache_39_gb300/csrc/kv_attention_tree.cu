@@ -73,6 +73,8 @@ constexpr float kLazy = 8.0f;          // log2 of the most a weight may pass the
 constexpr float kRefStart = -1e30f;    // of a row with no finite logit yet
 constexpr int kSmemMax = 232448;       // of a CTA
 constexpr int kJoinThreads = 128;
+constexpr int kJoins = 8;              // CTAs of the join to one of the attention
+constexpr int kMaxCtas = 2 * kJoinThreads;  // two to a thread of the join
 
 struct TreeArgs {
   const __nv_bfloat16* q;
@@ -1229,38 +1231,66 @@ attention_tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 
 // Join: out = sum_i f_i o_i / sum_i f_i l_i, f_i = 2^(ref_i - max ref), over the parts of the
 // segment that CTA x began and did not end: its own second part, then the first parts of the
-// same member of the gangs behind it.  A warp per row, 4 channels a lane.
+// same member of the gangs behind it.  A thread has 4 channels, DP / 4 of them a row.  Every CTA looks
+// through the list of such segments, so that their rows are shared out whoever began them: a row to a
+// group, or, where there are fewer rows than CTAs, to all groups of a CTA, which take parts in turn.
+// (With the rows of a segment left to blocks of the CTA that began it: one request of 8 rows behind
+// 1001 tokens 18.6 us with the attention, 14.5 so; two of up to 109306 tokens, one KV head, 118 rows of 150
+// parts, 57.6 and 28.1; 256 decode contexts 353 and 351; calls without a segment to join 0.5 more.  4 CTAs
+// to one of the attention, 8 or 12: 64 trees 125, 122 and 120 us, calls without a join 0.4 apart.)
 template <int DP, int kRows>
 __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kWarps = kJoinThreads / 32, kLanes = DP / 4, kGroups = kJoinThreads / kLanes, kBatch = 4;
+  __shared__ int4 s_join[kMaxCtas];
+  __shared__ int s_end[kMaxCtas];            // rows to join of the segments that CTAs 0 .. x began
+  __shared__ int s_sum[2 * kWarps];
+  __shared__ float4 s_o[kGroups][kLanes];
+  __shared__ float2 s_stat[kGroups];
   pdl_allow_next();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int x = blockIdx.x;
-  const int4 j = a.joins[x];
-  if (j.x < 0) return;
-  const int head = j.y / a.passes, pass = j.y - head * a.passes;
-  const int row0 = pass * kRows * kTile, rows = min(j.w * a.group - row0, kRows * kTile);
-  const int g0 = x / a.gang, member = x - g0 * a.gang;
-  const float2* stats = reinterpret_cast<const float2*>(a.parts + (int64_t)a.gangs * a.gang * 2 * a.part_rows * DP);
-  const int first = a.q_start[j.x];
-  for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rows;
-       row += gridDim.y * (kJoinThreads / 32)) {
+  const int tid = threadIdx.x, warp = tid >> 5, ctas = a.gangs * a.gang;
+  int end[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int x = h * kJoinThreads + tid;
+    const int4 j = x < ctas ? a.joins[x] : make_int4(-1, 0, 0, 0);
+    s_join[x] = j;
+    end[h] = j.x < 0 ? 0 : max(0, min(j.w * a.group - j.y % a.passes * kRows * kTile, kRows * kTile));
+  }
+  if (!__syncthreads_or(end[0] | end[1])) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    end[h] = warp_inclusive_scan<int>(end[h]);
+    if ((tid & 31) == 31) s_sum[h * kWarps + warp] = end[h];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int w = 0; w < 2 * kWarps; ++w)
+      if (w < h * kWarps + warp) end[h] += s_sum[w];
+    s_end[h * kJoinThreads + tid] = end[h];
+  }
+  __syncthreads();
+  const int total = s_end[kMaxCtas - 1], group = tid / kLanes, lane = tid % kLanes;
+  const bool together = total <= (int)gridDim.x;
+  const int step = together ? kGroups : 1, sub = together ? group : 0;   // parts of this group
+  const float2* stats = reinterpret_cast<const float2*>(a.parts + (int64_t)ctas * 2 * a.part_rows * DP);
+  for (int item = together ? blockIdx.x : blockIdx.x * kGroups + group; item < total;
+       item += gridDim.x * (kGroups / step)) {
+    int x = 0;                               // the first one with item < s_end[x]
+    for (int hi = kMaxCtas - 1; x < hi;) {
+      const int mid = (x + hi) >> 1;
+      if (s_end[mid] > item) hi = mid; else x = mid + 1;
+    }
+    const int row = item - (x > 0 ? s_end[x - 1] : 0);
+    const int4 j = s_join[x];
+    const int first = a.q_start[j.x];
+    const int head = j.y / a.passes, pass = j.y - head * a.passes, row0 = pass * kRows * kTile;
+    const int g0 = x / a.gang, member = x - g0 * a.gang;
     float top = kRefStart, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 4;
-    for (int i = g0; i <= j.z; i += kBatch) {
-      float2 st[kBatch];
-      float4 v[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int64_t part = ((int64_t)((i + b) * a.gang + member) * 2 + (i + b == g0 ? 1 : 0)) * a.part_rows + row;
-        st[b] = make_float2(kRefStart, 0.f);
-        v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i + b <= j.z) {
-          st[b] = stats[part];
-          if (4 * lane < DP) v[b] = *reinterpret_cast<const float4*>(a.parts + part * DP + 4 * lane);
-        }
-      }
+    auto add = [&](const float2 (&st)[kBatch], const float4 (&v)[kBatch]) {
       float up = top;
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) up = fmaxf(up, st[b].x);
@@ -1273,6 +1303,37 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const __grid_co
         const float h = ex2(st[b].x - up);
         l = fmaf(st[b].y, h, l);
         o = make_float4(fmaf(v[b].x, h, o.x), fmaf(v[b].y, h, o.y), fmaf(v[b].z, h, o.z), fmaf(v[b].w, h, o.w));
+      }
+    };
+    float2 st[kBatch];
+    float4 v[kBatch];
+    for (int i = g0 + sub; i <= j.z; i += kBatch * step) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int k = i + b * step;
+        const int64_t part = ((int64_t)(k * a.gang + member) * 2 + (k == g0 ? 1 : 0)) * a.part_rows + row;
+        st[b] = make_float2(kRefStart, 0.f);
+        v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k <= j.z) {
+          st[b] = stats[part];
+          v[b] = *reinterpret_cast<const float4*>(a.parts + part * DP + 4 * lane);
+        }
+      }
+      add(st, v);
+    }
+    if (together) {                          // one item a CTA
+      s_o[group][lane] = o;
+      if (lane == 0) s_stat[group] = make_float2(top, l);
+      __syncthreads();
+      if (group > 0) return;
+      top = kRefStart;
+      l = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int g = 0; g < kGroups; g += kBatch) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) st[b] = s_stat[g + b], v[b] = s_o[g + b][lane];
+        add(st, v);
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1300,7 +1361,8 @@ Plan plan_of(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_
   // the largest divisor of the (KV head, pass) pairs up to 8 (measured above)
   p.gang = segs < 8 ? segs : 8;
   while (segs % p.gang != 0) --p.gang;
-  p.gangs = sm_count() / p.gang;
+  const int ctas = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+  p.gangs = ctas / p.gang;
   if (p.gangs < 1) p.gang = p.gangs = 1;
   p.part_rows = rows < p.rows * kTile ? rows : p.rows * kTile;
   const int tile_rows = rows < kTile ? rows : kTile;
@@ -1328,8 +1390,7 @@ int launch(const TreeArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map
   const unsigned ctas = (unsigned)(a.gangs * a.gang);
   const int rc = launch_pdl(kernel, ctas, kThreadsOf<kRows>, smem, stream, a, q_map, k_map, v_map);
   if (rc != KV_OK) return rc;
-  const unsigned chunks = (unsigned)(a.part_rows + 15) / 16;
-  return launch_pdl(join_tree_kernel<DP, kRows>, dim3(ctas, chunks), kJoinThreads, 0, stream, a);
+  return launch_pdl(join_tree_kernel<DP, kRows>, kJoins * ctas, kJoinThreads, 0, stream, a);
 }
 
 template <int DP, int kRows>

@@ -25,7 +25,7 @@
 //              rescale and the output
 //   issuer     the matrix instructions: S = Q K^T, then O += P V with P in tensor memory, over the
 //              logits it is made of
-//   checker    V of the units that hold the step's rows or a span's end, before the issuer reads it
+//   values     checks V of the units that hold the step's rows or a span's end, before the issuer reads it
 //   describer  the requests' units in order: which keys are there, each box's place in the pool
 //   2 copiers  K and V by TMA boxes of 8 tokens and more into a ring of 128-key tiles in the 128-byte swizzle
 //   Q loader

@@ -183,10 +183,10 @@ class Model:
             yield from self.settle(self.q_full[g % self.q_bufs], g // self.q_bufs)
         yield from self.meet_all()
 
-    def checker(self):
+    def value_check(self):
         edges = 0
         for u in range(len(self.units)):
-            if (yield from self.gives_up("checker", u)):
+            if (yield from self.gives_up("values", u)):
                 break
             x = yield from self.read(u)
             if x is None:
@@ -459,7 +459,7 @@ class Model:
     def run(self):
         rng = self.rng
         self.rises = [rng.random() < 0.3 for _ in self.units]
-        roles = [self.describer(), self.copier(False), self.copier(True), self.q_loader(), self.checker(), self.issuer()]
+        roles = [self.describer(), self.copier(False), self.copier(True), self.q_loader(), self.value_check(), self.issuer()]
         roles += [self.softmax(t, h, q) for t in range(self.tiles) for h in range(2) for q in range(self.quarters)]
         self.roles = len(roles)
         weight = [rng.choice([0.05, 0.3, 1, 1, 3]) for _ in roles] + [rng.choice([0.05, 0.3, 1, 3]) for _ in range(2)]
@@ -513,7 +513,7 @@ def test_every_schedule_ends_and_reads_what_is_there(tiles, slots, q_bufs, seed)
 def test_ends_where_a_role_gives_up(tiles, slots, q_bufs, seed):
     rng = random.Random(7000 * seed + 10 * slots + tiles)
     segments = segments_of(rng, tiles)
-    roles = ["describer", "k", "v", "q", "checker", "issuer"] + \
+    roles = ["describer", "k", "v", "q", "values", "issuer"] + \
         [("softmax", t, h, 0) for t in range(tiles) for h in range(2)]
     m = Model(rng, segments, tiles, slots, q_bufs, 1, stall=(rng.choice(roles), rng.randrange(sum(n for n, *_ in segments))))
     m.run()

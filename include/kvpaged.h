@@ -767,9 +767,9 @@ int64_t kv_attention_tree_workspace(int32_t num_reqs, int32_t max_rows, int32_t 
  * Without draft_probs q is 1 at x and 0 elsewhere, and Z_(j+1) = Z_j - s_j(x).  A kept child is the next
  * row.  With no child left, the last token is the smallest t with sum_(k <= t) s(k) > u_0 sum_k
  * s(k); where s is 0 everywhere, s = p.  So the tokens are distributed as the target's.
- * Sums are held in integers of 2^-46 and 64 bits, whose order does not matter; a weight is
- * rounded to a multiple of 2^-46.  The same call gives the same bits every time.  (Rows that sum to
- * 2^17 and more are no probabilities: the last token is then any, or -1.)
+ * Sums are held in integers of 2^-45 and 64 bits, whose order does not matter; a weight is
+ * a multiple of 2^-45, off by less than that.  The same call gives the same bits every time.  (Rows that
+ * sum to 2^18 and more are no probabilities: the last token is then any, or -1.)
  * Probabilities below 0 and NaN count as 0, above 1 as 1; numbers below 0 and NaN count as 0, of 1 and
  * above as the largest below 1.  A token outside [0, vocab) is passed over with
  * KV_ERR_BAD_TOKEN; so is a row whose parent is not a row before it (KV_ERR_BAD_TREE) and

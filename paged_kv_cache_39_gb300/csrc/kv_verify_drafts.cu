@@ -11,9 +11,12 @@
 //
 // A sum of 10^5 fp32 terms in 32 bits would move the borders between tokens by 1e-7 of the whole,
 // and which token a number falls on would hang on the order of the sum.  So weights are
-// integers, multiples of 2^-46: with s = h + l (h fp32, l what h's roundings left),
+// integers, multiples of 2^-45: with s = h + l (h fp32, l what h's roundings left),
 //   t = 1 + h in fp32 is h to a multiple of 2^-23, its bits are that integer;
-//   (h - (t - 1)) + l is exact and below 2^-23; added to 1.5 * 2^-23 its bits are multiples of 2^-46.
+//   h - (t - 1) is exact and 2^-24 at most, l is at most 2^-25 (half a step of an h below 1): their sum
+//   stays within 0.75 * 2^-23, so with 1.5 * 2^-22 added it lies in [2^-22, 2^-21), where bits count 2^-45.
+// (1.5 * 2^-23 would leave +-2^-24 only.)  The last two sums' roundings are 2^-48 and 2^-46: less than one
+// unit together.
 // Four additions and two integer ones an element, no conversions, and 64-bit sums whose order
 // does not matter.  p - q is exact as h + l (both are known to 24 bits and p > q); s_j - Z_j q
 // carries Z_j and s_j in two fp32 each, 2^-46 of the whole.
@@ -38,8 +41,9 @@ namespace {
 
 constexpr int kClusterMax = 8;
 constexpr int kThreadsPerSm = 1024;  // at 64 registers
-constexpr float kLowBias = 0x1.8p-23f;
-constexpr double kUnit = 0x1p-46;
+constexpr float kLowBias = 0x1.8p-22f;
+constexpr int kLowBits = 22;               // of a weight, in units: t's are 2^-23
+constexpr double kUnit = 0x1p-45;
 
 struct VerifyArgs {
   const void* target;
@@ -119,7 +123,7 @@ __device__ __forceinline__ void add_weights(uint64_t h, uint64_t l, uint32_t& hi
 __device__ __forceinline__ uint64_t weight_sum(uint32_t hi, uint32_t lo, uint32_t count) {
   hi -= count * 0x3f800000u;
   lo -= count * __float_as_uint(kLowBias);
-  return ((uint64_t)hi << 23) + (uint64_t)(int64_t)(int32_t)lo;
+  return ((uint64_t)hi << kLowBits) + (uint64_t)(int64_t)(int32_t)lo;
 }
 template <Kind kind>
 __device__ __forceinline__ uint64_t weight_of(float p, float q, const float2* z, int count) {

@@ -43,7 +43,9 @@
  *   waits for that kernel to complete before its first memory access, so the
  *   results are those of plain stream order (also inside CUDA graphs).
  *   A pointer may be NULL only where the call reads nothing through it (for
- *   example `positions` when num_tokens == 0).
+ *   example `positions` when num_tokens == 0).  What a call reads stays as it
+ *   is until the call has ended: it may be read more than once, by blocks that
+ *   rely on one another's findings.
  * Layouts.  All arrays are dense, row-major, without padding between rows
  *   other than the stated strides.  Block tables are int32
  *   [rows, table_stride]: row r is request r, column j the physical block of

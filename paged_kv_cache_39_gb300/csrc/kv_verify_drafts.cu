@@ -308,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads) verify_ker
   bool known = false;                        // the sums of (at, count) are there
   uint64_t whole = 0;
   int turn = 0;
+  // at most a pass for each row but the first, and two for the last token, whatever is read (counting them takes
+  // a register too many: 256 chains 54 us instead of 43)
   while (true) {
     if (tid == 0) {
       int pass = 0;
@@ -483,7 +485,9 @@ __global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads) verify_ker
     const int src = __ffs(found) - 1;
     uint64_t up = __shfl_sync(kFull, incl - mine, src);
     const int from = __shfl_sync(kFull, i0, src), to = __shfl_sync(kFull, i1, src);
-    for (int i = from + lane;; i += 32) {
+    // as far as the piece goes: it holds the token, unless its elements have changed since the first look
+    for (int at_i = from; at_i < to; at_i += 32) {
+      const int i = at_i + lane;
       const uint64_t w = warp_inclusive_scan<uint64_t>(i < to ? weight(i) : 0);
       const uint32_t past = __ballot_sync(kFull, up + w > want);
       if (past != 0) {

@@ -96,3 +96,14 @@ def test_numbers_beside_a_border(refusals, V, dtype, count):
     assert not kept.any() and err.item() == 0
     wrong = [i for i, (a, b) in enumerate(zip(got[::refusals + 1].tolist(), want)) if a != b]
     assert not wrong, f"{len(wrong)} of {count} beside the border, first {wrong[:5]}"
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("rows", [1, 200])
+def test_rows_that_are_no_probabilities_end(dtype, rows):
+    """2^20 tokens of 1 each: their sum passes 64 bits, the last token is any or none."""
+    V = 2 ** 20
+    p = torch.ones((rows, V), dtype=dtype, device=dev())
+    u = torch.linspace(0, 0.99, rows, device=dev())
+    got, _, kept = kv.kv_verify_drafts(p, i32([0] * rows), i32(np.arange(rows + 1)), u)
+    assert not kept.any() and ((got >= -1) & (got < V)).all()

@@ -686,8 +686,8 @@ int64_t kv_attention_q4_workspace(int32_t num_reqs, int32_t num_q_heads, int32_t
  *   cache_positions  int64 [num_rows]: context_len + i.
  *
  * A row whose parent is not a row before it sets KV_ERR_BAD_TREE and stands like row 0: it
- * sees itself, at depth 0.  A negative context_len sets KV_ERR_BAD_POSITION; both positions
- * of its rows are -1.
+ * sees itself, at depth 0.  A negative context_len sets KV_ERR_BAD_POSITION where its request
+ * has rows; both positions of those are -1.
  * Errors: KV_EINVAL for negative counts, null or misaligned pointers (tree_mask and
  * positions 8 bytes, others 4), an output that shares bytes with an input or another output.
  */

@@ -31,7 +31,7 @@ tree_layout_kernel(const int32_t* __restrict__ parents, const int32_t* __restric
   const int64_t ctx = context_len[r];
   uint32_t err = 0;
   if (rows.count < 0) err |= KV_ERR_BAD_QSL;
-  else if (ctx < 0) err |= KV_ERR_BAD_POSITION;
+  else if (rows.count > 0 && ctx < 0) err |= KV_ERR_BAD_POSITION;
   uint64_t mask[2];
   int up[2];
 #pragma unroll

@@ -723,7 +723,8 @@ int kv_tree_layout(const int32_t* parents, const int32_t* q_start_loc, const int
  * (KV_ERR_BAD_POSITION).  Positions a row does not see contribute nothing to it, whatever they hold.
  * A NaN or an infinity in a value row makes that channel NaN or infinite for the rows that
  * see it.  Products and sums are held in 32 bits; the weights are rounded to bf16 for
- * their product with V.  The same call gives the same bits every time.
+ * their product with V.  Logits (scale * q_i . k_p) of 2^30 and more may give NaN or zeros.  The same
+ * call gives the same bits every time.
  * Errors: KV_EINVAL for null or misaligned pointers, sizes out of range, a stride below the
  * row, num_q_heads not a multiple of num_kv_heads, a scale that is not positive and finite, a
  * workspace that is missing, misaligned or too small, out or workspace sharing bytes with

@@ -710,7 +710,10 @@ int kv_tree_layout(const int32_t* parents, const int32_t* q_start_loc, const int
  *   tree_mask      int64 [num_rows]: row i sees row j of its request (position
  *                  context_len + j) where bit j is set, itself included; bits at and past
  *                  the request's rows mean nothing.  NULL: row i sees the rows j <= i.
- *   max_rows       1 .. KV_MAX_TREE_ROWS: no request has more rows (KV_ERR_BAD_QSL).
+ *   max_rows       1 .. KV_MAX_TREE_ROWS: no request has more rows (KV_ERR_BAD_QSL).  Every request's
+ *                  keys are read once for each 256 of max_rows * (num_q_heads / num_kv_heads), or
+ *                  part of them, whatever rows it has: give no more than the batch has, and a few
+ *                  requests of many rows a call of their own.
  *   out            bf16 [num_rows, num_q_heads, head_dim], dense, apart from the inputs.
  *   workspace      as kv_attention_q4, of kv_attention_tree_workspace() bytes.
  *

@@ -51,6 +51,9 @@
 //   Two buffers for Q where five tiles (ten of 64 channels) still fit, or one: 195 and 204 us with cp.async
 //   (64 x 16 rows), the same with TMA.
 //   Q by TMA, or by cp.async from one warp: 254 and 263 us for 64 rows.
+// A call has as many passes over the keys as max_rows asks for, 256 rows each, and a request goes through all of
+// them: 240 requests with one row and 16 with 64, 512 to 4096 tokens, 32 query heads: 442, 439 and 438 us with 8, 4
+// and 2 KV heads (one, two and four passes), 330 + 78, 178 + 76 and 99 + 75 in two calls.
 // One tile is bound by memory.  Two are bound by the chain from scores to weights to products and back:
 // 4180 cycles a unit, of which the matrix unit works 2048 and the exponential unit 2048; and by the
 // instruction cache: the same waits in longer code cost 5 to 10 %.

@@ -27,10 +27,12 @@
 // the L2.
 //
 // Measured: 256 chains of 2 to 6 rows, 131072 fp32 probabilities (224 MB) 43 us, 5.2 TB/s: a CTA's passes
-// follow one another, and a second wave of CTAs begins as the first ends.  64 trees of 5 to 25 rows,
-// 100003 in bf16 (21 MB) 36 to 41 us: up to a dozen refusals one after another, each a pass
-// over the rows out of the L2 and a meeting of the cluster.  One chain of 6 rows, 32000: 7.7 us.  Two
-// vectors in flight a thread: 43 us, four 54 (the 256 chains).
+// follow one another with 32 KB in flight, and of the 304 CTAs that can run at once there are 256, so 48 of 152
+// SMs have one where the others have two.  64 trees of 5 to 25 rows, 100003 in bf16 (21 MB) 36 to 41 us: up to a dozen
+// refusals one after another, each a pass over the rows out of the L2 and a meeting of the cluster.  One chain of
+// 6 rows, 32000: 7.7 to 8.5 us.  Two vectors in flight a thread: 43 us, four 54 (the 256 chains).  Without draft
+// probabilities, where a refusal needs no pass: 32, 14.6 and 7.8 us.  An element goes through every refusal before it
+// again, so 63 of them at one row (100003 in bf16) take 2.3 ms, and 53 us without draft probabilities.
 #include <cuda_bf16.h>
 
 #include "kv_tc.cuh"

@@ -785,8 +785,8 @@ def kv_attention_tree(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     the bf16 paged caches.
 
     query [N, q_heads, D] bf16, any row stride; request r owns rows [q_start_loc[r],
-    q_start_loc[r+1]), at most ``max_rows`` <= 64 of them, and attends positions
-    [span_start_r, context_len_r) of its cache (``span_start`` None: all of them) and, at
+    q_start_loc[r+1]), at most ``max_rows`` <= 64 of them (the time goes by this bound, not by the
+    request's own rows), and attends positions [span_start_r, context_len_r) of its cache (``span_start`` None: all of them) and, at
     context_len_r + j, the rows j whose bits are set in the row's ``tree_mask`` (int64 [N];
     None: the row itself and those before it).  The rows' own K and V are in the caches
     already.  ``scale`` defaults to D ** -0.5.  The workspace is allocated here, as in
